@@ -14,6 +14,10 @@ to, and a missing library is an error.
     o, lse = attn_fwd_fp8(q8, k8, vt8, q_scale, k_scale, v_scale, causal=True)  # e4m3 inputs
     dq, dk, dv = attn_bwd(q, k, v, o, lse, dout, causal=True)   # gradients
     o_h, lse_h = ring_attn_fwd_host(q_h, k_h, v_h, P=8, causal=True)  # host tensors in and out
+    q, k = rope_axes(q, k, positions, *RopePlan(128, (16, 24, 24)))   # rotary positions, several axes
+    o, lse = attn_paged(q_new, k_pages, v_pages, page_table, kv_lens, cu_seqlens)  # over a paged cache
+
+(the cache side, PagedCache and its page management included, is in paged.py)
 """
 from __future__ import annotations
 
@@ -28,7 +32,9 @@ from ._lib import AttnBlock, AttnError, lib
 __all__ = ["attn_fwd", "attn_partial", "attn_partial_blocks", "attn_fwd_varlen", "attn_fwd_fp8", "attn_bwd", "lse_merge",
            "ring_attn_fwd", "ring_attn_fwd_static", "ring_attn_fwd_host", "ring_host_workspace_bytes",
            "EmulatedRing",
-           "query_device_error", "AttnError", "lib", "RING_SCRATCH_BYTES"]
+           "query_device_error", "AttnError", "lib", "RING_SCRATCH_BYTES",
+           "attn_paged", "attn_paged_workspace_bytes", "rope_axes", "rope_axes_bwd", "RopePlan", "paged_append",
+           "paged_reserve", "paged_free", "paged_fork", "paged_copy", "paged_compact", "PagedCache"]
 
 RING_SCRATCH_BYTES = 64 << 20  # the library's fixed scratch array for ring_attn_fwd_static
 
@@ -525,3 +531,7 @@ def query_device_error(device: torch.device | None = None) -> None:
     """Synchronise the current stream and raise AttnError if a kernel timed out."""
     device = device or torch.device("cuda", torch.cuda.current_device())
     _check(lib.attn_query_device_error(_stream_handle(device)), "device wait")
+
+
+from .paged import (PagedCache, RopePlan, attn_paged, attn_paged_workspace_bytes, paged_append,  # noqa: E402
+                    paged_compact, paged_copy, paged_fork, paged_free, paged_reserve, rope_axes, rope_axes_bwd)

@@ -22,8 +22,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libseqattn.so")
-SOURCES = ["attn_kernel.cu", "lse_merge.cu", "api.cu"]
-HEADERS = ["ptx.cuh", "kernels.h", "attn_common.cuh", "attn_bwd.cuh"]
+SOURCES = ["attn_kernel.cu", "lse_merge.cu", "rope.cu", "pages.cu", "api.cu", "api_paged.cu"]
+HEADERS = ["ptx.cuh", "kernels.h", "attn_common.cuh", "attn_bwd.cuh", "attn_paged.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -39,7 +39,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps.append(os.path.join(ROOT, "include", "seqattn.h"))
+    deps += [os.path.join(ROOT, "include", h) for h in ("seqattn.h", "seqattn_paged.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

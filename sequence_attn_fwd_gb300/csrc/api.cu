@@ -276,6 +276,11 @@ int check_common(const void *q, const void *k, const void *v, const void *o, con
 
 }  // namespace
 
+namespace seqattn {
+int keep_cuda_error(cudaError_t e) { return cuda_fail(e); }
+void *tensor_map_encoder() { return reinterpret_cast<void *>(encode_fn()); }
+}  // namespace seqattn
+
 extern "C" {
 
 int attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,

@@ -728,6 +728,7 @@ cudaError_t launch_dispatch(int D, bool f32_out, bool long_keys, const CUtensorM
 }  // namespace seqattn
 
 #include "attn_bwd.cuh"
+#include "attn_paged.cuh"
 
 namespace seqattn {
 

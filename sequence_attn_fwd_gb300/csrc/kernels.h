@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace seqattn {
@@ -108,6 +109,103 @@ cudaError_t launch_attention_segments(int D, bool f32_out, const CUtensorMap &tm
 
 cudaError_t launch_lse_merge(const float *o_parts, const float *lse_parts, int P, long long nrows,
                              int D, void *o, bool bf16_out, float *lse, cudaStream_t stream);
+
+// ---------------------------------------------------------------- paged cache
+// The device view of a paged K/V cache (paged_cache of seqattn_paged.h).
+struct PagedView {
+  void *k_pages, *v_pages;
+  long long page_stride;   // elements
+  const int *page_table;
+  long long table_stride;
+  const int *kv_lens;
+  const int *cu_seqlens;   // [B + 1] rows of the packed new tokens
+  int B, n_pages, page_size, max_pages, Hkv;
+};
+
+// Attention of packed new tokens over a paged cache. The rows of a KV head are
+// numbered (token, query head of the group), group fastest; a 128-row tile has
+// `tok` whole tokens (tok * G <= 128), a work item two tiles.
+struct PagedAttnParams {
+  PagedView cache;
+  void *o;                 // bf16, row t of head h at h * o_h + t * o_s
+  long long o_h, o_s;
+  float *lse;              // [Hq, total_q] or null
+  float *part_o;           // workspace: [2 * kPagedMaxCtas][part_rows][D]
+  float *part_lse;         // workspace: [2 * kPagedMaxCtas][part_rows]
+  int part_rows;           // rows of a work item that can hold a token
+  int Hq, G, tok, total_q, causal;
+  int page_log2;           // log2(page_size)
+  float scale_log2;
+};
+constexpr int kPagedMaxCtas = 160;   // CTAs of one launch (at most one per SM)
+constexpr int kPagedMaxSeqs = 4096;  // sequences of one launch (their prefix sums sit in shared memory)
+
+// Maps: q bf16 4-D [Hkv][total_q][G][D], box 64 x G x tok x 1; k, v bf16 4-D
+// [n_pages][Hkv][page_size][D], box 64 x min(page_size, 128) x 1 x 1; 128-byte
+// swizzle. Two kernels: the attention and the merge of split rows.
+cudaError_t launch_attn_paged(int D, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                              const PagedAttnParams &p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- rotary positions, appends
+struct RopeView {
+  const void *in;
+  void *out;
+  long long in_b, in_h, in_s, out_b, out_h, out_s;  // elements
+  int heads;                                        // 0: nothing
+};
+// Turns per position of each pair, as a fraction of 2^64, and its axis (-1: not turned).
+struct RopeTable {
+  uint64_t turns[64];
+  signed char axis[64];
+};
+struct RopeParams {
+  RopeView q, k, v;        // v: appends only
+  PagedView cache;         // appends only
+  const int *positions;    // null: nothing is turned (appends only)
+  long long pos_axis, pos_b;
+  int B, S, inverse;       // appends: B = 1, S = the packed tokens
+};
+cudaError_t launch_rope(const RopeParams &p, const RopeTable &tbl, int D, bool f32, bool interleaved,
+                        cudaStream_t stream);
+cudaError_t launch_append(const RopeParams &p, const RopeTable &tbl, int D, bool interleaved, cudaStream_t stream);
+
+// ---------------------------------------------------------------- page management
+struct PageTables {
+  int *page_table;
+  long long table_stride;
+  int *kv_lens, *page_refs;
+  int B, max_pages, n_pages, page_log2;
+};
+constexpr int kPageListMax = 512;  // rows, pairs or copies of one launch, passed by value
+struct PageList {
+  int n;
+  int a[kPageListMax], b[kPageListMax];
+};
+struct PoolView {
+  unsigned char *base;
+  long long layer_stride, page_stride, page_bytes;
+  int n_layers;
+};
+constexpr int kMaxPools = 32;
+struct PoolList {
+  int n, total_layers;
+  PoolView pool[kMaxPools];
+};
+cudaError_t launch_reserve(const PageTables &t, const int *n_new, int *status, cudaStream_t stream);
+cudaError_t launch_free(const PageTables &t, const PageList &rows, cudaStream_t stream);
+cudaError_t launch_fork(const PageTables &t, const PoolList &pools, const PageList &pairs, int *status,
+                        cudaStream_t stream);
+cudaError_t launch_copy(const PoolList &pools, const PageList &pairs, cudaStream_t stream);
+cudaError_t launch_compact(const PoolList &pools, const int *page_table, int *out_table, long long table_stride,
+                           const int *page_refs, int *out_refs, int *n_live, int *workspace, int B, int max_pages,
+                           int n_pages, cudaStream_t stream);
+
+size_t compact_workspace_ints(int n_pages);
+
+// Shared by the C-ABI files: keeps the error for attn_last_cuda_error() and
+// returns ATTN_ERR_CUDA; the driver's tensor-map encoder (null if not found).
+int keep_cuda_error(cudaError_t e);
+void *tensor_map_encoder();
 
 // One CTA waits on an mbarrier nothing arrives at until timeout_us runs out.
 cudaError_t launch_expire_wait(unsigned timeout_us, cudaStream_t stream);
