@@ -70,12 +70,12 @@ int rows_per_item(int G, int total_q) {
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct Workspace {
-  size_t lse, total;
+  size_t lse, cuts, total;
 };
 Workspace workspace_of(int G, int total_q, int D) {
   const size_t rows = static_cast<size_t>(2 * seqattn::kPagedMaxCtas) * rows_per_item(G, total_q);
-  const size_t o = round256(rows * D * sizeof(float));
-  return {o, o + round256(rows * sizeof(float))};
+  const size_t lse = round256(rows * D * sizeof(float)), cuts = lse + round256(rows * sizeof(float));
+  return {lse, cuts, cuts + round256(seqattn::kPagedMaxCtas * sizeof(int4))};
 }
 
 // A tensor of rows: strides in elements, multiples of 16 bytes (of dimensions
@@ -166,6 +166,10 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
   if (!isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   const int G = Hq / cache->Hkv, D = cache->D;
   if (G > 128 || total_q > kMaxKeys) return ATTN_ERR_UNSUPPORTED;
+  // the key tiles of all items are counted in 32 bits
+  const long long items = (static_cast<long long>(total_q) / (2 * (128 / G)) + cache->B) * cache->Hkv;
+  const long long tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 127) / 128;
+  if (tiles > 0 && items > 0x7fffffffll / tiles) return ATTN_ERR_UNSUPPORTED;
   if (cache->B == 0 || total_q == 0) return ATTN_OK;
   if (!q || !o || !workspace || !aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 16) || !aligned(lse, 4))
     return ATTN_ERR_INVALID_ARG;
@@ -179,8 +183,8 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
   const cuuint64_t uD = static_cast<cuuint64_t>(D);
   const cuuint64_t qh = Hq > 1 ? static_cast<cuuint64_t>(q_head_stride) : uD;
   const cuuint64_t qs = total_q > 1 ? static_cast<cuuint64_t>(q_row_stride) : uD;
-  const int tok = 128 / G;
-  CUtensorMap tq, tk, tv;
+  const int tok = 128 / G, tok32 = 32 / G;
+  CUtensorMap tq, tq32, tk, tv;
   const cuuint64_t q_dims[4] = {uD, static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(total_q),
                                 static_cast<cuuint64_t>(cache->Hkv)};
   const cuuint64_t q_strides[3] = {qh * 2, qs * 2, qh * 2 * G};
@@ -188,7 +192,9 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
                                  static_cast<cuuint64_t>(cache->n_pages)};
   const cuuint64_t kv_strides[3] = {uD * 2, uD * 2 * cache->page_size, static_cast<cuuint64_t>(cache->page_stride) * 2};
   const unsigned box_rows = cache->page_size < 128 ? cache->page_size : 128;
-  if (!make_map_4d(&tq, q, q_dims, q_strides, G, tok) || !make_map_4d(&tk, cache->k_pages, kv_dims, kv_strides, box_rows, 1) ||
+  if (!make_map_4d(&tq, q, q_dims, q_strides, G, tok) ||
+      !make_map_4d(&tq32, q, q_dims, q_strides, G, tok32 > 0 ? tok32 : 1) ||
+      !make_map_4d(&tk, cache->k_pages, kv_dims, kv_strides, box_rows, 1) ||
       !make_map_4d(&tv, cache->v_pages, kv_dims, kv_strides, box_rows, 1))
     return keep_cuda_error(cudaErrorInvalidValue);
 
@@ -200,15 +206,17 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
   p.lse = lse;
   p.part_o = static_cast<float *>(workspace);
   p.part_lse = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + ws.lse);
+  p.cuts = reinterpret_cast<int4 *>(static_cast<unsigned char *>(workspace) + ws.cuts);
   p.part_rows = rows_per_item(G, total_q);
   p.Hq = Hq;
   p.G = G;
   p.tok = tok;
+  p.tok32 = tok32;
   p.total_q = total_q;
   p.causal = causal;
   p.page_log2 = log2_of(cache->page_size);
   p.scale_log2 = scale * 1.4426950408889634f;
-  return done(seqattn::launch_attn_paged(D, tq, tk, tv, p, reinterpret_cast<cudaStream_t>(stream)));
+  return done(seqattn::launch_attn_paged(D, tq, tq32, tk, tv, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int rope_axes(const rope_rows *q, const rope_rows *k, const int *positions, long long pos_axis, long long pos_b,

@@ -23,6 +23,15 @@
 // an MMA issuer per query tile taking turns, a softmax warpgroup per query
 // tile. The producer reads the page table, one lane per page of a key tile
 // (128 / page_size boxes, or one box inside a larger page).
+//
+// Few rows (at most 64 of a KV head: single tokens, drafts). Reading a key tile
+// takes about 2,800 clocks of one SM's share of the DRAM rate (D = 128), so the
+// chain S, softmax, P V of one tile after the other must stay below that. A
+// row of 128 scores per thread does not (about 4,200 clocks measured). So each
+// tile holds its at most 32 rows four times, and warp w of its warpgroup takes
+// the 32 keys 32 w .. of its copy as an attention of their own -- reference,
+// sum and O rows -- with P zero for the other keys; the four copies are merged
+// in the epilogue. The products cost the same, the softmax a quarter.
 #pragma once
 
 namespace seqattn {
@@ -39,8 +48,9 @@ struct Cfg {
   static constexpr int kTileBytes = kRowsPerTile * D * 2;
   static constexpr int kStages = 131072 / kTileBytes;
   static constexpr int kNumBarriers = 2 + 2 * kStages + 7;
-  static constexpr int kSmemBytes = 1024 + 2 * kTileBytes + kStages * kTileBytes + 8 * kNumBarriers + 16 +
-                                    8 * 12 + 8 * (kPagedMaxSeqs + 1);
+  static constexpr int kStageBytes = 8192;  // of each tile: four copies x 16 columns x 32 rows, fp32
+  static constexpr int kSmemBytes = 1024 + 2 * kTileBytes + kStages * kTileBytes + 2 * kStageBytes + 8 * kNumBarriers +
+                                    16 + 4 * 12 + 4 * (kPagedMaxSeqs + 1);
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -104,26 +114,25 @@ __device__ __forceinline__ long long tiles_before(const PagedAttnParams &p, cons
 
 // prefix[0 .. B]: key tiles of all KV heads of the sequences before each, by
 // every thread of the CTA; warp_sums has 12 entries.
-__device__ __forceinline__ void prefix_tiles(const PagedAttnParams &p, long long *prefix, long long *warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__device__ __forceinline__ void prefix_tiles(const PagedAttnParams &p, int *prefix, int *warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int B = p.cache.B, per = (B + blockDim.x - 1) / blockDim.x;
   const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
-  long long sum = 0;
+  int sum = 0;
   for (int b = b0; b < b1; ++b) {
     const Seq s = sequence(p, b);
-    const long long t = s.q_len > 0 ? tiles_before(p, s, row_blocks(p, s)) * p.cache.Hkv : 0;
     prefix[b] = sum;
-    sum += t;
+    if (s.q_len > 0) sum += static_cast<int>(tiles_before(p, s, row_blocks(p, s))) * p.cache.Hkv;
   }
-  long long incl = sum;
+  int incl = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+    const int y = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += y;
   }
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  long long base = incl - sum;
+  int base = incl - sum;
   for (int i = 0; i < warp; ++i) base += warp_sums[i];
   for (int b = b0; b < b1; ++b) prefix[b] += base;
   if (threadIdx.x == blockDim.x - 1) prefix[B] = base + sum;
@@ -131,7 +140,7 @@ __device__ __forceinline__ void prefix_tiles(const PagedAttnParams &p, long long
 }
 
 // The sequence whose range of tiles has `pos`.
-__device__ __forceinline__ int seq_of(const long long *prefix, int B, long long pos) {
+__device__ __forceinline__ int seq_of(const int *prefix, int B, int pos) {
   int lo = 0, hi = B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -142,8 +151,25 @@ __device__ __forceinline__ int seq_of(const long long *prefix, int B, long long 
 }
 
 // Key tiles per CTA of a launch of n_ctas.
-__device__ __forceinline__ long long tiles_per_cta(long long total, int n_ctas) {
-  return (total + n_ctas - 1) / n_ctas;
+__device__ __forceinline__ int tiles_per_cta(int total, int n_ctas) { return total / n_ctas + (total % n_ctas != 0); }
+
+// An item and the tile within it at a position of the line of all tiles.
+struct Place {
+  int b, h, rb, r;
+};
+__device__ __forceinline__ Place place_of(const PagedAttnParams &p, const int *prefix, int pos, Seq &s) {
+  const int b = seq_of(prefix, p.cache.B, pos);
+  s = sequence(p, b);
+  const int per_head = max(1, (prefix[b + 1] - prefix[b]) / p.cache.Hkv);
+  const int off = pos - prefix[b], h = off / per_head;
+  int rest = off - h * per_head, rb = 0;
+  const int rbs = row_blocks(p, s);
+  for (; rb < rbs; ++rb) {
+    const int n = item_tiles(p, s, rb);
+    if (rest < n) break;
+    rest -= n;
+  }
+  return {b, h, rb, rest};
 }
 
 // A CTA's part of one work item: key tiles [j0, j1) of row block rb.
@@ -151,111 +177,145 @@ struct Segment {
   Seq s;
   int b, h, rb, j0, j1;
   int slot;  // partial written, -1: the whole item, written directly
+  int tok;   // tokens of each of the two tiles
+  int last_cta;  // the CTA that has the item's last tile
 };
-
+__device__ __forceinline__ bool few_rows(const PagedAttnParams &p, const Segment &g) { return g.tok != p.tok; }
 __device__ __forceinline__ const int *page_row(const PagedAttnParams &p, const Segment &g) {
   return p.cache.page_table + g.b * p.cache.table_stride;
 }
 
-// Walks the segments of tile range [pos, end) in order; every role walks its own.
+// Walks the segments of this CTA's range of tiles in order; every role walks its own.
 struct Walk {
-  long long pos, end, begin;
-  int b, h, rb, r;  // r: first tile of the next segment within its item
+  int pos, end, per;
+  Place at;
   bool fresh;
-  __device__ __forceinline__ Walk(const long long *prefix, int B, int n_ctas)
-      : b(0), h(0), rb(0), r(0), fresh(true) {
-    const long long per = tiles_per_cta(prefix[B], n_ctas);
-    begin = pos = min(per * blockIdx.x, prefix[B]);
-    end = min(pos + per, prefix[B]);
+  __device__ __forceinline__ Walk(const int *prefix, int B, int n_ctas) : fresh(true) {
+    per = tiles_per_cta(prefix[B], n_ctas);
+    pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(prefix[B])));
+    end = static_cast<int>(min(static_cast<long long>(pos) + per, static_cast<long long>(prefix[B])));
   }
-  __device__ __forceinline__ bool next(const PagedAttnParams &p, const long long *prefix, Segment &g) {
+  __device__ __forceinline__ bool next(const PagedAttnParams &p, const int *prefix, Segment &g) {
     if (pos >= end) return false;
     if (fresh) {
-      b = seq_of(prefix, p.cache.B, pos);
-      g.s = sequence(p, b);
-      const long long per_head = (prefix[b + 1] - prefix[b]) / p.cache.Hkv;
-      const long long off = pos - prefix[b];
-      h = static_cast<int>(off / per_head);
-      long long rest = off - h * per_head;
-      const int rbs = row_blocks(p, g.s);
-      for (rb = 0; rb < rbs; ++rb) {
-        const int n = item_tiles(p, g.s, rb);
-        if (rest < n) break;
-        rest -= n;
-      }
-      r = static_cast<int>(rest);
+      at = place_of(p, prefix, pos, g.s);
       fresh = false;
     } else {
       // the item after the last one, skipping those that see no key
-      if (++rb >= row_blocks(p, g.s)) {
-        rb = 0;
-        if (++h >= p.cache.Hkv) {
-          h = 0;
-          do ++b;
-          while (b < p.cache.B && prefix[b + 1] == prefix[b]);
-          if (b >= p.cache.B) return false;
-          g.s = sequence(p, b);
+      if (++at.rb >= row_blocks(p, g.s)) {
+        at.rb = 0;
+        if (++at.h >= p.cache.Hkv) {
+          at.h = 0;
+          do ++at.b;
+          while (at.b < p.cache.B && prefix[at.b + 1] == prefix[at.b]);
+          if (at.b >= p.cache.B) return false;
+          g.s = sequence(p, at.b);
         }
       }
       const int rbs = row_blocks(p, g.s);
-      while (rb < rbs && item_tiles(p, g.s, rb) == 0) ++rb;
-      r = 0;
+      while (at.rb < rbs && item_tiles(p, g.s, at.rb) == 0) ++at.rb;
+      at.r = 0;
     }
     // (the bounds on b and rb only matter when the lengths change during the
     // call, which must not happen: then the walk ends instead of running on)
-    const int n = rb < row_blocks(p, g.s) ? item_tiles(p, g.s, rb) : 0;
-    if (n <= r) return false;
-    g.b = b;
-    g.h = h;
-    g.rb = rb;
-    g.j0 = r;
-    g.j1 = static_cast<int>(min(static_cast<long long>(n), r + (end - pos)));
+    const int n = at.rb < row_blocks(p, g.s) ? item_tiles(p, g.s, at.rb) : 0;
+    if (n <= at.r) return false;
+    g.b = at.b;
+    g.h = at.h;
+    g.rb = at.rb;
+    g.j0 = at.r;
+    g.j1 = min(n, at.r + (end - pos));
     g.slot = g.j0 == 0 && g.j1 == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (g.j0 == 0 ? 1 : 0);
+    g.tok = g.s.q_len <= 2 * p.tok32 ? p.tok32 : p.tok;
+    g.last_cta = (pos - g.j0 + n - 1) / per;
     pos += g.j1 - g.j0;
     return true;
   }
   // Key tiles of segment g that query tile t goes through, counted from g.j0.
   static __device__ __forceinline__ int tiles(const PagedAttnParams &p, const Segment &g, int t) {
-    const int first = (2 * g.rb + t) * p.tok;
+    const int first = (2 * g.rb + t) * g.tok;
     if (first >= g.s.q_len) return 0;
-    return max(0, min(g.j1, tiles_seen(p, g.s, first + p.tok)) - g.j0);
+    return max(0, min(g.j1, tiles_seen(p, g.s, first + g.tok)) - g.j0);
   }
 };
+
+// The pages of a key tile and which of them are there. Each lane of a warp
+// looks one up ahead of time; `mask` then has one bit per page.
+struct PageBits {
+  int per_tile;  // pages of a key tile, 1 if a page has 128 keys or more
+  int entry;     // this lane's entry of the next tile
+  __device__ __forceinline__ PageBits(const PagedAttnParams &p)
+      : per_tile(p.page_log2 < 7 ? kRowsPerTile >> p.page_log2 : 1), entry(0) {}
+  __device__ __forceinline__ void look_up(const PagedAttnParams &p, const Segment &g, int j) {
+    const int lane = threadIdx.x & 31;
+    entry = 0;
+    if (lane < per_tile) {
+      const int i = p.page_log2 < 7 ? j * per_tile + lane : (j * kRowsPerTile) >> p.page_log2;
+      if ((i << p.page_log2) < g.s.kv_len) entry = page_row(p, g)[i];
+    }
+  }
+  __device__ __forceinline__ unsigned mask(const PagedAttnParams &p) const {
+    const int lane = threadIdx.x & 31;
+    return __ballot_sync(0xffffffffu, lane >= per_tile || (entry >= 0 && entry < p.cache.n_pages));
+  }
+};
+
+// V slots past kv_len may hold anything, NaN too, and 0 * NaN would reach O:
+// they are zeroed in shared memory before the product reads them. `cv` is the
+// ring position of the V tile; its slot stays the tile's until both issuers
+// have used it.
+template <int D>
+__device__ __forceinline__ bool clear_tail(int valid_keys, int cv, uint32_t bar_full0, uint32_t ring_base,
+                                           volatile int *abort_flag, int *err) {
+  using C = Cfg<D>;
+  const int slot = cv % C::kStages;
+  if (!__all_sync(0xffffffffu, mbar_wait(bar_full0 + 8u * slot, (cv / C::kStages) & 1, abort_flag, err))) return false;
+  const int pieces = (kRowsPerTile - valid_keys) * 8;  // 16-byte pieces of a 128-byte column block
+  for (int i = threadIdx.x & 127; i < pieces * C::kColBlocks; i += 128)
+    st_shared_v4(ring_base + slot * C::kTileBytes + (i / pieces) * kColBlockBytes + valid_keys * 128 + (i % pieces) * 16,
+                 0u, 0u, 0u, 0u);
+  fence_proxy_async_shared();
+  return true;
+}
+
+// O rows of TMEM by alpha (this thread's row; its warp all together).
+template <int D>
+__device__ __forceinline__ void scale_o(uint32_t o_addr, float alpha) {
+#pragma unroll 1
+  for (int cb = 0; cb < D / 32; ++cb) {
+    uint32_t v[32];
+    tmem_ld32(o_addr + 32 * cb, v);
+    tmem_ld_wait(v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+    tmem_st32(o_addr + 32 * cb, v);
+  }
+  tmem_st_wait();
+}
 
 // Softmax and epilogue of one row of query tile t over a segment (one thread a
 // row, TMEM lane = tile row; the dense forward's scheme). `ring` is the ring
 // position of the segment's first K tile.
 template <int D>
-__device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const Segment &g, int t, int n, int r,
+__device__ __noinline__ bool softmax_segment(const PagedAttnParams &p, const Segment &g, int t, int n, int r,
                                                 uint32_t s_addr, uint32_t o_addr, uint32_t bar_sfull,
                                                 uint32_t bar_pfull, uint32_t bar_ofull, uint32_t bar_full0,
                                                 uint32_t ring_base, int ring, int step_base, uint32_t ofull_parity,
                                                 volatile int *abort_flag, int *err) {
-  using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
   const int tok = (2 * g.rb + t) * p.tok + r / p.G;  // within the sequence
   const bool row_valid = r < p.tok * p.G && tok < g.s.q_len;
   const bool warp_valid = __any_sync(0xffffffffu, row_valid);
   const int row_last = !row_valid ? -1 : (p.causal ? g.s.kv_len - g.s.q_len + tok : g.s.kv_len - 1);
   const float c2 = p.scale_log2;
-  const int page_size = 1 << p.page_log2;
-  const int per_tile = page_size < kRowsPerTile ? kRowsPerTile >> p.page_log2 : 1;  // pages of a key tile
-  // which pages of key tile j are there, one bit each (each lane looks one up)
-  auto pages_there = [&](int j) -> unsigned {
-    int e = 0;
-    if (lane < per_tile) {
-      const int i = page_size < kRowsPerTile ? j * per_tile + lane : (j * kRowsPerTile) >> p.page_log2;
-      e = (i << p.page_log2) < g.s.kv_len ? page_row(p, g)[i] : 0;
-    }
-    return __ballot_sync(0xffffffffu, lane >= per_tile || (e >= 0 && e < p.cache.n_pages));
-  };
+  PageBits bits(p);
   float m = -INFINITY, l = 0.f;
   bool ok = true;
-  unsigned there = warp_valid ? pages_there(g.j0) : 0xffffffffu;
+  if (warp_valid && n > 0) bits.look_up(p, g, g.j0);
 
   for (int j = 0; j < n; ++j) {
-    const unsigned now = there;
-    if (warp_valid && j + 1 < n) there = pages_there(g.j0 + j + 1);
+    const unsigned now = warp_valid ? bits.mask(p) : 0xffffffffu;
+    if (warp_valid && j + 1 < n) bits.look_up(p, g, g.j0 + j + 1);
     ok = __all_sync(0xffffffffu, mbar_wait(bar_sfull, static_cast<uint32_t>(step_base + j) & 1u, abort_flag, err));
     if (!ok) break;
     tc_fence_after();
@@ -273,7 +333,7 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
         if (holes) {
 #pragma unroll
           for (int c = 0; c < cols; ++c)
-            if (!((now >> (per_tile == 1 ? 0 : (c0 + c) >> p.page_log2)) & 1u)) x[c] = __float_as_uint(-INFINITY);
+            if (!((now >> (bits.per_tile == 1 ? 0 : (c0 + c) >> p.page_log2)) & 1u)) x[c] = __float_as_uint(-INFINITY);
         }
       };
       auto load_scores = [&](uint32_t(&sr)[128]) {
@@ -307,16 +367,7 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
           const float alpha = (m_new == -INFINITY) ? 1.f : ex2_approx(m - m_new);
           m = m_new;
           l *= alpha;
-#pragma unroll 1
-          for (int cb = 0; cb < D / 32; ++cb) {
-            uint32_t orr[32];
-            tmem_ld32(o_addr + 32 * cb, orr);
-            tmem_ld_wait(orr);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * alpha);
-            tmem_st32(o_addr + 32 * cb, orr);
-          }
-          tmem_st_wait();
+          scale_o<D>(o_addr, alpha);
           load_scores(sr);
           rowsum = exp_row<false, 0>(reinterpret_cast<const float *>(sr), c2, (m == -INFINITY) ? 0.f : m, pk);
         }
@@ -326,20 +377,9 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
       tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
       tmem_st_wait();
     }
-    // V slots past kv_len may hold anything, NaN too, and 0 * NaN would reach
-    // O: they are zeroed in shared memory before the product reads them. The
-    // slot stays this tile's until both issuers have used it.
-    const int valid_keys = g.s.kv_len - kv0;
-    if (valid_keys < kRowsPerTile) {
-      const int cv = ring + 2 * j + 1, slot = cv % C::kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_full0 + 8u * slot, (cv / C::kStages) & 1, abort_flag, err));
+    if (g.s.kv_len - kv0 < kRowsPerTile) {
+      ok = clear_tail<D>(g.s.kv_len - kv0, ring + 2 * j + 1, bar_full0, ring_base, abort_flag, err);
       if (!ok) break;
-      const int pieces = (kRowsPerTile - valid_keys) * 8;  // 16-byte pieces of a 128-byte column block
-      for (int i = threadIdx.x & 127; i < pieces * C::kColBlocks; i += 128)
-        st_shared_v4(ring_base + slot * C::kTileBytes + (i / pieces) * kColBlockBytes + valid_keys * 128 +
-                         (i % pieces) * 16,
-                     0u, 0u, 0u, 0u);
-      fence_proxy_async_shared();
     }
     tc_fence_before();
     __syncwarp();
@@ -409,22 +449,197 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
   return done;
 }
 
+// The same for a tile of at most 32 rows held four times: warp w of the
+// warpgroup takes keys 32 w .. 32 w + 31 of each tile for the rows of its copy
+// (lane = row), the copies are merged at the end through `stage` (this tile's
+// 8 KB of shared memory).
+template <int D>
+__device__ __noinline__ bool few_rows_segment(const PagedAttnParams &p, const Segment &g, int t, int n, int w,
+                                                 uint32_t s_addr, uint32_t o_addr, uint32_t bar_sfull,
+                                                 uint32_t bar_pfull, uint32_t bar_ofull, uint32_t bar_full0,
+                                                 uint32_t ring_base, int ring, int step_base, uint32_t ofull_parity,
+                                                 float *stage, volatile int *abort_flag, int *err) {
+  const int lane = threadIdx.x & 31;
+  const int tok = t * g.tok + lane / p.G;
+  const bool row_valid = lane < g.tok * p.G && tok < g.s.q_len;
+  if (t * g.tok >= g.s.q_len) return true;  // no row of this tile: n is 0 too
+  // last key seen, counted from this warp's first one
+  const int row_last = (!row_valid ? -1 : (p.causal ? g.s.kv_len - g.s.q_len + tok : g.s.kv_len - 1)) - 32 * w;
+  const float c2 = p.scale_log2;
+  PageBits bits(p);
+  float m = -INFINITY, l = 0.f;
+  bool ok = true;
+  if (n > 0) bits.look_up(p, g, g.j0);
+  for (int j = 0; j < n; ++j) {
+    const unsigned now = bits.mask(p);
+    if (j + 1 < n) bits.look_up(p, g, g.j0 + j + 1);
+    ok = __all_sync(0xffffffffu, mbar_wait(bar_sfull, static_cast<uint32_t>(step_base + j) & 1u, abort_flag, err));
+    if (!ok) break;
+    tc_fence_after();
+    const int kv0 = (g.j0 + j) * kRowsPerTile;
+    uint32_t x[32];
+    // the scores times scale log2(e), masked
+    auto load_scores = [&] {
+      tmem_ld32(s_addr + 32 * w, x);
+      tmem_ld_wait(x);
+      const int last = row_last - kv0;
+      if (__any_sync(0xffffffffu, row_valid && last < 31)) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c > last) x[c] = __float_as_uint(-INFINITY);
+      }
+      if (now != 0xffffffffu) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (!((now >> (bits.per_tile == 1 ? 0 : (32 * w + c) >> p.page_log2)) & 1u))
+            x[c] = __float_as_uint(-INFINITY);
+      }
+      if (!row_valid) {  // rows of no token, other sequences' rows: nothing
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = __float_as_uint(-INFINITY);
+      }
+    };
+    load_scores();
+    float top = __uint_as_float(x[0]);
+#pragma unroll
+    for (int c = 1; c < 31; c += 2) top = fmax3(top, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+    top = fmaxf(top, __uint_as_float(x[31])) * c2;
+    // the reference moves, and O with it, only when it would let a P above 2^8
+    // through or there is none yet
+    const bool move = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
+    if (__any_sync(0xffffffffu, move)) {
+      const float m_new = fmaxf(m, top);
+      const float alpha = (m_new == -INFINITY) ? 1.f : ex2_approx(m - m_new);
+      m = m_new;
+      l *= alpha;
+      if (j > 0) scale_o<D>(o_addr, alpha);
+    }
+    const float ref = (m == -INFINITY) ? 0.f : m;
+    uint32_t pk[16];
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float a = ex2_approx(fmaf(__uint_as_float(x[2 * c]), c2, -ref));
+      const float b = ex2_approx(fmaf(__uint_as_float(x[2 * c + 1]), c2, -ref));
+      s0 += a;
+      s1 += b;
+      // P enters the tensor cores in bf16, as in the dense forward; l is summed before the rounding
+      __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      pk[c] = *reinterpret_cast<uint32_t *>(&h);
+    }
+    l += s0 + s1;
+    const uint32_t none[16] = {};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q == w) tmem_st16(s_addr + 16 * q, pk);
+      else tmem_st16(s_addr + 16 * q, none);
+    }
+    tmem_st_wait();
+    if (g.s.kv_len - kv0 < kRowsPerTile) {
+      ok = clear_tail<D>(g.s.kv_len - kv0, ring + 2 * j + 1, bar_full0, ring_base, abort_flag, err);
+      if (!ok) break;
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_pfull);
+  }
+  bool have_o = false;
+  if (ok && n > 0) {
+    have_o = __all_sync(0xffffffffu, mbar_wait(bar_ofull, ofull_parity, abort_flag, err));
+    tc_fence_after();
+  }
+  const int id = 1 + t;
+  if (!named_bar_and(id, 128, ok && (n == 0 || have_o))) return false;
+  // weights of the four copies of each row
+  float2 *stats = reinterpret_cast<float2 *>(stage);
+  stats[32 * w + lane] = make_float2(m, l);
+  named_bar_sync(id, 128);
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) top = fmaxf(top, stats[32 * q + lane].x);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float2 v = stats[32 * q + lane];
+    if (v.y > 0.f) sum = fmaf(v.y, ex2_approx(v.x - top), sum);
+  }
+  const float mine = l > 0.f ? ex2_approx(m - top) / sum : 0.f;
+  const int head = g.h * p.G + lane % p.G;
+  const int row = g.s.q0 + tok;
+  const size_t part = static_cast<size_t>(max(g.slot, 0)) * p.part_rows + t * g.tok * p.G + lane;
+  if (w == 0 && row_valid) {
+    const float lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    if (g.slot >= 0) p.part_lse[part] = lse;
+    else if (p.lse) p.lse[static_cast<size_t>(head) * p.total_q + row] = lse;
+  }
+  // O, 16 columns at a time: every copy's share, then warp w sums columns 4 w ..
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 16) {
+    uint32_t v[16];
+    if (have_o) {
+      tmem_ld16(o_addr + c0, v);
+      tmem_ld_wait(v);
+    }
+    named_bar_sync(id, 128);  // the stage has been read
+#pragma unroll
+    for (int i = 0; i < 16; ++i) stage[(16 * w + i) * 32 + lane] = mine > 0.f ? __uint_as_float(v[i]) * mine : 0.f;
+    named_bar_sync(id, 128);
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float *x = stage + (4 * w + i) * 32 + lane;
+      o[i] = (x[0] + x[16 * 32]) + (x[32 * 32] + x[48 * 32]);
+    }
+    if (row_valid) {
+      if (g.slot >= 0) {
+        *reinterpret_cast<float4 *>(p.part_o + part * D + c0 + 4 * w) = make_float4(o[0], o[1], o[2], o[3]);
+      } else {
+        __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h + row * p.o_s + c0 + 4 * w) =
+            make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+      }
+    }
+  }
+  named_bar_sync(id, 128);  // before the next segment's stats
+  return true;
+}
+
+// Rows of the items that see no key at all (every row, if `all`): O = 0, lse = -inf.
+template <int D>
+__device__ void write_unseen(const PagedAttnParams &p, bool all, int tid, int nthreads) {
+  for (int b = blockIdx.x; b < p.cache.B; b += gridDim.x) {
+    const Seq s = sequence(p, b);
+    const int rbs = row_blocks(p, s);
+    int rb = 0;
+    while (rb < rbs && item_tiles(p, s, rb) == 0) ++rb;
+    const int toks = all ? s.q_len : min(s.q_len, rb * 2 * p.tok);
+    for (long long i = tid; i < static_cast<long long>(toks) * p.Hq * (D / 8); i += nthreads) {
+      const int c = static_cast<int>(i % (D / 8));
+      const int head = static_cast<int>(i / (D / 8) % p.Hq), row = s.q0 + static_cast<int>(i / (D / 8) / p.Hq);
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h + row * p.o_s + 8 * c) =
+          make_uint4(0u, 0u, 0u, 0u);
+      if (c == 0 && p.lse) p.lse[static_cast<size_t>(head) * p.total_q + row] = -INFINITY;
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttnParams p) {
+    attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q32,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ PagedAttnParams p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem =
       reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *sQ = smem;                          // [tile][col block][128 rows][128 B]
   uint8_t *sRing = smem + 2 * C::kTileBytes;   // [slot][col block][128 rows][128 B]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sRing + C::kStages * C::kTileBytes);
+  uint8_t *sStage = sRing + C::kStages * C::kTileBytes;  // [tile][8 KB]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sStage + 2 * C::kStageBytes);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBarriers);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *turn = reinterpret_cast<volatile int *>(tmem_slot + 2);
-  long long *warp_sums = reinterpret_cast<long long *>(tmem_slot + 4);
-  long long *prefix = warp_sums + 12;
+  int *warp_sums = reinterpret_cast<int *>(tmem_slot + 4);
+  int *prefix = warp_sums + 12;
 
   const uint32_t bar0 = smem_addr(bars);
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -460,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  launch_dependents();  // the merge: its CTAs wait for this kernel before they read
   const uint32_t tmem = *tmem_slot;
   const bool skip = *abort_flag != 0;
   auto tS = [&](int t) -> uint32_t { return tmem + 128u * static_cast<uint32_t>(t); };
@@ -472,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!skip) {
       if (lane == 0) {
         tma_prefetch_map(&tm_q);
+        tma_prefetch_map(&tm_q32);
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
       }
@@ -480,10 +697,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool small = page_size < kRowsPerTile;
       const int boxes = small ? kRowsPerTile >> p.page_log2 : 1;  // pages of a key tile
       const uint32_t box_bytes = (small ? page_size : kRowsPerTile) * 128u;
-      const uint32_t q_bytes = static_cast<uint32_t>(p.tok * p.G) * 128u * C::kColBlocks;
       int c = 0, nq = 0;
       bool ok = true;
+      // the item that this CTA begins and another one ends, for the merge
+      int4 cut = make_int4(0, 0, 0, 0);
       while (ok && walk.next(p, prefix, g)) {
+        if (g.j0 == 0 && g.slot >= 0)
+          cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, g.last_cta);
         const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
         const bool two = Walk::tiles(p, g, 1) > 0;
         const int *row = page_row(p, g);
@@ -499,11 +719,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           ok = nq == 0 || mbar_wait(bar(kBarQEmpty), (nq - 1) & 1, abort_flag, err);
           if (ok) {
+            const bool few = few_rows(p, g);
+            const int copies = few ? 4 : 1;  // of each tile, 32 rows apart
+            const uint32_t q_bytes = static_cast<uint32_t>(copies * g.tok * p.G) * 128u * C::kColBlocks;
             mbar_arrive_expect_tx(bar(kBarQFull), two ? 2 * q_bytes : q_bytes);
             for (int t = 0; t < (two ? 2 : 1); ++t)
               for (int cb = 0; cb < C::kColBlocks; ++cb)
-                tma_load_4d_hint(smem_addr(sQ + (t * C::kColBlocks + cb) * kColBlockBytes), &tm_q, bar(kBarQFull),
-                                 cb * 64, 0, g.s.q0 + (2 * g.rb + t) * p.tok, g.h, pol_q);
+                for (int k = 0; k < copies; ++k)
+                  tma_load_4d_hint(smem_addr(sQ + (t * C::kColBlocks + cb) * kColBlockBytes + k * 32 * 128),
+                                   few ? &tm_q32 : &tm_q, bar(kBarQFull), cb * 64, 0,
+                                   g.s.q0 + (2 * g.rb + t) * g.tok, g.h, pol_q);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -532,6 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (lane == 0) p.cuts[blockIdx.x] = cut;
       if (lane == 0) {  // every copy must have landed before the CTA may exit
         if (nq > 0) mbar_drain(bar(kBarQFull), (nq - 1) & 1, err);
         for (int i = max(0, c - C::kStages); i < c; ++i)
@@ -552,9 +778,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && walk.next(p, prefix, g)) {
         const int nt = Walk::tiles(p, g, t);
         const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
+        // tile 1 has nothing to do: its issuer only gives Q back, and tile 0's
+        // goes on without taking turns and releases each slot for both
+        const bool single = Walk::tiles(p, g, 1) == 0;
         if (!mbar_wait(bar(kBarQFull), nq & 1, abort_flag, err)) break;
         ++nq;
         if (nt == 0) mma_commit(bar(kBarQEmpty));
+        if (single && t == 1) {
+          c += 2 * n_max;
+          continue;
+        }
         for (int j = 0; ok && j <= n_max; ++j) {
           const int cK = c + 2 * j, cV = c + 2 * j - 1;
           const int sK = cK % C::kStages, sV = (cV + C::kStages) % C::kStages;
@@ -575,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const int turn_at = base + 2 * j + t;
-          if (!wait_turn(turn, turn_at, abort_flag, err)) {
+          if (!single && !wait_turn(turn, turn_at, abort_flag, err)) {
             ok = false;
             break;
           }
@@ -594,14 +827,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_ss(s_col, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
             }
           }
-          *turn = turn_at + 1;
+          if (!single) *turn = turn_at + 1;
           if (has_s) mma_commit(bar(kBarSFull + t));
           if (has_pv) {
             if (j - 1 == nt - 1) mma_commit(bar(kBarOFull + t));
             mma_commit(bar(kBarEmpty + sV));
+            if (single) mma_commit(bar(kBarEmpty + sV));
           }
           if (has_s) {
             mma_commit(bar(kBarEmpty + sK));
+            if (single) mma_commit(bar(kBarEmpty + sK));
             if (j == nt - 1) mma_commit(bar(kBarQEmpty));
           }
           if (unused) {
@@ -611,24 +846,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         c += 2 * n_max;
         steps += nt;
-        base += 2 * (n_max + 1);
+        if (!single) base += 2 * (n_max + 1);
       }
       mma_commit(bar(kBarMmaDone));
       mbar_drain(bar(kBarMmaDone), 0, err);
     }
     __syncwarp();
-  } else if (warp < 8 && !skip) {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax + epilogue
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int steps = 0, ring = 0;
     uint32_t u = 0;
-    while (walk.next(p, prefix, g)) {
+    write_unseen<D>(p, skip, threadIdx.x, 256);
+    while (!skip && walk.next(p, prefix, g)) {
       const int n = Walk::tiles(p, g, t), n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
-      if (!softmax_segment<D>(p, g, t, n, r, tS(t) + lane_off, tO(t) + lane_off, bar(kBarSFull + t),
-                              bar(kBarPFull + t), bar(kBarOFull + t), bar(kBarFull), smem_addr(sRing), ring, steps,
-                              u & 1u, abort_flag, err))
-        break;
+      const bool fine =
+          few_rows(p, g)
+              ? few_rows_segment<D>(p, g, t, n, warp & 3, tS(t) + lane_off, tO(t) + lane_off, bar(kBarSFull + t),
+                                    bar(kBarPFull + t), bar(kBarOFull + t), bar(kBarFull), smem_addr(sRing), ring, steps,
+                                    u & 1u, reinterpret_cast<float *>(sStage + t * C::kStageBytes), abort_flag, err)
+              : softmax_segment<D>(p, g, t, n, r, tS(t) + lane_off, tO(t) + lane_off, bar(kBarSFull + t),
+                                   bar(kBarPFull + t), bar(kBarOFull + t), bar(kBarFull), smem_addr(sRing), ring, steps,
+                                   u & 1u, abort_flag, err);
+      if (!fine) break;
       ring += 2 * n_max;
       steps += n;
       if (n > 0) ++u;
@@ -643,110 +884,96 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The rows that the ranges cut, and the rows of items that see no key. Grid:
-// (row blocks, KV heads, sequences); a warp takes a row: the weights
-// exp(lse_i - max) of its partials, then their weighted sum in the order of
-// the keys, four (D = 128) or two columns a lane.
+// The rows of the items that were cut. CTA blockIdx.x of the attention began
+// such an item and described it (first token, rows, KV head, last CTA); a warp
+// takes a row (blockIdx.y: 8 rows): the weights exp(lse_i - max) of the row's
+// partials, then their weighted sum in the order of the keys, four (D = 128)
+// or two columns a lane.
 constexpr int kMergeThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PagedAttnParams p, int n_ctas) {
-  extern __shared__ long long prefix[];  // [B + 1], then 12 sums
-  const bool failed = *reinterpret_cast<volatile int *>(&g_device_error) != kErrNone;
-  prefix_tiles(p, prefix, prefix + p.cache.B + 1);
-  const long long per = tiles_per_cta(prefix[p.cache.B], n_ctas);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PagedAttnParams p) {
+  wait_prerequisites();
+  const int4 cut = p.cuts[blockIdx.x];
+  const int lane = threadIdx.x & 31, r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  if (r >= cut.y) return;
+  const int c0 = blockIdx.x, c1 = cut.w;
   constexpr int kCols = D / 32;
-  for (int b = blockIdx.z; b < p.cache.B; b += gridDim.z) {
-    const Seq s = sequence(p, b);
-    const int rbs = row_blocks(p, s);
-    for (int rb = blockIdx.x; rb < rbs; rb += gridDim.x) {
-      const int h = blockIdx.y;
-      const int n = failed ? 0 : item_tiles(p, s, rb);
-      long long t0 = 0;
-      int c0 = 0, c1 = 0;
-      if (n > 0) {
-        const long long per_head = (prefix[b + 1] - prefix[b]) / p.cache.Hkv;
-        t0 = prefix[b] + h * per_head + tiles_before(p, s, rb);
-        c0 = static_cast<int>(t0 / per);
-        c1 = static_cast<int>((t0 + n - 1) / per);
-        if (c0 == c1) continue;
-      }
-      const int rows = min(2 * p.tok, s.q_len - rb * 2 * p.tok) * p.G;
-      for (int r = warp; r < rows; r += kMergeThreads / 32) {
-        float acc[kCols] = {};
-        float m = -INFINITY, sum = 0.f;
-        auto at = [&](int c) -> size_t {
-          return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + r;
-        };
-        if (n > 0) {
-          for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[at(c)]);
+  float acc[kCols] = {};
+  float m = -INFINITY, sum = 0.f;
+  auto part = [&](int c) -> size_t { return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + r; };
+  // a timeout somewhere: the partials may be missing, the rows come out empty
+  const bool failed = *reinterpret_cast<volatile int *>(&g_device_error) != kErrNone;
+  if (!failed) {
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[part(c)]);
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  }
+  if (m != -INFINITY) {
+    for (int cb = c0; cb <= c1; cb += 32) {
+      const float w = cb + lane <= c1 ? expf(p.part_lse[part(cb + lane)] - m) : 0.f;
+      sum += w;
+      const int k_end = min(32, c1 - cb + 1);
+#pragma unroll 8
+      for (int k = 0; k < k_end; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        if (wk == 0.f) continue;  // a partial that saw no key has no O
+        const float *x = p.part_o + part(cb + k) * D + lane * kCols;
+        if constexpr (kCols == 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(x);
+          acc[0] = fmaf(wk, v.x, acc[0]);
+          acc[1] = fmaf(wk, v.y, acc[1]);
+          acc[2] = fmaf(wk, v.z, acc[2]);
+          acc[3] = fmaf(wk, v.w, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2 *>(x);
+          acc[0] = fmaf(wk, v.x, acc[0]);
+          acc[1] = fmaf(wk, v.y, acc[1]);
         }
-        if (m != -INFINITY) {
-          for (int cb = c0; cb <= c1; cb += 32) {
-            const float w = cb + lane <= c1 ? expf(p.part_lse[at(cb + lane)] - m) : 0.f;
-            sum += w;
-            const int k_end = min(32, c1 - cb + 1);
-#pragma unroll 4
-            for (int k = 0; k < k_end; ++k) {
-              const float wk = __shfl_sync(0xffffffffu, w, k);
-              if (wk == 0.f) continue;  // a partial that saw no key has no O
-              const float *x = p.part_o + at(cb + k) * D + lane * kCols;
-              if constexpr (kCols == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(x);
-                acc[0] = fmaf(wk, v.x, acc[0]);
-                acc[1] = fmaf(wk, v.y, acc[1]);
-                acc[2] = fmaf(wk, v.z, acc[2]);
-                acc[3] = fmaf(wk, v.w, acc[3]);
-              } else {
-                const float2 v = *reinterpret_cast<const float2 *>(x);
-                acc[0] = fmaf(wk, v.x, acc[0]);
-                acc[1] = fmaf(wk, v.y, acc[1]);
-              }
-            }
-          }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const int head = h * p.G + r % p.G, row = s.q0 + rb * 2 * p.tok + r / p.G;
-        __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h +
-                                                                 row * p.o_s + lane * kCols);
-#pragma unroll
-        for (int i = 0; i < kCols / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-        if (lane == 0 && p.lse)
-          p.lse[static_cast<size_t>(head) * p.total_q + row] = sum > 0.f ? m + logf(sum) : -INFINITY;
       }
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int head = cut.z * p.G + r % p.G, row = cut.x + r / p.G;
+  __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h +
+                                                           row * p.o_s + lane * kCols);
+#pragma unroll
+  for (int i = 0; i < kCols / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if (lane == 0 && p.lse)
+    p.lse[static_cast<size_t>(head) * p.total_q + row] = sum > 0.f ? m + logf(sum) : -INFINITY;
 }
 
 template <int D>
-cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tq32, const CUtensorMap &tk, const CUtensorMap &tv,
                          const PagedAttnParams &p, cudaStream_t stream) {
   auto kernel = attn_paged_kernel<D>;
   constexpr int kSmem = Cfg<D>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int n_ctas = sm_count() < kPagedMaxCtas ? sm_count() : kPagedMaxCtas;
-  kernel<<<n_ctas, kThreads, kSmem, stream>>>(tq, tk, tv, p);
+  kernel<<<n_ctas, kThreads, kSmem, stream>>>(tq, tq32, tk, tv, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // row blocks of the longest chunk there can be, bounded: the kernel strides
-  const long long rbs = (static_cast<long long>(p.total_q) + 2 * p.tok - 1) / (2 * p.tok);
-  const unsigned gx = static_cast<unsigned>(rbs < 64 ? rbs : 64);
-  const unsigned gz = static_cast<unsigned>(p.cache.B < 1024 ? p.cache.B : 1024);
-  const size_t smem = sizeof(long long) * (static_cast<size_t>(p.cache.B) + 1 + 12);
-  merge_kernel<D><<<dim3(gx, p.cache.Hkv, gz), kMergeThreads, smem, stream>>>(p, n_ctas);
-  return cudaGetLastError();
+  if (e != cudaSuccess || n_ctas == 1) return e;
+  // the merge starts while the attention still runs and waits for its end inside
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(n_ctas - 1, (p.part_rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
 }
 
 }  // namespace paged
 
-cudaError_t launch_attn_paged(int D, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                              const PagedAttnParams &p, cudaStream_t stream) {
-  return D == 64 ? paged::launch_typed<64>(tq, tk, tv, p, stream) : paged::launch_typed<128>(tq, tk, tv, p, stream);
+cudaError_t launch_attn_paged(int D, const CUtensorMap &tq, const CUtensorMap &tq32, const CUtensorMap &tk,
+                              const CUtensorMap &tv, const PagedAttnParams &p, cudaStream_t stream) {
+  return D == 64 ? paged::launch_typed<64>(tq, tq32, tk, tv, p, stream)
+                 : paged::launch_typed<128>(tq, tq32, tk, tv, p, stream);
 }
 
 }  // namespace seqattn

@@ -18,28 +18,38 @@ sequences (or CPU int32 tensors), checked before anything is launched.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
+import struct
 
 import torch
 
-from . import ATTN_BF16, ATTN_F32, _check, _require, _stream_handle
-from ._lib import PagedCacheView, PagedPool, RopeRows, lib
+from . import ATTN_BF16, ATTN_F32, _check, _require
+from ._lib import PagedPool, lib
 
 PAGED_NO_PAGES, PAGED_TOO_LONG, PAGED_IN_USE = 1, 2, 3
-_BF16, _I32 = torch.bfloat16, torch.int32
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+# paged_cache and rope_rows of include/seqattn_paged.h, packed (cheaper per call than ctypes structures)
+_CACHE = struct.Struct("@PPqPqPPiiiiii")
+_ROWS = struct.Struct("@PPqqqqqqi4x")
 
 
-def _on(device: torch.device):
-    """The device of the tensors as the current one (the kernels launch there)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _call(fn, what: str, dev: int, *args) -> None:
+    """fn(*args, stream) with device `dev` current (the kernels launch there), on its current stream."""
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != 0:
+        _check(st, what)
 
 
-def _one_device(what: str, *tensors):
-    dev = tensors[0].device
+def _one_device(what: str, *tensors) -> int:
+    dev = tensors[0].get_device()
     for t in tensors:
-        _require(t.is_cuda and t.device == dev, f"{what}: all tensors must be on one CUDA device")
+        if dev < 0 or t.get_device() != dev:
+            raise ValueError(f"{what}: all tensors must be on one CUDA device")
     return dev
 
 
@@ -47,53 +57,61 @@ def _host_ints(x, what: str) -> torch.Tensor:
     """A host list of ints as a contiguous int32 CPU tensor."""
     if not isinstance(x, torch.Tensor):
         x = torch.tensor([int(v) for v in x], dtype=_I32)
-    _require(x.device.type == "cpu" and x.dtype == _I32 and x.dim() == 1, f"{what} must be host ints (or int32 CPU)")
-    return x.contiguous()
+    if x.is_cuda or x.dtype != _I32 or x.dim() != 1:
+        raise ValueError(f"{what} must be host ints (or int32 CPU)")
+    return x if x.is_contiguous() else x.contiguous()
 
 
-def _ints(t: torch.Tensor, shape, what: str) -> None:
-    _require(t.dtype == _I32 and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-             f"{what} must be contiguous int32 {list(shape)}")
+def _ints(t: torch.Tensor, n: int, what: str) -> None:
+    if t.dtype != _I32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 [{n}]")
 
 
-def _tables(page_table: torch.Tensor, kv_lens=None, page_refs=None) -> None:
-    _require(page_table.dim() == 2 and page_table.dtype == _I32
-             and (page_table.shape[1] <= 1 or page_table.stride(1) == 1), "page_table must be int32 [B, max_pages]")
+def _tables(page_table: torch.Tensor, kv_lens=None, page_refs=None):
+    """(rows, columns, row stride) of the page table."""
+    if page_table.dim() != 2 or page_table.dtype != _I32:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    (B, W), (sb, sw) = page_table.shape, page_table.stride()
+    if (W > 1 and sw != 1) or (B > 1 and sb < W):
+        raise ValueError("page_table must have contiguous rows that do not overlap")
     if kv_lens is not None:
-        _ints(kv_lens, page_table.shape[:1], "kv_lens")
-    if page_refs is not None:
-        _require(page_refs.dtype == _I32 and page_refs.dim() == 1 and page_refs.is_contiguous() and page_refs.numel() > 0,
-                 "page_refs must be contiguous int32 [n_pages]")
-
-
-def _table_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+        _ints(kv_lens, B, "kv_lens")
+    if page_refs is not None and (page_refs.dtype != _I32 or page_refs.dim() != 1 or not page_refs.is_contiguous()
+                                  or page_refs.numel() == 0):
+        raise ValueError("page_refs must be contiguous int32 [n_pages]")
+    return B, W, sb if B > 1 else W
 
 
 def _distinct_memory(t: torch.Tensor, what: str) -> None:
     """Every dimension longer than one has a non-zero stride (no expanded output)."""
-    _require(all(n <= 1 or s != 0 for n, s in zip(t.shape, t.stride())), f"{what} must not be expanded")
+    if 0 in t.stride() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{what} must not be expanded")
 
 
-def _packed(t: torch.Tensor, total: int, D: int, dtype, what: str) -> None:
-    _require(t.dim() == 3 and t.shape[1] == total and t.shape[2] == D and t.dtype == dtype and t.is_cuda
-             and t.stride(2) == 1, f"{what} must be {dtype} [H, {total}, {D}] with D contiguous")
+def _packed(t: torch.Tensor, total: int, D: int, what: str):
+    """Strides of bf16 rows [H, total, D] with D contiguous."""
+    if t.dim() != 3 or t.dtype != _BF16 or t.shape[1] != total or t.shape[2] != D or t.stride(2) != 1:
+        raise ValueError(f"{what} must be bf16 [H, {total}, {D}] with D contiguous")
+    return t.stride()
 
 
-def _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens) -> PagedCacheView:
-    _require(k_pages.dim() == 4 and v_pages.shape == k_pages.shape, "pools must be [n_pages, Hkv, page_size, D]")
+def _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens):
+    """paged_cache as bytes, its device, and (B, Hkv, D)."""
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("pools must be [n_pages, Hkv, page_size, D]")
     n_pages, Hkv, ps, D = k_pages.shape
-    for t in (k_pages, v_pages):
-        _require(t.dtype == _BF16 and (n_pages == 0 or t[0].is_contiguous()), "pools must be bf16 with contiguous pages")
-    stride = k_pages.stride(0) if n_pages > 1 else Hkv * ps * D
-    _require(n_pages <= 1 or v_pages.stride(0) == stride, "the K and V pools must share their page stride")
-    _tables(page_table, kv_lens)
-    B = page_table.shape[0]
-    _ints(cu_seqlens, (B + 1,), "cu_seqlens")
-    _one_device("cache", k_pages, v_pages, page_table, kv_lens, cu_seqlens)
-    return PagedCacheView(k_pages.data_ptr(), v_pages.data_ptr(), stride, page_table.data_ptr(),
-                          _table_stride(page_table), kv_lens.data_ptr(), cu_seqlens.data_ptr(), B, n_pages, ps,
-                          page_table.shape[1], Hkv, D)
+    sk, sv = k_pages.stride(), v_pages.stride()
+    if (k_pages.dtype != _BF16 or v_pages.dtype != _BF16 or sk[3] != 1 or (ps > 1 and sk[2] != D)
+            or (Hkv > 1 and sk[1] != ps * D) or sv[1:] != sk[1:]):
+        raise ValueError("pools must be bf16 with contiguous pages")
+    if n_pages > 1 and sv[0] != sk[0]:
+        raise ValueError("the K and V pools must share their page stride")
+    B, W, row = _tables(page_table, kv_lens)
+    _ints(cu_seqlens, B + 1, "cu_seqlens")
+    dev = _one_device("the cache (CUDA tensors)", k_pages, v_pages, page_table, kv_lens, cu_seqlens)
+    return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), sk[0] if n_pages > 1 else Hkv * ps * D,
+                       page_table.data_ptr(), row, kv_lens.data_ptr(), cu_seqlens.data_ptr(), B, n_pages, ps, W, Hkv,
+                       D), dev, B, Hkv, D
 
 
 def attn_paged_workspace_bytes(Hq: int, Hkv: int, total_q: int, D: int) -> int:
@@ -118,33 +136,35 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, pa
     (unspecified where they are made here). workspace: a uint8 CUDA tensor of
     attn_paged_workspace_bytes(...), for one call at a time (made per call when
     not given)."""
-    _require(q.dim() == 3, "expected q [Hq, total_q, D]")
+    if q.dim() != 3:
+        raise ValueError("expected q [Hq, total_q, D]")
     Hq, total, D = q.shape
-    view = _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens)
-    _require(view.D == D and Hq % view.Hkv == 0, "q must have the cache's D and a multiple of its heads")
-    _packed(q, total, D, _BF16, "q")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    view, dev, B, Hkv, d = _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens)
+    if d != D or Hkv == 0 or Hq % Hkv != 0:
+        raise ValueError("q must have the cache's D and a multiple of its heads")
+    sq = _packed(q, total, D, "q")
     if out is None:
         out = torch.empty((Hq, total, D), dtype=_BF16, device=q.device)
+    else:
+        _distinct_memory(out, "out")
     if lse is None:
-        lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
-    _packed(out, total, D, _BF16, "out")
-    _distinct_memory(out, "out")
-    _require(out.shape[0] == Hq, "bad out")
-    _require(lse.shape == (Hq, total) and lse.dtype == torch.float32 and lse.is_contiguous(), "bad lse")
-    if total == 0 or view.B == 0:
+        lse = torch.empty((Hq, total), dtype=_F32, device=q.device)
+    so = _packed(out, total, D, "out")
+    if out.shape[0] != Hq:
+        raise ValueError("bad out")
+    if lse.dtype != _F32 or lse.shape != (Hq, total) or not lse.is_contiguous():
+        raise ValueError("bad lse")
+    if total == 0 or B == 0:
         return out, lse
-    need = attn_paged_workspace_bytes(Hq, view.Hkv, total, D)
+    need = lib.attn_paged_workspace_bytes(Hq, Hkv, total, D)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _require(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.numel() >= need,
-             "workspace must be a contiguous uint8 tensor of attn_paged_workspace_bytes(...) bytes")
-    dev = _one_device("attn_paged", q, k_pages, out, lse, workspace)
-    with _on(dev):
-        st = lib.attn_paged(q.data_ptr(), q.stride(0), q.stride(1), ctypes.addressof(view), out.data_ptr(),
-                            out.stride(0), out.stride(1), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), Hq,
-                            total, int(bool(causal)), scale, _stream_handle(dev))
-    _check(st, "attn_paged")
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
+        raise ValueError("workspace must be a contiguous uint8 tensor of attn_paged_workspace_bytes(...) bytes")
+    _one_device("attn_paged", k_pages, q, out, lse, workspace)
+    _call(lib.attn_paged, "attn_paged", dev, q.data_ptr(), sq[0], sq[1], view, out.data_ptr(), so[0], so[1],
+          lse.data_ptr(), workspace.data_ptr(), workspace.numel(), Hq, total, 1 if causal else 0,
+          1.0 / math.sqrt(D) if scale is None else float(scale))
     return out, lse
 
 
@@ -175,43 +195,48 @@ def _plan(inv_freq, axes, D: int):
     if not isinstance(inv_freq, torch.Tensor):
         inv_freq = torch.tensor([float(f) for f in inv_freq], dtype=torch.float64)
     axes = _host_ints(axes, "axes")
-    _require(inv_freq.device.type == "cpu" and inv_freq.dtype == torch.float64 and inv_freq.is_contiguous(),
-             "inv_freq must be host floats (or float64 CPU)")
-    _require(tuple(inv_freq.shape) == (D // 2,) and tuple(axes.shape) == (D // 2,), "inv_freq and axes need D / 2 entries")
+    if inv_freq.is_cuda or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be host floats (or float64 CPU)")
+    if inv_freq.numel() != D // 2 or axes.numel() != D // 2:
+        raise ValueError("inv_freq and axes need D / 2 entries")
     return inv_freq, axes
 
 
 def _rope(q, k, positions, inv_freq, axes, interleaved, inverse, out_q, out_k):
-    given = [t for t in (q, k) if t is not None]
-    _require(len(given) > 0, "q or k is needed")
-    B, _, S, D = given[0].shape
-    dtype = given[0].dtype
-    _require(dtype in (_BF16, torch.float32), "rows must be bf16 or fp32")
-    views, outs = [], []
-    for t, o in ((q, out_q), (k, out_k)):
+    first = k if q is None else q
+    if first is None:
+        raise ValueError("q or k is needed")
+    if first.dim() != 4:
+        raise ValueError("rows must be [B, H, S, D]")
+    B, _, S, D = first.shape
+    dtype = first.dtype
+    if dtype != _BF16 and dtype != _F32:
+        raise ValueError("rows must be bf16 or fp32")
+    views, outs, used = [None, None], [None, None], [positions]
+    for i, (t, o) in enumerate(((q, out_q), (k, out_k))):
         if t is None:
-            views.append(None)
-            outs.append(None)
             continue
-        o = torch.empty(t.shape, dtype=dtype, device=t.device) if o is None else o
-        for x in (t, o):
-            _require(x.dim() == 4 and x.shape == t.shape and (x.shape[0], x.shape[2], x.shape[3]) == (B, S, D)
-                     and x.dtype == dtype and x.is_cuda and x.stride(3) == 1,
-                     "rows must be [B, H, S, D] of one dtype with D contiguous")
-        _distinct_memory(o, "out")
-        outs.append(o)
-        views.append(RopeRows(t.data_ptr(), o.data_ptr(), t.stride(0), t.stride(1), t.stride(2), o.stride(0),
-                              o.stride(1), o.stride(2), t.shape[1]))
-    _require(positions.dim() == 3 and tuple(positions.shape[1:]) == (B, S) and positions.dtype == _I32
-             and (S <= 1 or positions.stride(2) == 1), "positions must be int32 [n_axes, B, S]")
+        if o is None:
+            o = torch.empty(t.shape, dtype=dtype, device=t.device)
+        else:
+            _distinct_memory(o, "out")
+        st, so, shape = t.stride(), o.stride(), t.shape
+        if (len(shape) != 4 or o.shape != shape or shape[0] != B or shape[2] != S or shape[3] != D or t.dtype != dtype
+                or o.dtype != dtype or st[3] != 1 or so[3] != 1):
+            raise ValueError("rows must be [B, H, S, D] of one dtype with D contiguous")
+        views[i] = _ROWS.pack(t.data_ptr(), o.data_ptr(), st[0], st[1], st[2], so[0], so[1], so[2], shape[1])
+        outs[i] = o
+        used += (t, o)
+    if positions.dim() != 3 or positions.dtype != _I32 or positions.shape[1] != B or positions.shape[2] != S:
+        raise ValueError("positions must be int32 [n_axes, B, S]")
+    sp = positions.stride()
+    if S > 1 and sp[2] != 1:
+        raise ValueError("positions must be contiguous along S")
     inv_freq, axes = _plan(inv_freq, axes, D)
-    dev = _one_device("rope_axes", positions, *given, *[o for o in outs if o is not None])
-    with _on(dev):
-        st = lib.rope_axes(*(None if v is None else ctypes.addressof(v) for v in views), positions.data_ptr(),
-                           positions.stride(0), positions.stride(1), positions.shape[0], inv_freq.data_ptr(),
-                           axes.data_ptr(), B, S, D, ATTN_F32 if dtype == torch.float32 else ATTN_BF16,
-                           int(bool(interleaved)), int(inverse), _stream_handle(dev))
-    _check(st, "rope_axes")
+    dev = _one_device("rope_axes", *used)
+    _call(lib.rope_axes, "rope_axes", dev, views[0], views[1], positions.data_ptr(), sp[0], sp[1], positions.shape[0],
+          inv_freq.data_ptr(), axes.data_ptr(), B, S, D, ATTN_F32 if dtype == _F32 else ATTN_BF16,
+          1 if interleaved else 0, inverse)
     return outs[0], outs[1]
 
 
@@ -237,42 +262,40 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     [n_axes,total], inv_freq and axes as for rope_axes) k is turned on the way,
     and q [Hq,total,D] into out_q (may be q), which is returned. Tokens whose slot
     is on no page are dropped."""
-    view = _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens)
-    _require(k.dim() == 3, "expected k [Hkv, total, D]")
-    total, D = k.shape[1], view.D
-    _require(q is None or positions is not None, "q is turned by positions: pass them")
-    rows = []
-    for t, H in ((k, view.Hkv), (v, view.Hkv), (q, None)):
-        if t is None:
-            continue
-        _packed(t, total, D, _BF16, "new tokens")
-        _require(H is None or t.shape[0] == H, "k and v must have the cache's heads")
-        rows.append(t)
-    vq = None
+    view, dev, _, Hkv, D = _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens)
+    if k.dim() != 3:
+        raise ValueError("expected k [Hkv, total, D]")
+    if q is not None and positions is None:
+        raise ValueError("q is turned by positions: pass them")
+    total = k.shape[1]
+    sk, sv = _packed(k, total, D, "k"), _packed(v, total, D, "v")
+    if k.shape[0] != Hkv or v.shape[0] != Hkv:
+        raise ValueError("k and v must have the cache's heads")
+    used, vq = [k_pages, k, v], None
     if q is not None:
-        out_q = torch.empty(q.shape, dtype=_BF16, device=q.device) if out_q is None else out_q
-        _packed(out_q, total, D, _BF16, "out_q")
-        _require(out_q.shape == q.shape, "bad out_q")
-        _distinct_memory(out_q, "out_q")
-        rows.append(out_q)
-        vq = RopeRows(q.data_ptr(), out_q.data_ptr(), 0, q.stride(0), q.stride(1), 0, out_q.stride(0), out_q.stride(1),
-                      q.shape[0])
-    vk = RopeRows(k.data_ptr(), None, 0, k.stride(0), k.stride(1), 0, 0, 0, view.Hkv)
-    vv = RopeRows(v.data_ptr(), None, 0, v.stride(0), v.stride(1), 0, 0, 0, view.Hkv)
+        sq = _packed(q, total, D, "q")
+        if out_q is None:
+            out_q = torch.empty(q.shape, dtype=_BF16, device=q.device)
+        else:
+            _distinct_memory(out_q, "out_q")
+        so = _packed(out_q, total, D, "out_q")
+        if out_q.shape != q.shape:
+            raise ValueError("bad out_q")
+        used += (q, out_q)
+        vq = _ROWS.pack(q.data_ptr(), out_q.data_ptr(), 0, sq[0], sq[1], 0, so[0], so[1], q.shape[0])
     pos, pos_axis, n_axes, f, a = None, 0, 0, None, None
     if positions is not None:
-        _require(positions.dim() == 2 and positions.shape[1] == total and positions.dtype == _I32
-                 and (total <= 1 or positions.stride(1) == 1), "positions must be int32 [n_axes, total]")
+        if positions.dim() != 2 or positions.dtype != _I32 or positions.shape[1] != total or (
+                total > 1 and positions.stride(1) != 1):
+            raise ValueError("positions must be int32 [n_axes, total]")
         inv_freq, axes = _plan(inv_freq, axes, D)
-        pos, pos_axis, n_axes, f, a = (positions.data_ptr(), positions.stride(0), positions.shape[0],
-                                       inv_freq.data_ptr(), axes.data_ptr())
-        rows.append(positions)
-    dev = _one_device("paged_append", k_pages, *rows)
-    with _on(dev):
-        st = lib.paged_append(None if vq is None else ctypes.addressof(vq), ctypes.addressof(vk), ctypes.addressof(vv),
-                              ctypes.addressof(view), pos, pos_axis, n_axes, f, a, total, int(bool(interleaved)),
-                              _stream_handle(dev))
-    _check(st, "paged_append")
+        pos, pos_axis, n_axes = positions.data_ptr(), positions.stride(0), positions.shape[0]
+        f, a = inv_freq.data_ptr(), axes.data_ptr()
+        used.append(positions)
+    _one_device("paged_append", *used)
+    _call(lib.paged_append, "paged_append", dev, vq, _ROWS.pack(k.data_ptr(), 0, 0, sk[0], sk[1], 0, 0, 0, Hkv),
+          _ROWS.pack(v.data_ptr(), 0, 0, sv[0], sv[1], 0, 0, 0, Hkv), view, pos, pos_axis, n_axes, f, a, total,
+          1 if interleaved else 0)
     return out_q
 
 
@@ -281,14 +304,18 @@ def _pools(pools, n_pages: int):
     pools = (pools,) if isinstance(pools, torch.Tensor) else tuple(pools)
     arr = (PagedPool * max(len(pools), 1))()
     for i, t in enumerate(pools):
-        _require(t.dim() in (4, 5) and t.shape[-4] == n_pages, "pools must be [(L,) n_pages, Hkv, page_size, D]")
-        layers = t if t.dim() == 5 else t[None]
-        _require(layers.numel() == 0 or layers[0, 0].is_contiguous(), "pages must be contiguous")
+        shape, s = tuple(t.shape), t.stride()
+        if len(shape) == 4:
+            shape, s = (1, *shape), (0, *s)
+        if len(shape) != 5 or shape[1] != n_pages:
+            raise ValueError("pools must be [(L,) n_pages, Hkv, page_size, D]")
+        _, _, h, r, d = shape
+        if (d > 1 and s[4] != 1) or (r > 1 and s[3] != d) or (h > 1 and s[2] != r * d):
+            raise ValueError("pools must have contiguous pages")
         _distinct_memory(t, "pools")
-        size = t.element_size()
-        page = layers.shape[2] * layers.shape[3] * layers.shape[4]
-        arr[i] = PagedPool(t.data_ptr(), (layers.stride(0) if layers.shape[0] > 1 else 0) * size,
-                           (layers.stride(1) if n_pages > 1 else page) * size, page * size, layers.shape[0])
+        size, page = t.element_size(), h * r * d
+        arr[i] = PagedPool(t.data_ptr(), (s[0] if shape[0] > 1 else 0) * size, (s[1] if n_pages > 1 else page) * size,
+                           page * size, shape[0])
     return pools, arr
 
 
@@ -298,30 +325,24 @@ def paged_reserve(page_table: torch.Tensor, kv_lens: torch.Tensor, page_refs: to
     lowest free pages (page_refs 0) in the order of the rows; kv_lens grows by
     n_new. Returns status int32 [B]: 0, PAGED_NO_PAGES or PAGED_TOO_LONG (that row
     unchanged)."""
-    _tables(page_table, kv_lens, page_refs)
-    B, W = page_table.shape
-    _ints(n_new, (B,), "n_new")
-    status = torch.empty(B, dtype=_I32, device=page_table.device) if status is None else status
-    _ints(status, (B,), "status")
+    B, W, row = _tables(page_table, kv_lens, page_refs)
+    _ints(n_new, B, "n_new")
+    if status is None:
+        status = torch.empty(B, dtype=_I32, device=page_table.device)
+    _ints(status, B, "status")
     dev = _one_device("paged_reserve", page_table, kv_lens, page_refs, n_new, status)
-    with _on(dev):
-        st = lib.paged_reserve(page_table.data_ptr(), _table_stride(page_table), kv_lens.data_ptr(), page_refs.data_ptr(),
-                               n_new.data_ptr(), status.data_ptr(), B, W, page_refs.numel(), int(page_size),
-                               _stream_handle(dev))
-    _check(st, "paged_reserve")
+    _call(lib.paged_reserve, "paged_reserve", dev, page_table.data_ptr(), row, kv_lens.data_ptr(), page_refs.data_ptr(),
+          n_new.data_ptr(), status.data_ptr(), B, W, page_refs.numel(), int(page_size))
     return status
 
 
 def paged_free(page_table: torch.Tensor, kv_lens: torch.Tensor, page_refs: torch.Tensor, rows) -> None:
     """The listed rows give up their pages (a page that no row holds any more is free) and become empty."""
     rows = _host_ints(rows, "rows")
-    _tables(page_table, kv_lens, page_refs)
-    B, W = page_table.shape
+    B, W, row = _tables(page_table, kv_lens, page_refs)
     dev = _one_device("paged_free", page_table, kv_lens, page_refs)
-    with _on(dev):
-        st = lib.paged_free(page_table.data_ptr(), _table_stride(page_table), kv_lens.data_ptr(), page_refs.data_ptr(),
-                            rows.data_ptr(), rows.numel(), B, W, page_refs.numel(), _stream_handle(dev))
-    _check(st, "paged_free")
+    _call(lib.paged_free, "paged_free", dev, page_table.data_ptr(), row, kv_lens.data_ptr(), page_refs.data_ptr(),
+          rows.data_ptr(), rows.numel(), B, W, page_refs.numel())
 
 
 def paged_fork(pools, page_table: torch.Tensor, kv_lens: torch.Tensor, page_refs: torch.Tensor, src, dst,
@@ -330,21 +351,20 @@ def paged_fork(pools, page_table: torch.Tensor, kv_lens: torch.Tensor, page_refs
     a partly filled last page copied in every pool. Returns status int32 [n]: 0,
     PAGED_NO_PAGES or PAGED_IN_USE (that row unchanged)."""
     src, dst = _host_ints(src, "src"), _host_ints(dst, "dst")
-    _require(src.numel() == dst.numel(), "src and dst must have one length")
-    _tables(page_table, kv_lens, page_refs)
-    B, W = page_table.shape
+    n = src.numel()
+    _require(dst.numel() == n, "src and dst must have one length")
+    B, W, row = _tables(page_table, kv_lens, page_refs)
     pools, arr = _pools(pools, page_refs.numel())
     if page_size is None:
         _require(len(pools) > 0 and len({t.shape[-2] for t in pools}) == 1, "pools of one page size, or page_size, needed")
         page_size = pools[0].shape[-2]
-    status = torch.empty(src.numel(), dtype=_I32, device=page_table.device) if status is None else status
-    _ints(status, (src.numel(),), "status")
+    if status is None:
+        status = torch.empty(n, dtype=_I32, device=page_table.device)
+    _ints(status, n, "status")
     dev = _one_device("paged_fork", page_table, kv_lens, page_refs, status, *pools)
-    with _on(dev):
-        st = lib.paged_fork(ctypes.addressof(arr), len(pools), page_table.data_ptr(), _table_stride(page_table),
-                            kv_lens.data_ptr(), page_refs.data_ptr(), src.data_ptr(), dst.data_ptr(), status.data_ptr(),
-                            src.numel(), B, W, page_refs.numel(), int(page_size), _stream_handle(dev))
-    _check(st, "paged_fork")
+    _call(lib.paged_fork, "paged_fork", dev, arr, len(pools), page_table.data_ptr(), row, kv_lens.data_ptr(),
+          page_refs.data_ptr(), src.data_ptr(), dst.data_ptr(), status.data_ptr(), n, B, W, page_refs.numel(),
+          int(page_size))
     return status
 
 
@@ -352,14 +372,12 @@ def paged_copy(pools, src, dst) -> None:
     """Page dst[i] becomes a copy of page src[i] in every pool (dst distinct, none in src)."""
     src, dst = _host_ints(src, "src"), _host_ints(dst, "dst")
     _require(src.numel() == dst.numel(), "src and dst must have one length")
-    first = pools if isinstance(pools, torch.Tensor) else pools[0]
-    n_pages = first.shape[-4]
+    pools = (pools,) if isinstance(pools, torch.Tensor) else tuple(pools)
+    _require(len(pools) > 0 and pools[0].dim() in (4, 5), "pools must be [(L,) n_pages, Hkv, page_size, D]")
+    n_pages = pools[0].shape[-4]
     pools, arr = _pools(pools, n_pages)
     dev = _one_device("paged_copy", *pools)
-    with _on(dev):
-        st = lib.paged_copy(ctypes.addressof(arr), len(pools), src.data_ptr(), dst.data_ptr(), src.numel(), n_pages,
-                            _stream_handle(dev))
-    _check(st, "paged_copy")
+    _call(lib.paged_copy, "paged_copy", dev, arr, len(pools), src.data_ptr(), dst.data_ptr(), src.numel(), n_pages)
 
 
 def paged_compact(pools, page_table: torch.Tensor, page_refs: torch.Tensor, out_table: torch.Tensor | None = None,
@@ -367,26 +385,22 @@ def paged_compact(pools, page_table: torch.Tensor, page_refs: torch.Tensor, out_
     """Moves the live pages to ids 0 .. n_live - 1 (the highest ids into the lowest
     free ones, both ascending); table and references follow, in place unless
     out_table / out_refs are given. Returns n_live, int32 [1] on the device."""
-    _tables(page_table, None, page_refs)
-    B, W = page_table.shape
+    B, W, row = _tables(page_table, None, page_refs)
     out_table = page_table if out_table is None else out_table
     out_refs = page_refs if out_refs is None else out_refs
-    _tables(out_table, None, out_refs)
-    _require(out_table.shape == page_table.shape and _table_stride(out_table) == _table_stride(page_table)
-             and out_refs.shape == page_refs.shape, "out_table and out_refs must be shaped like the inputs")
-    n_live = torch.empty(1, dtype=_I32, device=page_table.device) if n_live is None else n_live
-    _ints(n_live, (1,), "n_live")
+    _require(_tables(out_table, None, out_refs) == (B, W, row) and out_refs.numel() == page_refs.numel(),
+             "out_table and out_refs must be shaped like the inputs")
+    if n_live is None:
+        n_live = torch.empty(1, dtype=_I32, device=page_table.device)
+    _ints(n_live, 1, "n_live")
     n_pages = page_refs.numel()
     pools, arr = _pools(pools, n_pages)
     need = lib.paged_compact_workspace_bytes(n_pages)
     _require(need > 0, "too many pages")
     workspace = torch.empty(need, dtype=torch.uint8, device=page_table.device)
     dev = _one_device("paged_compact", page_table, page_refs, out_table, out_refs, n_live, *pools)
-    with _on(dev):
-        st = lib.paged_compact(ctypes.addressof(arr), len(pools), page_table.data_ptr(), out_table.data_ptr(),
-                               _table_stride(page_table), page_refs.data_ptr(), out_refs.data_ptr(), n_live.data_ptr(),
-                               workspace.data_ptr(), need, B, W, n_pages, _stream_handle(dev))
-    _check(st, "paged_compact")
+    _call(lib.paged_compact, "paged_compact", dev, arr, len(pools), page_table.data_ptr(), out_table.data_ptr(), row,
+          page_refs.data_ptr(), out_refs.data_ptr(), n_live.data_ptr(), workspace.data_ptr(), need, B, W, n_pages)
     return n_live
 
 

@@ -59,6 +59,7 @@ def test_attn_paged_refusals(lib):
     assert run(D=96) == 2 and run(D=256) == 2
     assert run(page_size=8) == 2 and run(page_size=24) == 2 and run(page_size=0) == 1
     assert run(max_pages=1 << 27, table_stride=1 << 27) == 2  # more than 2^30 keys
+    assert run(total=1 << 29, wb=1 << 40, B=4096, max_pages=1 << 26, table_stride=1 << 26) == 2  # key tiles past 2^31
     assert run(B=5000) == 2 and run(Hq=512) == 2  # too many sequences; more than 128 heads in a group
     assert run(Hq=3) == 1 and run(causal=2) == 1 and run(scale=0.0) == 1 and run(scale=float("inf")) == 1
     assert run(page_stride=16 * 128) == 1 and run(page_stride=2 * 16 * 128 + 4) == 1 and run(table_stride=7) == 1
@@ -73,7 +74,7 @@ def test_attn_paged_refusals(lib):
 
 def test_attn_paged_workspace(lib):
     up = lambda n: (n + 255) // 256 * 256
-    want = lambda rows, D: up(320 * rows * D * 4) + up(320 * rows * 4)
+    want = lambda rows, D: up(320 * rows * D * 4) + up(320 * rows * 4) + up(160 * 16)
     assert lib.attn_paged_workspace_bytes(28, 4, 1, 128) == want(7, 128)       # one token: a group's rows
     assert lib.attn_paged_workspace_bytes(28, 4, 10 ** 6, 128) == want(252, 128)  # two tiles of 18 tokens
     assert lib.attn_paged_workspace_bytes(8, 8, 10 ** 6, 64) == want(256, 64)
