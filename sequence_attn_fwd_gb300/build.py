@@ -23,7 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libseqattn.so")
 SOURCES = ["attn_kernel.cu", "lse_merge.cu", "rope.cu", "pages.cu", "api.cu", "api_paged.cu"]
-HEADERS = ["ptx.cuh", "kernels.h", "attn_common.cuh", "attn_bwd.cuh", "attn_paged.cuh"]
+HEADERS = ["ptx.cuh", "kernels.h", "attn_common.cuh", "attn_bwd.cuh", "attn_paged.cuh", "attn_paged_narrow.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -113,7 +113,7 @@ int make_table(seqattn::RopeTable *t, const double *inv_freq, const int *axes, i
 
 int check_tables(const int *page_table, long long table_stride, int B, int max_pages, int n_pages) {
   if (B < 0 || max_pages < 0 || n_pages <= 0 || table_stride < max_pages) return ATTN_ERR_INVALID_ARG;
-  if (B > seqattn::kPagedMaxSeqs || static_cast<long long>(B) * max_pages > 0x7fffffffll || n_pages > (1 << 28))
+  if (B > seqattn::kPagedMaxRows || static_cast<long long>(B) * max_pages > 0x7fffffffll || n_pages > (1 << 28))
     return ATTN_ERR_UNSUPPORTED;
   if (B > 0 && max_pages > 0 && (!page_table || !aligned(page_table, 4))) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
@@ -183,8 +183,8 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
   const cuuint64_t uD = static_cast<cuuint64_t>(D);
   const cuuint64_t qh = Hq > 1 ? static_cast<cuuint64_t>(q_head_stride) : uD;
   const cuuint64_t qs = total_q > 1 ? static_cast<cuuint64_t>(q_row_stride) : uD;
-  const int tok = 128 / G, tok32 = 32 / G;
-  CUtensorMap tq, tq32, tk, tv;
+  const int tok = 128 / G;
+  CUtensorMap tq, tqn[3], tk, tv;
   const cuuint64_t q_dims[4] = {uD, static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(total_q),
                                 static_cast<cuuint64_t>(cache->Hkv)};
   const cuuint64_t q_strides[3] = {qh * 2, qs * 2, qh * 2 * G};
@@ -192,8 +192,11 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
                                  static_cast<cuuint64_t>(cache->n_pages)};
   const cuuint64_t kv_strides[3] = {uD * 2, uD * 2 * cache->page_size, static_cast<cuuint64_t>(cache->page_stride) * 2};
   const unsigned box_rows = cache->page_size < 128 ? cache->page_size : 128;
+  for (int i = 0; i < 3; ++i) {
+    const int few = (16 << i) / G;
+    if (!make_map_4d(&tqn[i], q, q_dims, q_strides, G, few > 0 ? few : 1)) return keep_cuda_error(cudaErrorInvalidValue);
+  }
   if (!make_map_4d(&tq, q, q_dims, q_strides, G, tok) ||
-      !make_map_4d(&tq32, q, q_dims, q_strides, G, tok32 > 0 ? tok32 : 1) ||
       !make_map_4d(&tk, cache->k_pages, kv_dims, kv_strides, box_rows, 1) ||
       !make_map_4d(&tv, cache->v_pages, kv_dims, kv_strides, box_rows, 1))
     return keep_cuda_error(cudaErrorInvalidValue);
@@ -211,12 +214,11 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
   p.Hq = Hq;
   p.G = G;
   p.tok = tok;
-  p.tok32 = tok32;
   p.total_q = total_q;
   p.causal = causal;
   p.page_log2 = log2_of(cache->page_size);
   p.scale_log2 = scale * 1.4426950408889634f;
-  return done(seqattn::launch_attn_paged(D, tq, tq32, tk, tv, p, reinterpret_cast<cudaStream_t>(stream)));
+  return done(seqattn::launch_attn_paged(D, tq, tqn, tk, tv, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int rope_axes(const rope_rows *q, const rope_rows *k, const int *positions, long long pos_axis, long long pos_b,
@@ -296,7 +298,7 @@ int paged_free(int *page_table, long long table_stride, int *kv_lens, int *page_
   if (n < 0 || (n > 0 && !rows)) return ATTN_ERR_INVALID_ARG;
   if (n == 0) return ATTN_OK;
   if (!kv_lens || !page_refs || !aligned(kv_lens, 4) || !aligned(page_refs, 4)) return ATTN_ERR_INVALID_ARG;
-  bool seen[seqattn::kPagedMaxSeqs] = {};
+  bool seen[seqattn::kPagedMaxRows] = {};
   for (int i = 0; i < n; ++i) {
     if (rows[i] < 0 || rows[i] >= B || seen[rows[i]]) return ATTN_ERR_INVALID_ARG;
     seen[rows[i]] = true;
@@ -325,7 +327,7 @@ int paged_fork(const paged_pool *pools, int n_pools, int *page_table, long long 
   if (n == 0) return ATTN_OK;
   if (!kv_lens || !page_refs || !status || !aligned(kv_lens, 4) || !aligned(page_refs, 4) || !aligned(status, 4))
     return ATTN_ERR_INVALID_ARG;
-  bool target[seqattn::kPagedMaxSeqs] = {};
+  bool target[seqattn::kPagedMaxRows] = {};
   for (int i = 0; i < n; ++i) {
     if (src[i] < 0 || src[i] >= B || dst[i] < 0 || dst[i] >= B || target[dst[i]]) return ATTN_ERR_INVALID_ARG;
     target[dst[i]] = true;

@@ -24,14 +24,9 @@
 // tile. The producer reads the page table, one lane per page of a key tile
 // (128 / page_size boxes, or one box inside a larger page).
 //
-// Few rows (at most 64 of a KV head: single tokens, drafts). Reading a key tile
-// takes about 2,800 clocks of one SM's share of the DRAM rate (D = 128), so the
-// chain S, softmax, P V of one tile after the other must stay below that. A
-// row of 128 scores per thread does not (about 4,200 clocks measured). So each
-// tile holds its at most 32 rows four times, and warp w of its warpgroup takes
-// the 32 keys 32 w .. of its copy as an attention of their own -- reference,
-// sum and O rows -- with P zero for the other keys; the four copies are merged
-// in the epilogue. The products cost the same, the softmax a quarter.
+// This is the wide form. When no sequence of the call has more than 64 rows per
+// KV head, the launch takes the narrow form (attn_paged_narrow.cuh) on the same
+// ranges: every CTA finds that out for itself, along with its range.
 #pragma once
 
 namespace seqattn {
@@ -48,9 +43,14 @@ struct Cfg {
   static constexpr int kTileBytes = kRowsPerTile * D * 2;
   static constexpr int kStages = 131072 / kTileBytes;
   static constexpr int kNumBarriers = 2 + 2 * kStages + 7;
-  static constexpr int kStageBytes = 8192;  // of each tile: four copies x 16 columns x 32 rows, fp32
-  static constexpr int kSmemBytes = 1024 + 2 * kTileBytes + kStages * kTileBytes + 2 * kStageBytes + 8 * kNumBarriers +
-                                    16 + 4 * 12 + 4 * (kPagedMaxSeqs + 1);
+  // tiles of the wide form (Q, ring) or of the narrow one (ring, P, Q), then
+  // barriers, three words, warp sums, the narrow form's reductions, prefix sums
+  static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 2 * 16 * D * 2;
+  static_assert(2 * kTileBytes + kStages * kTileBytes <= kAreaBytes, "wide layout");
+  static constexpr int kMaxBarriers = 2 * (196608 / kTileBytes) + 10;
+  static constexpr int kRedFloats = 2 * 4 * 32;
+  static constexpr int kSmemBytes =
+      1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 24 + 4 * kRedFloats + 4 * (kPagedMaxSeqs + 1);
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -113,14 +113,16 @@ __device__ __forceinline__ long long tiles_before(const PagedAttnParams &p, cons
 }
 
 // prefix[0 .. B]: key tiles of all KV heads of the sequences before each, by
-// every thread of the CTA; warp_sums has 12 entries.
-__device__ __forceinline__ void prefix_tiles(const PagedAttnParams &p, int *prefix, int *warp_sums) {
+// every thread of the CTA; returns the most new tokens of a sequence. warp_sums
+// has 24 entries.
+__device__ __forceinline__ int prefix_tiles(const PagedAttnParams &p, int *prefix, int *warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int B = p.cache.B, per = (B + blockDim.x - 1) / blockDim.x;
   const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
-  int sum = 0;
+  int sum = 0, most = 0;
   for (int b = b0; b < b1; ++b) {
     const Seq s = sequence(p, b);
+    most = max(most, s.q_len);
     prefix[b] = sum;
     if (s.q_len > 0) sum += static_cast<int>(tiles_before(p, s, row_blocks(p, s))) * p.cache.Hkv;
   }
@@ -130,13 +132,19 @@ __device__ __forceinline__ void prefix_tiles(const PagedAttnParams &p, int *pref
     const int y = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += y;
   }
-  if (lane == 31) warp_sums[warp] = incl;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    warp_sums[warp] = incl;
+    warp_sums[12 + warp] = most;
+  }
   __syncthreads();
   int base = incl - sum;
   for (int i = 0; i < warp; ++i) base += warp_sums[i];
+  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) most = max(most, warp_sums[12 + i]);
   for (int b = b0; b < b1; ++b) prefix[b] += base;
   if (threadIdx.x == blockDim.x - 1) prefix[B] = base + sum;
   __syncthreads();
+  return most;
 }
 
 // The sequence whose range of tiles has `pos`.
@@ -177,10 +185,8 @@ struct Segment {
   Seq s;
   int b, h, rb, j0, j1;
   int slot;  // partial written, -1: the whole item, written directly
-  int tok;   // tokens of each of the two tiles
   int last_cta;  // the CTA that has the item's last tile
 };
-__device__ __forceinline__ bool few_rows(const PagedAttnParams &p, const Segment &g) { return g.tok != p.tok; }
 __device__ __forceinline__ const int *page_row(const PagedAttnParams &p, const Segment &g) {
   return p.cache.page_table + g.b * p.cache.table_stride;
 }
@@ -226,16 +232,15 @@ struct Walk {
     g.j0 = at.r;
     g.j1 = min(n, at.r + (end - pos));
     g.slot = g.j0 == 0 && g.j1 == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (g.j0 == 0 ? 1 : 0);
-    g.tok = g.s.q_len <= 2 * p.tok32 ? p.tok32 : p.tok;
     g.last_cta = (pos - g.j0 + n - 1) / per;
     pos += g.j1 - g.j0;
     return true;
   }
   // Key tiles of segment g that query tile t goes through, counted from g.j0.
   static __device__ __forceinline__ int tiles(const PagedAttnParams &p, const Segment &g, int t) {
-    const int first = (2 * g.rb + t) * g.tok;
+    const int first = (2 * g.rb + t) * p.tok;
     if (first >= g.s.q_len) return 0;
-    return max(0, min(g.j1, tiles_seen(p, g.s, first + g.tok)) - g.j0);
+    return max(0, min(g.j1, tiles_seen(p, g.s, first + p.tok)) - g.j0);
   }
 };
 
@@ -261,19 +266,16 @@ struct PageBits {
 };
 
 // V slots past kv_len may hold anything, NaN too, and 0 * NaN would reach O:
-// they are zeroed in shared memory before the product reads them. `cv` is the
-// ring position of the V tile; its slot stays the tile's until both issuers
-// have used it.
+// they are zeroed in shared memory, by the 128 threads of a warpgroup, before
+// the product reads them. The tile (at shared address v, its barrier and phase
+// given) stays until the products that use it are done.
 template <int D>
-__device__ __forceinline__ bool clear_tail(int valid_keys, int cv, uint32_t bar_full0, uint32_t ring_base,
+__device__ __forceinline__ bool clear_tail(int valid_keys, uint32_t v, uint32_t bar_full, uint32_t phase,
                                            volatile int *abort_flag, int *err) {
-  using C = Cfg<D>;
-  const int slot = cv % C::kStages;
-  if (!__all_sync(0xffffffffu, mbar_wait(bar_full0 + 8u * slot, (cv / C::kStages) & 1, abort_flag, err))) return false;
+  if (!__all_sync(0xffffffffu, mbar_wait(bar_full, phase, abort_flag, err))) return false;
   const int pieces = (kRowsPerTile - valid_keys) * 8;  // 16-byte pieces of a 128-byte column block
-  for (int i = threadIdx.x & 127; i < pieces * C::kColBlocks; i += 128)
-    st_shared_v4(ring_base + slot * C::kTileBytes + (i / pieces) * kColBlockBytes + valid_keys * 128 + (i % pieces) * 16,
-                 0u, 0u, 0u, 0u);
+  for (int i = threadIdx.x & 127; i < pieces * (D / 64); i += 128)
+    st_shared_v4(v + (i / pieces) * kColBlockBytes + valid_keys * 128 + (i % pieces) * 16, 0u, 0u, 0u, 0u);
   fence_proxy_async_shared();
   return true;
 }
@@ -297,7 +299,7 @@ __device__ __forceinline__ void scale_o(uint32_t o_addr, float alpha) {
 // row, TMEM lane = tile row; the dense forward's scheme). `ring` is the ring
 // position of the segment's first K tile.
 template <int D>
-__device__ __noinline__ bool softmax_segment(const PagedAttnParams &p, const Segment &g, int t, int n, int r,
+__device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const Segment &g, int t, int n, int r,
                                                 uint32_t s_addr, uint32_t o_addr, uint32_t bar_sfull,
                                                 uint32_t bar_pfull, uint32_t bar_ofull, uint32_t bar_full0,
                                                 uint32_t ring_base, int ring, int step_base, uint32_t ofull_parity,
@@ -378,7 +380,9 @@ __device__ __noinline__ bool softmax_segment(const PagedAttnParams &p, const Seg
       tmem_st_wait();
     }
     if (g.s.kv_len - kv0 < kRowsPerTile) {
-      ok = clear_tail<D>(g.s.kv_len - kv0, ring + 2 * j + 1, bar_full0, ring_base, abort_flag, err);
+      const int cv = ring + 2 * j + 1, slot = cv % Cfg<D>::kStages;  // ring position of the V tile
+      ok = clear_tail<D>(g.s.kv_len - kv0, ring_base + slot * Cfg<D>::kTileBytes, bar_full0 + 8u * slot,
+                         (cv / Cfg<D>::kStages) & 1, abort_flag, err);
       if (!ok) break;
     }
     tc_fence_before();
@@ -449,160 +453,6 @@ __device__ __noinline__ bool softmax_segment(const PagedAttnParams &p, const Seg
   return done;
 }
 
-// The same for a tile of at most 32 rows held four times: warp w of the
-// warpgroup takes keys 32 w .. 32 w + 31 of each tile for the rows of its copy
-// (lane = row), the copies are merged at the end through `stage` (this tile's
-// 8 KB of shared memory).
-template <int D>
-__device__ __noinline__ bool few_rows_segment(const PagedAttnParams &p, const Segment &g, int t, int n, int w,
-                                                 uint32_t s_addr, uint32_t o_addr, uint32_t bar_sfull,
-                                                 uint32_t bar_pfull, uint32_t bar_ofull, uint32_t bar_full0,
-                                                 uint32_t ring_base, int ring, int step_base, uint32_t ofull_parity,
-                                                 float *stage, volatile int *abort_flag, int *err) {
-  const int lane = threadIdx.x & 31;
-  const int tok = t * g.tok + lane / p.G;
-  const bool row_valid = lane < g.tok * p.G && tok < g.s.q_len;
-  if (t * g.tok >= g.s.q_len) return true;  // no row of this tile: n is 0 too
-  // last key seen, counted from this warp's first one
-  const int row_last = (!row_valid ? -1 : (p.causal ? g.s.kv_len - g.s.q_len + tok : g.s.kv_len - 1)) - 32 * w;
-  const float c2 = p.scale_log2;
-  PageBits bits(p);
-  float m = -INFINITY, l = 0.f;
-  bool ok = true;
-  if (n > 0) bits.look_up(p, g, g.j0);
-  for (int j = 0; j < n; ++j) {
-    const unsigned now = bits.mask(p);
-    if (j + 1 < n) bits.look_up(p, g, g.j0 + j + 1);
-    ok = __all_sync(0xffffffffu, mbar_wait(bar_sfull, static_cast<uint32_t>(step_base + j) & 1u, abort_flag, err));
-    if (!ok) break;
-    tc_fence_after();
-    const int kv0 = (g.j0 + j) * kRowsPerTile;
-    uint32_t x[32];
-    // the scores times scale log2(e), masked
-    auto load_scores = [&] {
-      tmem_ld32(s_addr + 32 * w, x);
-      tmem_ld_wait(x);
-      const int last = row_last - kv0;
-      if (__any_sync(0xffffffffu, row_valid && last < 31)) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (c > last) x[c] = __float_as_uint(-INFINITY);
-      }
-      if (now != 0xffffffffu) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (!((now >> (bits.per_tile == 1 ? 0 : (32 * w + c) >> p.page_log2)) & 1u))
-            x[c] = __float_as_uint(-INFINITY);
-      }
-      if (!row_valid) {  // rows of no token, other sequences' rows: nothing
-#pragma unroll
-        for (int c = 0; c < 32; ++c) x[c] = __float_as_uint(-INFINITY);
-      }
-    };
-    load_scores();
-    float top = __uint_as_float(x[0]);
-#pragma unroll
-    for (int c = 1; c < 31; c += 2) top = fmax3(top, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-    top = fmaxf(top, __uint_as_float(x[31])) * c2;
-    // the reference moves, and O with it, only when it would let a P above 2^8
-    // through or there is none yet
-    const bool move = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
-    if (__any_sync(0xffffffffu, move)) {
-      const float m_new = fmaxf(m, top);
-      const float alpha = (m_new == -INFINITY) ? 1.f : ex2_approx(m - m_new);
-      m = m_new;
-      l *= alpha;
-      if (j > 0) scale_o<D>(o_addr, alpha);
-    }
-    const float ref = (m == -INFINITY) ? 0.f : m;
-    uint32_t pk[16];
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const float a = ex2_approx(fmaf(__uint_as_float(x[2 * c]), c2, -ref));
-      const float b = ex2_approx(fmaf(__uint_as_float(x[2 * c + 1]), c2, -ref));
-      s0 += a;
-      s1 += b;
-      // P enters the tensor cores in bf16, as in the dense forward; l is summed before the rounding
-      __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-      pk[c] = *reinterpret_cast<uint32_t *>(&h);
-    }
-    l += s0 + s1;
-    const uint32_t none[16] = {};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (q == w) tmem_st16(s_addr + 16 * q, pk);
-      else tmem_st16(s_addr + 16 * q, none);
-    }
-    tmem_st_wait();
-    if (g.s.kv_len - kv0 < kRowsPerTile) {
-      ok = clear_tail<D>(g.s.kv_len - kv0, ring + 2 * j + 1, bar_full0, ring_base, abort_flag, err);
-      if (!ok) break;
-    }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_pfull);
-  }
-  bool have_o = false;
-  if (ok && n > 0) {
-    have_o = __all_sync(0xffffffffu, mbar_wait(bar_ofull, ofull_parity, abort_flag, err));
-    tc_fence_after();
-  }
-  const int id = 1 + t;
-  if (!named_bar_and(id, 128, ok && (n == 0 || have_o))) return false;
-  // weights of the four copies of each row
-  float2 *stats = reinterpret_cast<float2 *>(stage);
-  stats[32 * w + lane] = make_float2(m, l);
-  named_bar_sync(id, 128);
-  float top = -INFINITY, sum = 0.f;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) top = fmaxf(top, stats[32 * q + lane].x);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float2 v = stats[32 * q + lane];
-    if (v.y > 0.f) sum = fmaf(v.y, ex2_approx(v.x - top), sum);
-  }
-  const float mine = l > 0.f ? ex2_approx(m - top) / sum : 0.f;
-  const int head = g.h * p.G + lane % p.G;
-  const int row = g.s.q0 + tok;
-  const size_t part = static_cast<size_t>(max(g.slot, 0)) * p.part_rows + t * g.tok * p.G + lane;
-  if (w == 0 && row_valid) {
-    const float lse = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
-    if (g.slot >= 0) p.part_lse[part] = lse;
-    else if (p.lse) p.lse[static_cast<size_t>(head) * p.total_q + row] = lse;
-  }
-  // O, 16 columns at a time: every copy's share, then warp w sums columns 4 w ..
-#pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 16) {
-    uint32_t v[16];
-    if (have_o) {
-      tmem_ld16(o_addr + c0, v);
-      tmem_ld_wait(v);
-    }
-    named_bar_sync(id, 128);  // the stage has been read
-#pragma unroll
-    for (int i = 0; i < 16; ++i) stage[(16 * w + i) * 32 + lane] = mine > 0.f ? __uint_as_float(v[i]) * mine : 0.f;
-    named_bar_sync(id, 128);
-    float o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float *x = stage + (4 * w + i) * 32 + lane;
-      o[i] = (x[0] + x[16 * 32]) + (x[32 * 32] + x[48 * 32]);
-    }
-    if (row_valid) {
-      if (g.slot >= 0) {
-        *reinterpret_cast<float4 *>(p.part_o + part * D + c0 + 4 * w) = make_float4(o[0], o[1], o[2], o[3]);
-      } else {
-        __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h + row * p.o_s + c0 + 4 * w) =
-            make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
-      }
-    }
-  }
-  named_bar_sync(id, 128);  // before the next segment's stats
-  return true;
-}
-
 // Rows of the items that see no key at all (every row, if `all`): O = 0, lse = -inf.
 template <int D>
 __device__ void write_unseen(const PagedAttnParams &p, bool all, int tid, int nthreads) {
@@ -622,257 +472,331 @@ __device__ void write_unseen(const PagedAttnParams &p, bool all, int tid, int nt
   }
 }
 
+// ---------------------------------------------------------------- the wide form's roles
+template <int D>
+struct WideBars {
+  static constexpr int kStages = Cfg<D>::kStages;
+  static constexpr int kQFull = 0, kQEmpty = 1, kFull = 2, kEmpty = 2 + kStages, kSFull = 2 + 2 * kStages,
+                       kPFull = kSFull + 2, kOFull = kPFull + 2, kMmaDone = kOFull + 2;
+};
+// TMEM columns of S_t / P_t and of O_t
+__device__ __forceinline__ uint32_t s_column(uint32_t tmem, int t) { return tmem + 128u * static_cast<uint32_t>(t); }
+__device__ __forceinline__ uint32_t o_column(uint32_t tmem, int t) { return tmem + 256u + 128u * static_cast<uint32_t>(t); }
+
+// Producer: the whole warp. sQ [tile][col block][128 rows][128 B], sRing
+// [slot][col block][128 rows][128 B].
+template <int D>
+__device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, const int *prefix, const CUtensorMap *tm_q,
+                                           const CUtensorMap *tm_k, const CUtensorMap *tm_v, uint32_t bar0, uint32_t sQ,
+                                           uint32_t sRing, volatile int *abort_flag, int *err) {
+  using C = Cfg<D>;
+  using W = WideBars<D>;
+  const int lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  Segment g;
+  const uint64_t pol_q = l2_policy_evict_last(), pol_kv = l2_policy_evict_first();
+  const int page_size = 1 << p.page_log2;
+  const bool small = page_size < kRowsPerTile;
+  const int boxes = small ? kRowsPerTile >> p.page_log2 : 1;  // pages of a key tile
+  const uint32_t box_bytes = (small ? page_size : kRowsPerTile) * 128u;
+  int c = 0, nq = 0;
+  bool ok = true;
+  // the item that this CTA begins and another one ends, for the merge
+  int4 cut = make_int4(0, 0, 0, 0);
+  while (ok && walk.next(p, prefix, g)) {
+    if (g.j0 == 0 && g.slot >= 0)
+      cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, g.last_cta);
+    const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
+    const bool two = Walk::tiles(p, g, 1) > 0;
+    const int *row = page_row(p, g);
+    // the page of this lane for key tile j: n_pages (read as zeros) where there is none
+    auto page_of = [&](int j) -> int {
+      if (lane >= boxes) return 0;
+      const int i = small ? j * boxes + lane : (j * kRowsPerTile) >> p.page_log2;
+      int e = -1;
+      if ((i << p.page_log2) < g.s.kv_len) e = row[i];
+      return e >= 0 && e < p.cache.n_pages ? e : p.cache.n_pages;
+    };
+    int page = page_of(g.j0);
+    if (lane == 0) {
+      ok = nq == 0 || mbar_wait(bar(W::kQEmpty), (nq - 1) & 1, abort_flag, err);
+      if (ok) {
+        const uint32_t q_bytes = static_cast<uint32_t>(p.tok * p.G) * 128u * C::kColBlocks;
+        mbar_arrive_expect_tx(bar(W::kQFull), two ? 2 * q_bytes : q_bytes);
+        for (int t = 0; t < (two ? 2 : 1); ++t)
+          for (int cb = 0; cb < C::kColBlocks; ++cb)
+            tma_load_4d_hint(sQ + (t * C::kColBlocks + cb) * kColBlockBytes, tm_q, bar(W::kQFull), cb * 64, 0,
+                             g.s.q0 + (2 * g.rb + t) * p.tok, g.h, pol_q);
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    if (!ok) break;
+    ++nq;
+    for (int j = 0; j < n_max && ok; ++j) {
+      const int now = page;
+      if (j + 1 < n_max) page = page_of(g.j0 + j + 1);
+      const int in_page = small ? 0 : ((g.j0 + j) * kRowsPerTile) & (page_size - 1);
+      for (int which = 0; which < 2; ++which, ++c) {
+        const int slot = c % C::kStages;
+        if (lane == 0) {
+          ok = c < C::kStages || mbar_wait(bar(W::kEmpty + slot), ((c / C::kStages) - 1) & 1, abort_flag, err);
+          if (ok) mbar_arrive_expect_tx(bar(W::kFull + slot), C::kTileBytes);
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        if (lane < boxes) {
+          const CUtensorMap *map = which ? tm_v : tm_k;
+#pragma unroll
+          for (int cb = 0; cb < C::kColBlocks; ++cb)
+            tma_load_4d_hint(sRing + (slot * C::kColBlocks + cb) * kColBlockBytes + lane * box_bytes, map,
+                             bar(W::kFull + slot), cb * 64, in_page, g.h, now, pol_kv);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  if (lane == 0) p.cuts[blockIdx.x] = cut;
+  if (lane == 0) {  // every copy must have landed before the CTA may exit
+    if (nq > 0) mbar_drain(bar(W::kQFull), (nq - 1) & 1, err);
+    for (int i = max(0, c - C::kStages); i < c; ++i)
+      mbar_drain(bar(W::kFull + i % C::kStages), (i / C::kStages) & 1, err);
+  }
+  __syncwarp();
+}
+
+// MMA issuer of query tile t, one thread (the dense forward's scheme).
+template <int D>
+__device__ __noinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, const int *prefix, int t, uint32_t bar0,
+                                         uint32_t sQ, uint32_t sRing, uint32_t tmem, volatile int *turn,
+                                         volatile int *abort_flag, int *err) {
+  using C = Cfg<D>;
+  using W = WideBars<D>;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  Segment g;
+  constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, D, true);
+  constexpr int kKSteps = D / 16;
+  const uint32_t qt = sQ + t * C::kTileBytes, ring_base = sRing;
+  const uint32_t s_col = s_column(tmem, t), o_col = o_column(tmem, t);
+  int c = 0, nq = 0, steps = 0, base = 0;
+  bool ok = true;
+  while (ok && walk.next(p, prefix, g)) {
+    const int nt = Walk::tiles(p, g, t);
+    const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
+    // tile 1 has nothing to do: its issuer only gives Q back, and tile 0's
+    // goes on without taking turns and releases each slot for both
+    const bool single = Walk::tiles(p, g, 1) == 0;
+    if (!mbar_wait(bar(W::kQFull), nq & 1, abort_flag, err)) break;
+    ++nq;
+    if (nt == 0) mma_commit(bar(W::kQEmpty));
+    if (single && t == 1) {
+      c += 2 * n_max;
+      continue;
+    }
+    for (int j = 0; ok && j <= n_max; ++j) {
+      const int cK = c + 2 * j, cV = c + 2 * j - 1;
+      const int sK = cK % C::kStages, sV = (cV + C::kStages) % C::kStages;
+      const int cV2 = cK + 1, sV2 = cV2 % C::kStages;
+      const uint32_t k_base = ring_base + sK * C::kTileBytes, v_base = ring_base + sV * C::kTileBytes;
+      const bool has_pv = j >= 1 && j - 1 < nt, has_s = j < nt, unused = !has_s && j < n_max;
+      if ((has_s || unused) && !mbar_wait(bar(W::kFull + sK), (cK / C::kStages) & 1, abort_flag, err)) {
+        ok = false;
+        break;
+      }
+      if (unused && !mbar_wait(bar(W::kFull + sV2), (cV2 / C::kStages) & 1, abort_flag, err)) {
+        ok = false;
+        break;
+      }
+      if (has_pv && (!mbar_wait(bar(W::kFull + sV), (cV / C::kStages) & 1, abort_flag, err) ||
+                     !mbar_wait(bar(W::kPFull + t), (steps + j - 1) & 1, abort_flag, err))) {
+        ok = false;
+        break;
+      }
+      const int turn_at = base + 2 * j + t;
+      if (!single && !wait_turn(turn, turn_at, abort_flag, err)) {
+        ok = false;
+        break;
+      }
+      if (has_pv) {
+        tc_fence_after();
+        const uint64_t vd = sw128_desc(v_base, kColBlockBytes, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
+          mma_ts(o_col, s_col + kk * 8, vd + static_cast<uint64_t>(kk * 128), idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
+      }
+      if (has_s) {
+        const uint64_t qd = sw128_desc(qt, 16, 1024), kd = sw128_desc(k_base, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kKSteps; ++kk) {
+          const uint64_t off = static_cast<uint64_t>(((kk / 4) * kColBlockBytes + (kk % 4) * 32) >> 4);
+          mma_ss(s_col, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+        }
+      }
+      if (!single) *turn = turn_at + 1;
+      if (has_s) mma_commit(bar(W::kSFull + t));
+      if (has_pv) {
+        if (j - 1 == nt - 1) mma_commit(bar(W::kOFull + t));
+        mma_commit(bar(W::kEmpty + sV));
+        if (single) mma_commit(bar(W::kEmpty + sV));
+      }
+      if (has_s) {
+        mma_commit(bar(W::kEmpty + sK));
+        if (single) mma_commit(bar(W::kEmpty + sK));
+        if (j == nt - 1) mma_commit(bar(W::kQEmpty));
+      }
+      if (unused) {
+        mma_commit(bar(W::kEmpty + sK));
+        mma_commit(bar(W::kEmpty + sV2));
+      }
+    }
+    c += 2 * n_max;
+    steps += nt;
+    if (!single) base += 2 * (n_max + 1);
+  }
+  mma_commit(bar(W::kMmaDone));
+  mbar_drain(bar(W::kMmaDone), 0, err);
+}
+
+// Softmax warpgroup of query tile t.
+template <int D>
+__device__ __noinline__ void wide_softmax(const PagedAttnParams &p, Walk walk, const int *prefix, int t, uint32_t bar0,
+                                          uint32_t sRing, uint32_t tmem, volatile int *abort_flag, int *err) {
+  using W = WideBars<D>;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  const int r = threadIdx.x & 127;
+  const uint32_t lane_off = static_cast<uint32_t>(r & ~31) << 16;
+  int steps = 0, ring = 0;
+  uint32_t u = 0;
+  Segment g;
+  while (walk.next(p, prefix, g)) {
+    const int n = Walk::tiles(p, g, t), n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
+    if (!softmax_segment<D>(p, g, t, n, r, s_column(tmem, t) + lane_off, o_column(tmem, t) + lane_off,
+                            bar(W::kSFull + t), bar(W::kPFull + t), bar(W::kOFull + t), bar(W::kFull), sRing, ring, steps,
+                            u & 1u, abort_flag, err))
+      return;
+    ring += 2 * n_max;
+    steps += n;
+    if (n > 0) ++u;
+  }
+}
+
+}  // namespace paged
+}  // namespace seqattn
+
+#include "attn_paged_narrow.cuh"
+
+namespace seqattn {
+namespace paged {
+
+// Query maps by the tokens of their box: a wide tile's, and 16, 32, 64 rows'.
+struct QueryMaps {
+  CUtensorMap wide, narrow[3];
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q32,
-                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const __grid_constant__ PagedAttnParams p) {
+    attn_paged_kernel(const __grid_constant__ QueryMaps tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttnParams p) {
   using C = Cfg<D>;
+  using L = Narrow<D>;
+  using W = WideBars<D>;
+  static_assert(L::kAreaBytes <= C::kAreaBytes && L::kNumBarriers <= C::kMaxBarriers && W::kMmaDone < C::kMaxBarriers,
+                "shared memory layout");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem =
       reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t *sQ = smem;                          // [tile][col block][128 rows][128 B]
-  uint8_t *sRing = smem + 2 * C::kTileBytes;   // [slot][col block][128 rows][128 B]
-  uint8_t *sStage = sRing + C::kStages * C::kTileBytes;  // [tile][8 KB]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sStage + 2 * C::kStageBytes);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBarriers);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kAreaBytes);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kMaxBarriers);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  volatile int *turn = reinterpret_cast<volatile int *>(tmem_slot + 2);
+  volatile int *turn = reinterpret_cast<volatile int *>(tmem_slot + 2);  // next MMA burst slot (wide)
   int *warp_sums = reinterpret_cast<int *>(tmem_slot + 4);
-  int *prefix = warp_sums + 12;
-
-  const uint32_t bar0 = smem_addr(bars);
+  float *red = reinterpret_cast<float *>(warp_sums + 24);
+  int *prefix = reinterpret_cast<int *>(red + C::kRedFloats);
+  const uint32_t bar0 = smem_addr(bars), base = smem_addr(smem);
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
-  const int kBarQFull = 0, kBarQEmpty = 1, kBarFull = 2, kBarEmpty = 2 + C::kStages, kBarSFull = 2 + 2 * C::kStages,
-            kBarPFull = kBarSFull + 2, kBarOFull = kBarPFull + 2, kBarMmaDone = kBarOFull + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int *err = &g_device_error;
 
-  if (threadIdx.x == 0) {
-    mbar_init(bar(kBarQFull), 1);
-    mbar_init(bar(kBarQEmpty), 2);
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(bar(kBarFull + s), 1);
-      mbar_init(bar(kBarEmpty + s), 2);
-    }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(kBarSFull + t), 1);
-      mbar_init(bar(kBarPFull + t), 4);
-      mbar_init(bar(kBarOFull + t), 1);
-    }
-    mbar_init(bar(kBarMmaDone), 2);
-    // an earlier timeout, not yet cleared by the host: this CTA skips its work
-    // and the merge writes O = 0, lse = -inf
-    *abort_flag = *reinterpret_cast<volatile int *>(err) != kErrNone;
-    *turn = 0;
-    fence_barrier_init();
-  }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
-  prefix_tiles(p, prefix, warp_sums);
+  const int most = prefix_tiles(p, prefix, warp_sums);
+  const bool narrow = most * p.G <= 64;
+  const L sh(most * p.G, p.G);
+  if (threadIdx.x == 0) {
+    if (narrow) {
+      for (int s = 0; s < sh.stages; ++s) {
+        mbar_init(bar(L::kFull + s), 1);
+        mbar_init(bar(L::kEmpty + s), 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(L::kQFull + i), 1);
+        mbar_init(bar(L::kQEmpty + i), 1);
+        mbar_init(bar(L::kSFull + i), 1);
+      }
+      mbar_init(bar(L::kPFull), 4 * sh.groups);
+      mbar_init(bar(L::kPvDone), 1);
+      mbar_init(bar(L::kMmaDone), 1);
+    } else {
+      mbar_init(bar(W::kQFull), 1);
+      mbar_init(bar(W::kQEmpty), 2);
+      for (int s = 0; s < C::kStages; ++s) {
+        mbar_init(bar(W::kFull + s), 1);
+        mbar_init(bar(W::kEmpty + s), 2);
+      }
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(bar(W::kSFull + t), 1);
+        mbar_init(bar(W::kPFull + t), 4);
+        mbar_init(bar(W::kOFull + t), 1);
+      }
+      mbar_init(bar(W::kMmaDone), 2);
+    }
+    // an earlier timeout, not yet cleared by the host: this CTA skips its work
+    // and its rows come out as O = 0, lse = -inf
+    *abort_flag = *reinterpret_cast<volatile int *>(err) != kErrNone;
+    *turn = 0;
+    fence_barrier_init();
+  }
+  if (narrow) {
+    // rows of Q that no token fills: zeros, not whatever was there
+    for (int i = threadIdx.x; i < sh.q_bufs * sh.q_bytes() / 16; i += kThreads)
+      st_shared_v4(base + sh.q_at() + 16 * i, 0u, 0u, 0u, 0u);
+    fence_proxy_async_shared();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   launch_dependents();  // the merge: its CTAs wait for this kernel before they read
   const uint32_t tmem = *tmem_slot;
   const bool skip = *abort_flag != 0;
-  auto tS = [&](int t) -> uint32_t { return tmem + 128u * static_cast<uint32_t>(t); };
-  auto tO = [&](int t) -> uint32_t { return tmem + 256u + 128u * static_cast<uint32_t>(t); };
-  Walk walk(prefix, p.cache.B, gridDim.x);
-  Segment g;
+  const Walk walk(prefix, p.cache.B, gridDim.x);
+  if (skip && threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (warp < 8) write_unseen<D>(p, skip, threadIdx.x, 256);
 
-  if (warp == kTmaWarp) {
-    // ------------------------------------------------------------ producer (the whole warp)
-    if (!skip) {
-      if (lane == 0) {
-        tma_prefetch_map(&tm_q);
-        tma_prefetch_map(&tm_q32);
-        tma_prefetch_map(&tm_k);
-        tma_prefetch_map(&tm_v);
-      }
-      const uint64_t pol_q = l2_policy_evict_last(), pol_kv = l2_policy_evict_first();
-      const int page_size = 1 << p.page_log2;
-      const bool small = page_size < kRowsPerTile;
-      const int boxes = small ? kRowsPerTile >> p.page_log2 : 1;  // pages of a key tile
-      const uint32_t box_bytes = (small ? page_size : kRowsPerTile) * 128u;
-      int c = 0, nq = 0;
-      bool ok = true;
-      // the item that this CTA begins and another one ends, for the merge
-      int4 cut = make_int4(0, 0, 0, 0);
-      while (ok && walk.next(p, prefix, g)) {
-        if (g.j0 == 0 && g.slot >= 0)
-          cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, g.last_cta);
-        const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
-        const bool two = Walk::tiles(p, g, 1) > 0;
-        const int *row = page_row(p, g);
-        // the page of this lane for key tile j: n_pages (read as zeros) where there is none
-        auto page_of = [&](int j) -> int {
-          if (lane >= boxes) return 0;
-          const int i = small ? j * boxes + lane : (j * kRowsPerTile) >> p.page_log2;
-          int e = -1;
-          if ((i << p.page_log2) < g.s.kv_len) e = row[i];
-          return e >= 0 && e < p.cache.n_pages ? e : p.cache.n_pages;
-        };
-        int page = page_of(g.j0);
-        if (lane == 0) {
-          ok = nq == 0 || mbar_wait(bar(kBarQEmpty), (nq - 1) & 1, abort_flag, err);
-          if (ok) {
-            const bool few = few_rows(p, g);
-            const int copies = few ? 4 : 1;  // of each tile, 32 rows apart
-            const uint32_t q_bytes = static_cast<uint32_t>(copies * g.tok * p.G) * 128u * C::kColBlocks;
-            mbar_arrive_expect_tx(bar(kBarQFull), two ? 2 * q_bytes : q_bytes);
-            for (int t = 0; t < (two ? 2 : 1); ++t)
-              for (int cb = 0; cb < C::kColBlocks; ++cb)
-                for (int k = 0; k < copies; ++k)
-                  tma_load_4d_hint(smem_addr(sQ + (t * C::kColBlocks + cb) * kColBlockBytes + k * 32 * 128),
-                                   few ? &tm_q32 : &tm_q, bar(kBarQFull), cb * 64, 0,
-                                   g.s.q0 + (2 * g.rb + t) * g.tok, g.h, pol_q);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        ++nq;
-        for (int j = 0; j < n_max && ok; ++j) {
-          const int now = page;
-          if (j + 1 < n_max) page = page_of(g.j0 + j + 1);
-          const int in_page = small ? 0 : ((g.j0 + j) * kRowsPerTile) & (page_size - 1);
-          for (int which = 0; which < 2; ++which, ++c) {
-            const int slot = c % C::kStages;
-            if (lane == 0) {
-              ok = c < C::kStages || mbar_wait(bar(kBarEmpty + slot), ((c / C::kStages) - 1) & 1, abort_flag, err);
-              if (ok) mbar_arrive_expect_tx(bar(kBarFull + slot), C::kTileBytes);
-            }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok) break;
-            if (lane < boxes) {
-              const CUtensorMap *map = which ? &tm_v : &tm_k;
-#pragma unroll
-              for (int cb = 0; cb < C::kColBlocks; ++cb)
-                tma_load_4d_hint(smem_addr(sRing + (slot * C::kColBlocks + cb) * kColBlockBytes) + lane * box_bytes, map,
-                                 bar(kBarFull + slot), cb * 64, in_page, g.h, now, pol_kv);
-            }
-            __syncwarp();
-          }
-        }
-      }
-      if (lane == 0) p.cuts[blockIdx.x] = cut;
-      if (lane == 0) {  // every copy must have landed before the CTA may exit
-        if (nq > 0) mbar_drain(bar(kBarQFull), (nq - 1) & 1, err);
-        for (int i = max(0, c - C::kStages); i < c; ++i)
-          mbar_drain(bar(kBarFull + i % C::kStages), (i / C::kStages) & 1, err);
-      }
+  if (skip) {
+    // nothing
+  } else if (narrow) {
+    if (warp == kTmaWarp) {
+      narrow_producer<D>(p, sh, walk, prefix, &tm_q.narrow[sh.N == 16 ? 0 : (sh.N == 32 ? 1 : 2)], &tm_k, &tm_v, bar0, base,
+                         abort_flag, err);
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) narrow_issuer<D>(p, sh, walk, prefix, bar0, base, tmem, abort_flag, err);
+      __syncwarp();
+    } else if (warp < 4 * sh.groups) {
+      if (sh.N == 64)
+        narrow_softmax<D, 32>(p, sh, walk, prefix, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 4 * 32, abort_flag, err);
+      else
+        narrow_softmax<D, 16>(p, sh, walk, prefix, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 4 * 16, abort_flag, err);
     }
-    __syncwarp();
-  } else if (warp == kMmaWarp || warp == kMmaWarp1) {
-    // ------------------------------------------------------------ MMA issuers (the dense forward's scheme)
-    const int t = (warp == kMmaWarp) ? 0 : 1;
-    if (lane == 0 && !skip) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, D, true);
-      constexpr int kKSteps = D / 16;
-      const uint32_t qt = smem_addr(sQ) + t * C::kTileBytes, ring_base = smem_addr(sRing);
-      const uint32_t s_col = tS(t), o_col = tO(t);
-      int c = 0, nq = 0, steps = 0, base = 0;
-      bool ok = true;
-      while (ok && walk.next(p, prefix, g)) {
-        const int nt = Walk::tiles(p, g, t);
-        const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
-        // tile 1 has nothing to do: its issuer only gives Q back, and tile 0's
-        // goes on without taking turns and releases each slot for both
-        const bool single = Walk::tiles(p, g, 1) == 0;
-        if (!mbar_wait(bar(kBarQFull), nq & 1, abort_flag, err)) break;
-        ++nq;
-        if (nt == 0) mma_commit(bar(kBarQEmpty));
-        if (single && t == 1) {
-          c += 2 * n_max;
-          continue;
-        }
-        for (int j = 0; ok && j <= n_max; ++j) {
-          const int cK = c + 2 * j, cV = c + 2 * j - 1;
-          const int sK = cK % C::kStages, sV = (cV + C::kStages) % C::kStages;
-          const int cV2 = cK + 1, sV2 = cV2 % C::kStages;
-          const uint32_t k_base = ring_base + sK * C::kTileBytes, v_base = ring_base + sV * C::kTileBytes;
-          const bool has_pv = j >= 1 && j - 1 < nt, has_s = j < nt, unused = !has_s && j < n_max;
-          if ((has_s || unused) && !mbar_wait(bar(kBarFull + sK), (cK / C::kStages) & 1, abort_flag, err)) {
-            ok = false;
-            break;
-          }
-          if (unused && !mbar_wait(bar(kBarFull + sV2), (cV2 / C::kStages) & 1, abort_flag, err)) {
-            ok = false;
-            break;
-          }
-          if (has_pv && (!mbar_wait(bar(kBarFull + sV), (cV / C::kStages) & 1, abort_flag, err) ||
-                         !mbar_wait(bar(kBarPFull + t), (steps + j - 1) & 1, abort_flag, err))) {
-            ok = false;
-            break;
-          }
-          const int turn_at = base + 2 * j + t;
-          if (!single && !wait_turn(turn, turn_at, abort_flag, err)) {
-            ok = false;
-            break;
-          }
-          if (has_pv) {
-            tc_fence_after();
-            const uint64_t vd = sw128_desc(v_base, kColBlockBytes, 1024);
-#pragma unroll
-            for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
-              mma_ts(o_col, s_col + kk * 8, vd + static_cast<uint64_t>(kk * 128), idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
-          }
-          if (has_s) {
-            const uint64_t qd = sw128_desc(qt, 16, 1024), kd = sw128_desc(k_base, 16, 1024);
-#pragma unroll
-            for (int kk = 0; kk < kKSteps; ++kk) {
-              const uint64_t off = static_cast<uint64_t>(((kk / 4) * kColBlockBytes + (kk % 4) * 32) >> 4);
-              mma_ss(s_col, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-            }
-          }
-          if (!single) *turn = turn_at + 1;
-          if (has_s) mma_commit(bar(kBarSFull + t));
-          if (has_pv) {
-            if (j - 1 == nt - 1) mma_commit(bar(kBarOFull + t));
-            mma_commit(bar(kBarEmpty + sV));
-            if (single) mma_commit(bar(kBarEmpty + sV));
-          }
-          if (has_s) {
-            mma_commit(bar(kBarEmpty + sK));
-            if (single) mma_commit(bar(kBarEmpty + sK));
-            if (j == nt - 1) mma_commit(bar(kBarQEmpty));
-          }
-          if (unused) {
-            mma_commit(bar(kBarEmpty + sK));
-            mma_commit(bar(kBarEmpty + sV2));
-          }
-        }
-        c += 2 * n_max;
-        steps += nt;
-        if (!single) base += 2 * (n_max + 1);
-      }
-      mma_commit(bar(kBarMmaDone));
-      mbar_drain(bar(kBarMmaDone), 0, err);
-    }
-    __syncwarp();
-  } else if (warp < 8) {
-    // ------------------------------------------------------------ softmax + epilogue
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int steps = 0, ring = 0;
-    uint32_t u = 0;
-    write_unseen<D>(p, skip, threadIdx.x, 256);
-    while (!skip && walk.next(p, prefix, g)) {
-      const int n = Walk::tiles(p, g, t), n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
-      const bool fine =
-          few_rows(p, g)
-              ? few_rows_segment<D>(p, g, t, n, warp & 3, tS(t) + lane_off, tO(t) + lane_off, bar(kBarSFull + t),
-                                    bar(kBarPFull + t), bar(kBarOFull + t), bar(kBarFull), smem_addr(sRing), ring, steps,
-                                    u & 1u, reinterpret_cast<float *>(sStage + t * C::kStageBytes), abort_flag, err)
-              : softmax_segment<D>(p, g, t, n, r, tS(t) + lane_off, tO(t) + lane_off, bar(kBarSFull + t),
-                                   bar(kBarPFull + t), bar(kBarOFull + t), bar(kBarFull), smem_addr(sRing), ring, steps,
-                                   u & 1u, abort_flag, err);
-      if (!fine) break;
-      ring += 2 * n_max;
-      steps += n;
-      if (n > 0) ++u;
+  } else {
+    const uint32_t sQ = base, sRing = base + 2 * C::kTileBytes;
+    if (warp == kTmaWarp) {
+      wide_producer<D>(p, walk, prefix, &tm_q.wide, &tm_k, &tm_v, bar0, sQ, sRing, abort_flag, err);
+    } else if (warp == kMmaWarp || warp == kMmaWarp1) {
+      if (lane == 0) wide_issuer<D>(p, walk, prefix, warp == kMmaWarp ? 0 : 1, bar0, sQ, sRing, tmem, turn, abort_flag, err);
+      __syncwarp();
+    } else {
+      wide_softmax<D>(p, walk, prefix, warp >> 2, bar0, sRing, tmem, abort_flag, err);
     }
   }
 
@@ -945,14 +869,14 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
 }
 
 template <int D>
-cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tq32, const CUtensorMap &tk, const CUtensorMap &tv,
-                         const PagedAttnParams &p, cudaStream_t stream) {
+cudaError_t launch_typed(const QueryMaps &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PagedAttnParams &p,
+                         cudaStream_t stream) {
   auto kernel = attn_paged_kernel<D>;
   constexpr int kSmem = Cfg<D>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int n_ctas = sm_count() < kPagedMaxCtas ? sm_count() : kPagedMaxCtas;
-  kernel<<<n_ctas, kThreads, kSmem, stream>>>(tq, tq32, tk, tv, p);
+  kernel<<<n_ctas, kThreads, kSmem, stream>>>(tq, tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || n_ctas == 1) return e;
   // the merge starts while the attention still runs and waits for its end inside
@@ -970,10 +894,10 @@ cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tq32, const C
 
 }  // namespace paged
 
-cudaError_t launch_attn_paged(int D, const CUtensorMap &tq, const CUtensorMap &tq32, const CUtensorMap &tk,
+cudaError_t launch_attn_paged(int D, const CUtensorMap &tq, const CUtensorMap (&tqn)[3], const CUtensorMap &tk,
                               const CUtensorMap &tv, const PagedAttnParams &p, cudaStream_t stream) {
-  return D == 64 ? paged::launch_typed<64>(tq, tq32, tk, tv, p, stream)
-                 : paged::launch_typed<128>(tq, tq32, tk, tv, p, stream);
+  const paged::QueryMaps maps{tq, {tqn[0], tqn[1], tqn[2]}};
+  return D == 64 ? paged::launch_typed<64>(maps, tk, tv, p, stream) : paged::launch_typed<128>(maps, tk, tv, p, stream);
 }
 
 }  // namespace seqattn

@@ -124,9 +124,7 @@ struct PagedView {
 
 // Attention of packed new tokens over a paged cache. The rows of a KV head are
 // numbered (token, query head of the group), group fastest; a 128-row tile has
-// `tok` whole tokens (tok * G <= 128), a work item two tiles. Sequences of at
-// most 2 * tok32 new tokens (tok32 * G <= 32) take tiles of 32 rows, each four
-// times in the 128.
+// `tok` whole tokens (tok * G <= 128), a work item two tiles.
 struct PagedAttnParams {
   PagedView cache;
   void *o;                 // bf16, row t of head h at h * o_h + t * o_s
@@ -136,18 +134,20 @@ struct PagedAttnParams {
   float *part_lse;         // workspace: [2 * kPagedMaxCtas][part_rows]
   int4 *cuts;              // workspace: [kPagedMaxCtas] the items that the CTAs begin and do not end
   int part_rows;           // rows of a work item that can hold a token
-  int Hq, G, tok, tok32, total_q, causal;
+  int Hq, G, tok, total_q, causal;
   int page_log2;           // log2(page_size)
   float scale_log2;
 };
 constexpr int kPagedMaxCtas = 160;   // CTAs of one launch (at most one per SM)
-constexpr int kPagedMaxSeqs = 4096;  // sequences of one launch (their prefix sums sit in shared memory)
+constexpr int kPagedMaxSeqs = 2048;  // sequences of one launch (their prefix sums sit in shared memory)
+constexpr int kPagedMaxRows = 4096;  // rows of a page table
 
-// Maps: q and q32 bf16 4-D [Hkv][total_q][G][D], box 64 x G x tok x 1 and 64 x
-// G x tok32 x 1 (unused if tok32 is 0); k, v bf16 4-D
-// [n_pages][Hkv][page_size][D], box 64 x min(page_size, 128) x 1 x 1; 128-byte
-// swizzle. Two kernels: the attention and the merge of split rows.
-cudaError_t launch_attn_paged(int D, const CUtensorMap &tm_q, const CUtensorMap &tm_q32, const CUtensorMap &tm_k,
+// Maps: q bf16 4-D [Hkv][total_q][G][D], box 64 x G x tok x 1, and the same with
+// boxes of 16 / G, 32 / G, 64 / G tokens (at least one) for calls whose sequences
+// have that few rows; k, v bf16 4-D [n_pages][Hkv][page_size][D], box 64 x
+// min(page_size, 128) x 1 x 1; 128-byte swizzle. Two kernels: the attention and
+// the merge of split rows.
+cudaError_t launch_attn_paged(int D, const CUtensorMap &tm_q, const CUtensorMap (&tm_qn)[3], const CUtensorMap &tm_k,
                               const CUtensorMap &tm_v, const PagedAttnParams &p, cudaStream_t stream);
 
 // ---------------------------------------------------------------- rotary positions, appends

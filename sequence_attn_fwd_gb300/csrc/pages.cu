@@ -85,7 +85,7 @@ __device__ __forceinline__ int pages_for(long long tokens, int page_log2) {
   return static_cast<int>((tokens + (1ll << page_log2) - 1) >> page_log2);
 }
 
-// prefix[0..n] of need(i), n <= kPagedMaxSeqs (prefix saturates far above any pool).
+// prefix[0..n] of need(i), n <= kPagedMaxRows (prefix saturates far above any pool).
 template <typename Need>
 __device__ void scan_needs(int *prefix, int n, int *warp_sums, Need need) {
   const int per = (n + kPlanThreads - 1) / kPlanThreads;
@@ -106,7 +106,7 @@ __device__ void scan_needs(int *prefix, int n, int *warp_sums, Need need) {
 // gives rank r to the row whose range holds it. A row that the pool cannot
 // serve whole (only the last one reached can have got some pages) gives them back.
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(PageTables t, const int *n_new, int *status) {
-  __shared__ int prefix[kPagedMaxSeqs + 1];
+  __shared__ int prefix[kPagedMaxRows + 1];
   __shared__ int warp_sums[33];
   const long long room = static_cast<long long>(t.max_pages) << t.page_log2;
   auto len_of = [&](int b) -> long long { return max(t.kv_lens[b], 0); };
