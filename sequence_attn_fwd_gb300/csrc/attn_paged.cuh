@@ -44,13 +44,14 @@ struct Cfg {
   static constexpr int kStages = 131072 / kTileBytes;
   static constexpr int kNumBarriers = 2 + 2 * kStages + 7;
   // tiles of the wide form (Q, ring) or of the narrow one (ring, P, Q), then
-  // barriers, three words, warp sums, the narrow form's reductions, prefix sums
+  // barriers, three words, warp sums, the range's start, the narrow form's
+  // reductions, prefix sums
   static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 2 * 16 * D * 2;
   static_assert(2 * kTileBytes + kStages * kTileBytes <= kAreaBytes, "wide layout");
   static constexpr int kMaxBarriers = 2 * (196608 / kTileBytes) + 10;
-  static constexpr int kRedFloats = 2 * 4 * 32;
+  static constexpr int kRedFloats = 2 * 6 * 32;
   static constexpr int kSmemBytes =
-      1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 24 + 4 * kRedFloats + 4 * (kPagedMaxSeqs + 1);
+      1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 24 + 32 + 4 * kRedFloats + 4 * (kPagedMaxSeqs + 1);
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -191,20 +192,32 @@ __device__ __forceinline__ const int *page_row(const PagedAttnParams &p, const S
   return p.cache.page_table + g.b * p.cache.table_stride;
 }
 
-// Walks the segments of this CTA's range of tiles in order; every role walks its own.
+// Where a CTA's range begins, found once by its producer warp and read by every role.
+struct Start {
+  Place at;
+  Seq s;
+};
+
+// Walks the segments of this CTA's range of tiles in order; every role walks its
+// own. One copy of the code for all roles: what runs once per CTA costs its
+// instruction fetches more than its work.
 struct Walk {
   int pos, end, per;
+  const int *prefix;
+  const Start *start;
   Place at;
   bool fresh;
-  __device__ __forceinline__ Walk(const int *prefix, int B, int n_ctas) : fresh(true) {
+  __device__ __forceinline__ Walk(const int *prefix_, const Start *start_, int B, int n_ctas)
+      : prefix(prefix_), start(start_), fresh(true) {
     per = tiles_per_cta(prefix[B], n_ctas);
     pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(prefix[B])));
     end = static_cast<int>(min(static_cast<long long>(pos) + per, static_cast<long long>(prefix[B])));
   }
-  __device__ __forceinline__ bool next(const PagedAttnParams &p, const int *prefix, Segment &g) {
+  __device__ __noinline__ bool next(const PagedAttnParams &p, Segment &g) {
     if (pos >= end) return false;
     if (fresh) {
-      at = place_of(p, prefix, pos, g.s);
+      at = start->at;
+      g.s = start->s;
       fresh = false;
     } else {
       // the item after the last one, skipping those that see no key
@@ -243,6 +256,15 @@ struct Walk {
     return max(0, min(g.j1, tiles_seen(p, g.s, first + p.tok)) - g.j0);
   }
 };
+
+// The table entry of lane `lane` for key tile j of a sequence with kv_len keys:
+// one entry per page of the tile, -1 past them and past the sequence.
+__device__ __forceinline__ int page_entry(const PagedAttnParams &p, const int *row, int kv_len, int j, int lane) {
+  const bool small = p.page_log2 < 7;
+  if (lane >= (small ? kRowsPerTile >> p.page_log2 : 1)) return -1;
+  const int i = small ? j * (kRowsPerTile >> p.page_log2) + lane : (j * kRowsPerTile) >> p.page_log2;
+  return (i << p.page_log2) < kv_len ? row[i] : -1;
+}
 
 // The pages of a key tile and which of them are there. Each lane of a warp
 // looks one up ahead of time; `mask` then has one bit per page.
@@ -455,7 +477,7 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
 
 // Rows of the items that see no key at all (every row, if `all`): O = 0, lse = -inf.
 template <int D>
-__device__ void write_unseen(const PagedAttnParams &p, bool all, int tid, int nthreads) {
+__device__ __noinline__ void write_unseen(const PagedAttnParams &p, bool all, int tid, int nthreads) {
   for (int b = blockIdx.x; b < p.cache.B; b += gridDim.x) {
     const Seq s = sequence(p, b);
     const int rbs = row_blocks(p, s);
@@ -486,9 +508,9 @@ __device__ __forceinline__ uint32_t o_column(uint32_t tmem, int t) { return tmem
 // Producer: the whole warp. sQ [tile][col block][128 rows][128 B], sRing
 // [slot][col block][128 rows][128 B].
 template <int D>
-__device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, const int *prefix, const CUtensorMap *tm_q,
+__device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, const CUtensorMap *tm_q,
                                            const CUtensorMap *tm_k, const CUtensorMap *tm_v, uint32_t bar0, uint32_t sQ,
-                                           uint32_t sRing, volatile int *abort_flag, int *err) {
+                                           uint32_t sRing, int first_entry, volatile int *abort_flag, int *err) {
   using C = Cfg<D>;
   using W = WideBars<D>;
   const int lane = threadIdx.x & 31;
@@ -503,21 +525,15 @@ __device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, 
   bool ok = true;
   // the item that this CTA begins and another one ends, for the merge
   int4 cut = make_int4(0, 0, 0, 0);
-  while (ok && walk.next(p, prefix, g)) {
+  while (ok && walk.next(p, g)) {
     if (g.j0 == 0 && g.slot >= 0)
       cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, g.last_cta);
     const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
     const bool two = Walk::tiles(p, g, 1) > 0;
     const int *row = page_row(p, g);
     // the page of this lane for key tile j: n_pages (read as zeros) where there is none
-    auto page_of = [&](int j) -> int {
-      if (lane >= boxes) return 0;
-      const int i = small ? j * boxes + lane : (j * kRowsPerTile) >> p.page_log2;
-      int e = -1;
-      if ((i << p.page_log2) < g.s.kv_len) e = row[i];
-      return e >= 0 && e < p.cache.n_pages ? e : p.cache.n_pages;
-    };
-    int page = page_of(g.j0);
+    auto page_of = [&](int entry) -> int { return entry >= 0 && entry < p.cache.n_pages ? entry : p.cache.n_pages; };
+    int page = page_of(nq == 0 ? first_entry : page_entry(p, row, g.s.kv_len, g.j0, lane));
     if (lane == 0) {
       ok = nq == 0 || mbar_wait(bar(W::kQEmpty), (nq - 1) & 1, abort_flag, err);
       if (ok) {
@@ -534,7 +550,7 @@ __device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, 
     ++nq;
     for (int j = 0; j < n_max && ok; ++j) {
       const int now = page;
-      if (j + 1 < n_max) page = page_of(g.j0 + j + 1);
+      if (j + 1 < n_max) page = page_of(page_entry(p, row, g.s.kv_len, g.j0 + j + 1, lane));
       const int in_page = small ? 0 : ((g.j0 + j) * kRowsPerTile) & (page_size - 1);
       for (int which = 0; which < 2; ++which, ++c) {
         const int slot = c % C::kStages;
@@ -566,7 +582,7 @@ __device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, 
 
 // MMA issuer of query tile t, one thread (the dense forward's scheme).
 template <int D>
-__device__ __noinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, const int *prefix, int t, uint32_t bar0,
+__device__ __noinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, int t, uint32_t bar0,
                                          uint32_t sQ, uint32_t sRing, uint32_t tmem, volatile int *turn,
                                          volatile int *abort_flag, int *err) {
   using C = Cfg<D>;
@@ -579,7 +595,7 @@ __device__ __noinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, co
   const uint32_t s_col = s_column(tmem, t), o_col = o_column(tmem, t);
   int c = 0, nq = 0, steps = 0, base = 0;
   bool ok = true;
-  while (ok && walk.next(p, prefix, g)) {
+  while (ok && walk.next(p, g)) {
     const int nt = Walk::tiles(p, g, t);
     const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
     // tile 1 has nothing to do: its issuer only gives Q back, and tile 0's
@@ -658,7 +674,7 @@ __device__ __noinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, co
 
 // Softmax warpgroup of query tile t.
 template <int D>
-__device__ __noinline__ void wide_softmax(const PagedAttnParams &p, Walk walk, const int *prefix, int t, uint32_t bar0,
+__device__ __noinline__ void wide_softmax(const PagedAttnParams &p, Walk walk, int t, uint32_t bar0,
                                           uint32_t sRing, uint32_t tmem, volatile int *abort_flag, int *err) {
   using W = WideBars<D>;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -667,7 +683,7 @@ __device__ __noinline__ void wide_softmax(const PagedAttnParams &p, Walk walk, c
   int steps = 0, ring = 0;
   uint32_t u = 0;
   Segment g;
-  while (walk.next(p, prefix, g)) {
+  while (walk.next(p, g)) {
     const int n = Walk::tiles(p, g, t), n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
     if (!softmax_segment<D>(p, g, t, n, r, s_column(tmem, t) + lane_off, o_column(tmem, t) + lane_off,
                             bar(W::kSFull + t), bar(W::kPFull + t), bar(W::kOFull + t), bar(W::kFull), sRing, ring, steps,
@@ -709,7 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *turn = reinterpret_cast<volatile int *>(tmem_slot + 2);  // next MMA burst slot (wide)
   int *warp_sums = reinterpret_cast<int *>(tmem_slot + 4);
-  float *red = reinterpret_cast<float *>(warp_sums + 24);
+  Start *start = reinterpret_cast<Start *>(warp_sums + 24);
+  float *red = reinterpret_cast<float *>(warp_sums + 32);
   int *prefix = reinterpret_cast<int *>(red + C::kRedFloats);
   const uint32_t bar0 = smem_addr(bars), base = smem_addr(smem);
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -723,6 +740,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int most = prefix_tiles(p, prefix, warp_sums);
   const bool narrow = most * p.G <= 64;
   const L sh(most * p.G, p.G);
+  const Walk walk(prefix, start, p.cache.B, gridDim.x);
+  int first_entry = -1;  // the producer's lanes: the first key tile's pages
+  if (warp == kTmaWarp && walk.pos < walk.end) {
+    Start s;
+    s.at = place_of(p, prefix, walk.pos, s.s);
+    first_entry = page_entry(p, p.cache.page_table + s.at.b * p.cache.table_stride, s.s.kv_len, s.at.r, lane);
+    if (lane == 0) *start = s;
+  }
   if (threadIdx.x == 0) {
     if (narrow) {
       for (int s = 0; s < sh.stages; ++s) {
@@ -769,7 +794,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   launch_dependents();  // the merge: its CTAs wait for this kernel before they read
   const uint32_t tmem = *tmem_slot;
   const bool skip = *abort_flag != 0;
-  const Walk walk(prefix, p.cache.B, gridDim.x);
   if (skip && threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (warp < 8) write_unseen<D>(p, skip, threadIdx.x, 256);
 
@@ -777,26 +801,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     // nothing
   } else if (narrow) {
     if (warp == kTmaWarp) {
-      narrow_producer<D>(p, sh, walk, prefix, &tm_q.narrow[sh.N == 16 ? 0 : (sh.N == 32 ? 1 : 2)], &tm_k, &tm_v, bar0, base,
-                         abort_flag, err);
+      narrow_producer<D>(p, sh, walk, &tm_q.narrow[sh.N == 16 ? 0 : (sh.N == 32 ? 1 : 2)], &tm_k, &tm_v, bar0, base,
+                         first_entry, abort_flag, err);
     } else if (warp == kMmaWarp) {
-      if (lane == 0) narrow_issuer<D>(p, sh, walk, prefix, bar0, base, tmem, abort_flag, err);
+      if (lane == 0) narrow_issuer<D>(p, sh, walk, bar0, base, tmem, abort_flag, err);
       __syncwarp();
     } else if (warp < 4 * sh.groups) {
       if (sh.N == 64)
-        narrow_softmax<D, 32>(p, sh, walk, prefix, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 4 * 32, abort_flag, err);
+        narrow_softmax<D, 32>(p, sh, walk, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 6 * 32, abort_flag, err);
       else
-        narrow_softmax<D, 16>(p, sh, walk, prefix, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 4 * 16, abort_flag, err);
+        narrow_softmax<D, 16>(p, sh, walk, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 6 * 32, abort_flag, err);
     }
   } else {
     const uint32_t sQ = base, sRing = base + 2 * C::kTileBytes;
     if (warp == kTmaWarp) {
-      wide_producer<D>(p, walk, prefix, &tm_q.wide, &tm_k, &tm_v, bar0, sQ, sRing, abort_flag, err);
+      wide_producer<D>(p, walk, &tm_q.wide, &tm_k, &tm_v, bar0, sQ, sRing, first_entry, abort_flag, err);
     } else if (warp == kMmaWarp || warp == kMmaWarp1) {
-      if (lane == 0) wide_issuer<D>(p, walk, prefix, warp == kMmaWarp ? 0 : 1, bar0, sQ, sRing, tmem, turn, abort_flag, err);
+      if (lane == 0) wide_issuer<D>(p, walk, warp == kMmaWarp ? 0 : 1, bar0, sQ, sRing, tmem, turn, abort_flag, err);
       __syncwarp();
     } else {
-      wide_softmax<D>(p, walk, prefix, warp >> 2, bar0, sRing, tmem, abort_flag, err);
+      wide_softmax<D>(p, walk, warp >> 2, bar0, sRing, tmem, abort_flag, err);
     }
   }
 

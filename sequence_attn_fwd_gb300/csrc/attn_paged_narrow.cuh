@@ -65,9 +65,10 @@ __device__ __forceinline__ uint32_t idesc_narrow(int N, bool pv) {
 
 // Producer: the whole warp.
 template <int D>
-__device__ __noinline__ void narrow_producer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk, const int *prefix,
+__device__ __noinline__ void narrow_producer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
                                              const CUtensorMap *tm_q, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
-                                             uint32_t bar0, uint32_t smem, volatile int *abort_flag, int *err) {
+                                             uint32_t bar0, uint32_t smem, int first_entry, volatile int *abort_flag,
+                                             int *err) {
   using C = Narrow<D>;
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -83,20 +84,15 @@ __device__ __noinline__ void narrow_producer(const PagedAttnParams &p, const Nar
   bool ok = true;
   Segment g;
   int4 cut = make_int4(0, 0, 0, 0);
-  while (ok && walk.next(p, prefix, g)) {
+  while (ok && walk.next(p, g)) {
     if (g.j0 == 0 && g.slot >= 0) cut = make_int4(g.s.q0, g.s.q_len * p.G, g.h, g.last_cta);
     const int n = g.j1 - g.j0;
     const int *row = page_row(p, g);
-    auto page_of = [&](int j) -> int {  // n_pages (read as zeros) where there is none
-      if (lane >= boxes) return 0;
-      const int i = small ? j * boxes + lane : (j * kRowsPerTile) >> p.page_log2;
-      int e = -1;
-      if ((i << p.page_log2) < g.s.kv_len) e = row[i];
-      return e >= 0 && e < p.cache.n_pages ? e : p.cache.n_pages;
-    };
+    // n_pages (read as zeros) where there is none
+    auto page_of = [&](int entry) -> int { return entry >= 0 && entry < p.cache.n_pages ? entry : p.cache.n_pages; };
     const int qb = nq % sh.q_bufs, use = nq / sh.q_bufs;
     bool q_due = true;  // this segment's Q is still to be loaded
-    int page = page_of(g.j0);
+    int page = page_of(nq == 0 ? first_entry : page_entry(p, row, g.s.kv_len, g.j0, lane));
     for (int f = 0; f < 2 * n && ok; ++f, ++fills) {
       // Q as soon as its buffer is free, but K and V go ahead of it meanwhile:
       // the slots of the first fills are given back by earlier segments
@@ -128,7 +124,7 @@ __device__ __noinline__ void narrow_producer(const PagedAttnParams &p, const Nar
           tma_load_4d_hint(smem + at.slot * C::kTileBytes + cb * kColBlockBytes + lane * box_bytes, map,
                            bar(C::kFull + at.slot), cb * 64, in_page, g.h, now, pol_kv);
       }
-      if (which && f + 1 < 2 * n) page = page_of(j + 1);
+      if (which && f + 1 < 2 * n) page = page_of(page_entry(p, row, g.s.kv_len, j + 1, lane));
       at = at.next(sh.stages);
     }
     ++nq;
@@ -146,7 +142,7 @@ __device__ __noinline__ void narrow_producer(const PagedAttnParams &p, const Nar
 
 // MMA issuer: one thread.
 template <int D>
-__device__ __noinline__ void narrow_issuer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk, const int *prefix,
+__device__ __noinline__ void narrow_issuer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
                                            uint32_t bar0, uint32_t smem, uint32_t tmem, volatile int *abort_flag,
                                            int *err) {
   using C = Narrow<D>;
@@ -159,7 +155,7 @@ __device__ __noinline__ void narrow_issuer(const PagedAttnParams &p, const Narro
   int nq = 0;
   bool ok = true;
   Segment g;
-  while (ok && walk.next(p, prefix, g)) {
+  while (ok && walk.next(p, g)) {
     const int n = g.j1 - g.j0;
     const int qb = nq % sh.q_bufs;
     if (!mbar_wait(bar(C::kQFull + qb), (nq / sh.q_bufs) & 1, abort_flag, err)) break;
@@ -168,10 +164,12 @@ __device__ __noinline__ void narrow_issuer(const PagedAttnParams &p, const Narro
     const uint64_t q_block = static_cast<uint64_t>((sh.N * 128) >> 4);  // from one 64-column block to the next
     auto scores = [&](const RingPos &at, uint32_t to, bool last) {
       const uint64_t kd = sw128_desc(smem + at.slot * C::kTileBytes, 16, 1024);
+#pragma unroll 1
+      for (int cb = 0; cb < C::kColBlocks; ++cb)
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss(tmem + (to & 1u) * sh.N, kd + static_cast<uint64_t>(((kk / 4) * kColBlockBytes + (kk % 4) * 32) >> 4),
-               qd + (kk / 4) * q_block + static_cast<uint64_t>((kk % 4) * 2), idesc_s, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss(tmem + (to & 1u) * sh.N, kd + static_cast<uint64_t>((cb * kColBlockBytes + kk * 32) >> 4),
+                 qd + cb * q_block + static_cast<uint64_t>(kk * 2), idesc_s, cb + kk > 0 ? 1u : 0u);
       mma_commit(bar(C::kSFull + (to & 1u)));
       mma_commit(bar(C::kEmpty + at.slot));
       if (last) mma_commit(bar(C::kQEmpty + qb));
@@ -194,7 +192,7 @@ __device__ __noinline__ void narrow_issuer(const PagedAttnParams &p, const Narro
       // upper 64 rows of the product read the bytes behind the tile and are
       // never looked at (rows of a product do not mix)
       const uint64_t vd = sw128_desc(smem + v.slot * C::kTileBytes, kColBlockBytes, 1024);
-#pragma unroll
+#pragma unroll 4
       for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
         mma_ss(o_col, vd + static_cast<uint64_t>(kk * 128), pd + static_cast<uint64_t>(kk * 128), idesc_o,
                (j > 0 || kk > 0) ? 1u : 0u);
@@ -214,19 +212,29 @@ __device__ __noinline__ void narrow_issuer(const PagedAttnParams &p, const Narro
   mbar_drain(bar(C::kMmaDone), 0, err);
 }
 
-// Floats as ints of the same order (finite values and infinities), and back.
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
+// Reduces 16 values over the 32 lanes of a warp at once, halving the values with
+// every step: lane i returns the result of value i / 2.
+template <typename Op>
+__device__ __forceinline__ float reduce16(float (&v)[16], Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int half = 8; half > 0; half >>= 1) {
+    const bool upper = lane & (2 * half);
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = upper ? v[i + half] : v[i], give = upper ? v[i] : v[i + half];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 2 * half));
+    }
+  }
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
-__device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 // Softmax and epilogue of columns [col0, col0 + C) of S^T: one thread per key
-// (and, in the epilogue, per column of O). `red` is this warpgroup's 4 x C
+// (and, in the epilogue, per column of O). `red` is this warpgroup's 6 x C
 // floats of shared memory, `gi` its number. Every warp goes through the same
 // barriers whatever fails: a wait that runs out is carried to the next vote.
 template <int D, int C>
-__device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk, const int *prefix,
+__device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
                                             int gi, uint32_t bar0, uint32_t smem, uint32_t tmem, float *red,
                                             volatile int *abort_flag, int *err) {
   using L = Narrow<D>;
@@ -237,10 +245,13 @@ __device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narr
   const uint32_t o_addr = tmem + lane_off + 2 * sh.N + col0;
   const uint32_t p_row = smem + sh.p_at() + key * 128;
   const float c2 = p.scale_log2;
+  auto larger = [](float a, float b) { return fmaxf(a, b); };
+  auto sum_of = [](float a, float b) { return a + b; };
+  float *ref = red + 4 * C, *factor = red + 5 * C;  // references of the columns; a factor for each
   RingPos k{0, 0};
   uint32_t step = 0;
   Segment g;
-  while (walk.next(p, prefix, g)) {
+  while (walk.next(p, g)) {
     const int n = g.j1 - g.j0, rows = g.s.q_len * p.G;
     const int first_last = p.causal ? g.s.kv_len - g.s.q_len : g.s.kv_len - 1;  // last key of the first token
     const int *table = page_row(p, g);
@@ -254,6 +265,7 @@ __device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narr
       m[c] = -INFINITY;
       l[c] = 0.f;
     }
+    if (key < C) ref[key] = -INFINITY;
     int entry = entry_of(g.j0);
     bool ok = true;
     for (int j = 0; j < n; ++j, ++step) {
@@ -263,73 +275,91 @@ __device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narr
       ok = ok && __all_sync(0xffffffffu,
                             mbar_wait(bar(L::kSFull + (step & 1u)), (step >> 1) & 1u, abort_flag, err));
       tc_fence_after();
-      float x[C];
-      {
-        uint32_t raw[C];
-        if constexpr (C == 16) tmem_ld16(tmem + lane_off + (step & 1u) * sh.N + col0, raw);
-        else tmem_ld32(tmem + lane_off + (step & 1u) * sh.N + col0, raw);
+      const bool partly = kv0 + kRowsPerTile - 1 > first_last;  // some row does not see all keys of the tile
+      // 16 columns from h on of this key's scores, times scale log2(e), masked
+      auto load_scores = [&](int h, float(&x)[16]) {
+        uint32_t raw[16];
+        tmem_ld16(tmem + lane_off + (step & 1u) * sh.N + col0 + h, raw);
         tmem_ld_wait(raw);
 #pragma unroll
-        for (int c = 0; c < C; ++c) x[c] = there ? __uint_as_float(raw[c]) * c2 : -INFINITY;
-      }
-      if (kv0 + kRowsPerTile - 1 > first_last) {  // some row does not see all keys of the tile
-        int tok = col0 / p.G, head = col0 - tok * p.G;
+        for (int c = 0; c < 16; ++c) x[c] = there ? __uint_as_float(raw[c]) * c2 : -INFINITY;
+        if (partly) {
+          int tok = (col0 + h) / p.G, head = col0 + h - tok * p.G;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int last = p.causal ? min(first_last + tok, g.s.kv_len - 1) : first_last;
-          if (kv0 + key > last) x[c] = -INFINITY;
-          if (++head == p.G) {
-            head = 0;
-            ++tok;
+          for (int c = 0; c < 16; ++c) {
+            const int last = p.causal ? min(first_last + tok, g.s.kv_len - 1) : first_last;
+            if (kv0 + key > last) x[c] = -INFINITY;
+            if (++head == p.G) {
+              head = 0;
+              ++tok;
+            }
           }
         }
-      }
+      };
+      float x[16];
       bool move = false;
 #pragma unroll
-      for (int c = 0; c < C; ++c) move = move || x[c] > m[c] + 8.f;
+      for (int h = 0; h < C; h += 16) {
+        load_scores(h, x);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) move = move || x[c] > m[h + c] + 8.f;
+      }
       if (!named_bar_and(id, 128, ok && !move)) {
         // maxima of the tile's 128 keys, then O and l onto the new reference
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float top = from_ordered(__reduce_max_sync(0xffffffffu, ordered(x[c])));
-          if (lane == 0) red[w * C + c] = top;
+        for (int h = 0; h < C; h += 16) {
+          if (C > 16) load_scores(h, x);
+          float y[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) y[c] = x[c];
+          const float top = reduce16(y, larger);
+          if (!(lane & 1)) red[w * C + h + (lane >> 1)] = top;
+        }
+        named_bar_sync(id, 128);
+        if (key < C) {
+          const float top = fmaxf(fmaxf(red[key], red[C + key]), fmaxf(red[2 * C + key], red[3 * C + key]));
+          const float old_ref = ref[key], new_ref = fmaxf(old_ref, top);
+          ref[key] = new_ref;
+          factor[key] = new_ref == -INFINITY ? 1.f : ex2_approx(old_ref - new_ref);
         }
         ok = named_bar_and(id, 128, ok);
         if (ok && j > 0)
           ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kPvDone), (step - 1) & 1u, abort_flag, err));
         tc_fence_after();
         const bool old = ok && j > 0;  // O holds the sum of the tiles before
-        uint32_t v[C] = {};
-        if (old) {
-          if constexpr (C == 16) tmem_ld16(o_addr, v);
-          else tmem_ld32(o_addr, v);
-          tmem_ld_wait(v);
-        }
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float top = fmaxf(fmaxf(red[c], red[C + c]), fmaxf(red[2 * C + c], red[3 * C + c]));
-          const float m_new = fmaxf(m[c], top);
-          const float alpha = m_new == -INFINITY ? 1.f : ex2_approx(m[c] - m_new);
-          m[c] = m_new;
-          l[c] *= alpha;
-          v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
+        for (int h = 0; h < C; h += 16) {
+          uint32_t v[16] = {};
+          if (old) {
+            tmem_ld16(o_addr + h, v);
+            tmem_ld_wait(v);
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float alpha = factor[h + c];
+            m[h + c] = ref[h + c];
+            l[h + c] *= alpha;
+            v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
+          }
+          if (old) tmem_st16(o_addr + h, v);
         }
-        if (old) {
-          if constexpr (C == 16) tmem_st16(o_addr, v);
-          else tmem_st32(o_addr, v);
-          tmem_st_wait();
-        }
+        if (old) tmem_st_wait();
       }
       uint32_t pk[C / 2];
 #pragma unroll
-      for (int c = 0; c < C; c += 2) {
-        const float a = ex2_approx(x[c] - (m[c] == -INFINITY ? 0.f : m[c]));
-        const float b = ex2_approx(x[c + 1] - (m[c + 1] == -INFINITY ? 0.f : m[c + 1]));
-        l[c] += a;
-        l[c + 1] += b;
-        // P enters the tensor cores in bf16, as in the dense forward; l is summed before the rounding
-        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        pk[c / 2] = *reinterpret_cast<uint32_t *>(&h);
+      for (int h = 0; h < C; h += 16) {
+        if (C > 16) load_scores(h, x);
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+          const int i = h + c;
+          const float a = ex2_approx(x[c] - (m[i] == -INFINITY ? 0.f : m[i]));
+          const float b = ex2_approx(x[c + 1] - (m[i + 1] == -INFINITY ? 0.f : m[i + 1]));
+          l[i] += a;
+          l[i + 1] += b;
+          // P enters the tensor cores in bf16, as in the dense forward; l is summed before the rounding
+          __nv_bfloat162 pair = __floats2bfloat162_rn(a, b);
+          pk[i / 2] = *reinterpret_cast<uint32_t *>(&pair);
+        }
       }
       // the product of the tile before has read P
       if (j > 0)
@@ -352,47 +382,52 @@ __device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narr
     }
     ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::kPvDone), (step - 1) & 1u, abort_flag, err));
     tc_fence_after();
-    // l over the keys: the warps' sums through shared memory
+    // l over the keys, and from it each row's factor and lse
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      float s = l[c];
+    for (int h = 0; h < C; h += 16) {
+      float y[16];
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      l[c] = s;
-    }
-    named_bar_sync(id, 128);  // red has been read
-    if (lane == 0) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) red[w * C + c] = l[c];
+      for (int c = 0; c < 16; ++c) y[c] = l[h + c];
+      const float s = reduce16(y, sum_of);
+      if (!(lane & 1)) red[w * C + h + (lane >> 1)] = s;
     }
     if (!named_bar_and(id, 128, ok)) return;
-#pragma unroll
-    for (int c = 0; c < C; ++c) l[c] = (red[c] + red[C + c]) + (red[2 * C + c] + red[3 * C + c]);
-    uint32_t v[C];
-    if constexpr (C == 16) tmem_ld16(o_addr, v);
-    else tmem_ld32(o_addr, v);
-    tmem_ld_wait(v);
-    const size_t part = static_cast<size_t>(max(g.slot, 0)) * p.part_rows;
+    const size_t part = static_cast<size_t>(max(g.slot, 0)) * p.part_rows + col0;
+    if (key < C) {
+      const float sum = (red[key] + red[C + key]) + (red[2 * C + key] + red[3 * C + key]);
+      factor[key] = sum > 0.f ? 1.f / sum : 0.f;
+      if (col0 + key < rows) {
+        const float lse = sum > 0.f ? (ref[key] + log2f(sum)) * kLn2 : -INFINITY;
+        const int tok = (col0 + key) / p.G, head = g.h * p.G + (col0 + key) - tok * p.G;
+        if (g.slot >= 0) p.part_lse[part + key] = lse;
+        else if (p.lse) p.lse[static_cast<size_t>(head) * p.total_q + g.s.q0 + tok] = lse;
+      }
+    }
+    named_bar_sync(id, 128);
+    // a thread has column `key` of O, one row after the other
+    const int n_rows = min(C, rows - col0);
     int tok = col0 / p.G, head = col0 - tok * p.G;
+    float *to_part = p.part_o + part * D + key;
+    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.o) + (g.h * p.G + head) * p.o_h + (g.s.q0 + tok) * p.o_s + key;
+#pragma unroll 1
+    for (int h = 0; h < n_rows; h += 8) {
+      uint32_t v[8];
+      tmem_ld8(o_addr + h, v);
+      tmem_ld_wait(v);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (col0 + c < rows) {
-        const float inv = l[c] > 0.f ? 1.f / l[c] : 0.f;
-        const float o = __uint_as_float(v[c]) * inv;
-        const float lse = l[c] > 0.f ? (m[c] + log2f(l[c])) * kLn2 : -INFINITY;
-        if (g.slot >= 0) {
-          if (key < D) p.part_o[(part + col0 + c) * D + key] = o;
-          if (key == c) p.part_lse[part + col0 + c] = lse;
-        } else {
-          const int h = g.h * p.G + head, row = g.s.q0 + tok;
-          if (key < D) static_cast<__nv_bfloat16 *>(p.o)[h * p.o_h + row * p.o_s + key] = __float2bfloat16_rn(o);
-          if (key == c && p.lse) p.lse[static_cast<size_t>(h) * p.total_q + row] = lse;
+      for (int c = 0; c < 8; ++c) {
+        if (h + c < n_rows && key < D) {
+          const float o = __uint_as_float(v[c]) * factor[h + c];
+          if (g.slot >= 0) to_part[(h + c) * D] = o;
+          else *to = __float2bfloat16_rn(o);
+        }
+        to += p.o_h;
+        if (++head == p.G) {
+          head = 0;
+          to += p.o_s - p.G * p.o_h;
         }
       }
-      if (++head == p.G) {
-        head = 0;
-        ++tok;
-      }
+      __syncwarp();
     }
   }
 }
