@@ -44,14 +44,14 @@ struct Cfg {
   static constexpr int kStages = 131072 / kTileBytes;
   static constexpr int kNumBarriers = 2 + 2 * kStages + 7;
   // tiles of the wide form (Q, ring) or of the narrow one (ring, P, Q), then
-  // barriers, three words, warp sums, the range's start, the narrow form's
+  // barriers, three words, warp sums, the first segment, the narrow form's
   // reductions, prefix sums
   static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 2 * 16 * D * 2;
   static_assert(2 * kTileBytes + kStages * kTileBytes <= kAreaBytes, "wide layout");
   static constexpr int kMaxBarriers = 2 * (196608 / kTileBytes) + 10;
   static constexpr int kRedFloats = 2 * 6 * 32;
   static constexpr int kSmemBytes =
-      1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 24 + 32 + 4 * kRedFloats + 4 * (kPagedMaxSeqs + 1);
+      1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 24 + 48 + 4 * kRedFloats + 4 * (kPagedMaxSeqs + 1);
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -192,49 +192,23 @@ __device__ __forceinline__ const int *page_row(const PagedAttnParams &p, const S
   return p.cache.page_table + g.b * p.cache.table_stride;
 }
 
-// Where a CTA's range begins, found once by its producer warp and read by every role.
-struct Start {
-  Place at;
-  Seq s;
-};
-
-// Walks the segments of this CTA's range of tiles in order; every role walks its
-// own. One copy of the code for all roles: what runs once per CTA costs its
-// instruction fetches more than its work.
+// Walks the segments of a CTA's range of tiles in order; every role walks its own.
+// The first one is found once, by the producer warp, and read by every role from
+// shared memory; the code for the others is one copy for all roles: what runs
+// once per CTA costs its instruction fetches more than its work.
 struct Walk {
   int pos, end, per;
   const int *prefix;
-  const Start *start;
-  Place at;
+  const Segment *first;
   bool fresh;
-  __device__ __forceinline__ Walk(const int *prefix_, const Start *start_, int B, int n_ctas)
-      : prefix(prefix_), start(start_), fresh(true) {
+  __device__ __forceinline__ Walk(const int *prefix_, const Segment *first_, int B, int n_ctas)
+      : prefix(prefix_), first(first_), fresh(true) {
     per = tiles_per_cta(prefix[B], n_ctas);
     pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(prefix[B])));
     end = static_cast<int>(min(static_cast<long long>(pos) + per, static_cast<long long>(prefix[B])));
   }
-  __device__ __noinline__ bool next(const PagedAttnParams &p, Segment &g) {
-    if (pos >= end) return false;
-    if (fresh) {
-      at = start->at;
-      g.s = start->s;
-      fresh = false;
-    } else {
-      // the item after the last one, skipping those that see no key
-      if (++at.rb >= row_blocks(p, g.s)) {
-        at.rb = 0;
-        if (++at.h >= p.cache.Hkv) {
-          at.h = 0;
-          do ++at.b;
-          while (at.b < p.cache.B && prefix[at.b + 1] == prefix[at.b]);
-          if (at.b >= p.cache.B) return false;
-          g.s = sequence(p, at.b);
-        }
-      }
-      const int rbs = row_blocks(p, g.s);
-      while (at.rb < rbs && item_tiles(p, g.s, at.rb) == 0) ++at.rb;
-      at.r = 0;
-    }
+  // The segment at position `pos` of the line, which is tile at.r of its item.
+  __device__ __forceinline__ bool make(const PagedAttnParams &p, const Place &at, Segment &g) const {
     // (the bounds on b and rb only matter when the lengths change during the
     // call, which must not happen: then the walk ends instead of running on)
     const int n = at.rb < row_blocks(p, g.s) ? item_tiles(p, g.s, at.rb) : 0;
@@ -246,6 +220,34 @@ struct Walk {
     g.j1 = min(n, at.r + (end - pos));
     g.slot = g.j0 == 0 && g.j1 == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (g.j0 == 0 ? 1 : 0);
     g.last_cta = (pos - g.j0 + n - 1) / per;
+    return true;
+  }
+  __device__ __forceinline__ bool next(const PagedAttnParams &p, Segment &g) {
+    if (pos >= end) return false;
+    if (fresh) {
+      g = *first;
+      fresh = false;
+      pos += g.j1 - g.j0;
+      return g.j1 > g.j0;
+    }
+    return next_item(p, g);
+  }
+  __device__ __noinline__ bool next_item(const PagedAttnParams &p, Segment &g) {
+    // the item after the last one, skipping those that see no key
+    Place at{g.b, g.h, g.rb + 1, 0};
+    if (at.rb >= row_blocks(p, g.s)) {
+      at.rb = 0;
+      if (++at.h >= p.cache.Hkv) {
+        at.h = 0;
+        do ++at.b;
+        while (at.b < p.cache.B && prefix[at.b + 1] == prefix[at.b]);
+        if (at.b >= p.cache.B) return false;
+        g.s = sequence(p, at.b);
+      }
+    }
+    const int rbs = row_blocks(p, g.s);
+    while (at.rb < rbs && item_tiles(p, g.s, at.rb) == 0) ++at.rb;
+    if (!make(p, at, g)) return false;
     pos += g.j1 - g.j0;
     return true;
   }
@@ -725,8 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *turn = reinterpret_cast<volatile int *>(tmem_slot + 2);  // next MMA burst slot (wide)
   int *warp_sums = reinterpret_cast<int *>(tmem_slot + 4);
-  Start *start = reinterpret_cast<Start *>(warp_sums + 24);
-  float *red = reinterpret_cast<float *>(warp_sums + 32);
+  Segment *first = reinterpret_cast<Segment *>(warp_sums + 24);
+  float *red = reinterpret_cast<float *>(warp_sums + 36);
   int *prefix = reinterpret_cast<int *>(red + C::kRedFloats);
   const uint32_t bar0 = smem_addr(bars), base = smem_addr(smem);
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -740,13 +742,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int most = prefix_tiles(p, prefix, warp_sums);
   const bool narrow = most * p.G <= 64;
   const L sh(most * p.G, p.G);
-  const Walk walk(prefix, start, p.cache.B, gridDim.x);
+  const Walk walk(prefix, first, p.cache.B, gridDim.x);
   int first_entry = -1;  // the producer's lanes: the first key tile's pages
   if (warp == kTmaWarp && walk.pos < walk.end) {
-    Start s;
-    s.at = place_of(p, prefix, walk.pos, s.s);
-    first_entry = page_entry(p, p.cache.page_table + s.at.b * p.cache.table_stride, s.s.kv_len, s.at.r, lane);
-    if (lane == 0) *start = s;
+    Segment g;
+    const Place at = place_of(p, prefix, walk.pos, g.s);
+    if (!walk.make(p, at, g)) g.j0 = g.j1 = 0;
+    else first_entry = page_entry(p, page_row(p, g), g.s.kv_len, g.j0, lane);
+    if (lane == 0) *first = g;
   }
   if (threadIdx.x == 0) {
     if (narrow) {

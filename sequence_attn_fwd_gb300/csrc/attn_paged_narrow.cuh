@@ -229,6 +229,10 @@ __device__ __forceinline__ float reduce16(float (&v)[16], Op op) {
   return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
+// The reference of a column that has seen no key: any score passes it, and
+// 2^(-inf - it) is still 0.
+constexpr float kNoReference = -1e30f;
+
 // Softmax and epilogue of columns [col0, col0 + C) of S^T: one thread per key
 // (and, in the epilogue, per column of O). `red` is this warpgroup's 6 x C
 // floats of shared memory, `gi` its number. Every warp goes through the same
@@ -262,10 +266,10 @@ __device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narr
     float m[C], l[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      m[c] = -INFINITY;
+      m[c] = kNoReference;
       l[c] = 0.f;
     }
-    if (key < C) ref[key] = -INFINITY;
+    if (key < C) ref[key] = kNoReference;
     int entry = entry_of(g.j0);
     bool ok = true;
     for (int j = 0; j < n; ++j, ++step) {
@@ -276,13 +280,19 @@ __device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narr
                             mbar_wait(bar(L::kSFull + (step & 1u)), (step >> 1) & 1u, abort_flag, err));
       tc_fence_after();
       const bool partly = kv0 + kRowsPerTile - 1 > first_last;  // some row does not see all keys of the tile
-      // 16 columns from h on of this key's scores, times scale log2(e), masked
-      auto load_scores = [&](int h, float(&x)[16]) {
+      const bool holes = __any_sync(0xffffffffu, !there);
+      // 16 columns from h on of this key's scores times scale log2(e), masked,
+      // less the columns' references
+      auto load_scores = [&](int h, const float *less, float *x) {
         uint32_t raw[16];
         tmem_ld16(tmem + lane_off + (step & 1u) * sh.N + col0 + h, raw);
         tmem_ld_wait(raw);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) x[c] = there ? __uint_as_float(raw[c]) * c2 : -INFINITY;
+        for (int c = 0; c < 16; ++c) x[c] = fmaf(__uint_as_float(raw[c]), c2, less ? -less[c] : 0.f);
+        if (holes) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) x[c] = there ? x[c] : -INFINITY;
+        }
         if (partly) {
           int tok = (col0 + h) / p.G, head = col0 + h - tok * p.G;
 #pragma unroll
@@ -296,31 +306,29 @@ __device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narr
           }
         }
       };
-      float x[16];
-      bool move = false;
+      float x[C];
+      float top = -INFINITY;
 #pragma unroll
       for (int h = 0; h < C; h += 16) {
-        load_scores(h, x);
+        load_scores(h, m + h, x + h);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) move = move || x[c] > m[h + c] + 8.f;
+        for (int c = 0; c < 16; c += 2) top = fmax3(top, x[h + c], x[h + c + 1]);
       }
-      if (!named_bar_and(id, 128, ok && !move)) {
+      if (!named_bar_and(id, 128, ok && !(top > 8.f))) {
         // maxima of the tile's 128 keys, then O and l onto the new reference
 #pragma unroll
         for (int h = 0; h < C; h += 16) {
-          if (C > 16) load_scores(h, x);
           float y[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) y[c] = x[c];
-          const float top = reduce16(y, larger);
-          if (!(lane & 1)) red[w * C + h + (lane >> 1)] = top;
+          load_scores(h, nullptr, y);
+          const float most = reduce16(y, larger);
+          if (!(lane & 1)) red[w * C + h + (lane >> 1)] = most;
         }
         named_bar_sync(id, 128);
         if (key < C) {
-          const float top = fmaxf(fmaxf(red[key], red[C + key]), fmaxf(red[2 * C + key], red[3 * C + key]));
-          const float old_ref = ref[key], new_ref = fmaxf(old_ref, top);
+          const float most = fmaxf(fmaxf(red[key], red[C + key]), fmaxf(red[2 * C + key], red[3 * C + key]));
+          const float old_ref = ref[key], new_ref = fmaxf(old_ref, most);
           ref[key] = new_ref;
-          factor[key] = new_ref == -INFINITY ? 1.f : ex2_approx(old_ref - new_ref);
+          factor[key] = ex2_approx(old_ref - new_ref);
         }
         ok = named_bar_and(id, 128, ok);
         if (ok && j > 0)
@@ -342,24 +350,19 @@ __device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narr
             v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
           }
           if (old) tmem_st16(o_addr + h, v);
+          load_scores(h, m + h, x + h);
         }
         if (old) tmem_st_wait();
       }
       uint32_t pk[C / 2];
 #pragma unroll
-      for (int h = 0; h < C; h += 16) {
-        if (C > 16) load_scores(h, x);
-#pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          const int i = h + c;
-          const float a = ex2_approx(x[c] - (m[i] == -INFINITY ? 0.f : m[i]));
-          const float b = ex2_approx(x[c + 1] - (m[i + 1] == -INFINITY ? 0.f : m[i + 1]));
-          l[i] += a;
-          l[i + 1] += b;
-          // P enters the tensor cores in bf16, as in the dense forward; l is summed before the rounding
-          __nv_bfloat162 pair = __floats2bfloat162_rn(a, b);
-          pk[i / 2] = *reinterpret_cast<uint32_t *>(&pair);
-        }
+      for (int i = 0; i < C; i += 2) {
+        const float a = ex2_approx(x[i]), b = ex2_approx(x[i + 1]);
+        l[i] += a;
+        l[i + 1] += b;
+        // P enters the tensor cores in bf16, as in the dense forward; l is summed before the rounding
+        __nv_bfloat162 pair = __floats2bfloat162_rn(a, b);
+        pk[i / 2] = *reinterpret_cast<uint32_t *>(&pair);
       }
       // the product of the tile before has read P
       if (j > 0)
