@@ -166,10 +166,10 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
   if (!isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   const int G = Hq / cache->Hkv, D = cache->D;
   if (G > 128 || total_q > kMaxKeys) return ATTN_ERR_UNSUPPORTED;
-  // the key tiles of all items are counted in 32 bits
+  // the key tiles of all items, and a few more each, are counted in 32 bits
   const long long items = (static_cast<long long>(total_q) / (2 * (128 / G)) + cache->B) * cache->Hkv;
   const long long tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 127) / 128;
-  if (tiles > 0 && items > 0x7fffffffll / tiles) return ATTN_ERR_UNSUPPORTED;
+  if (items > 0x7fffffffll / (tiles + 16)) return ATTN_ERR_UNSUPPORTED;
   if (cache->B == 0 || total_q == 0) return ATTN_OK;
   if (!q || !o || !workspace || !aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 16) || !aligned(lse, 4))
     return ATTN_ERR_INVALID_ARG;

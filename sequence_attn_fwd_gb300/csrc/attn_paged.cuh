@@ -9,9 +9,9 @@
 // rows of one tile: row r of a tile is token r / G, head r % G, `tok` whole
 // tokens per 128-row tile (one TMA box of a 4-D view lays them out). A work
 // item is two such tiles of one (sequence, KV head); its cost is the number
-// of 128-key tiles its last token sees. The key tiles of all items, put end
-// to end, are cut into equal ranges, one per CTA, whatever the lengths: every
-// CTA has the same work to within one tile. An item inside one range is
+// of 128-key tiles its last token sees and a constant. The costs of all items,
+// put end to end, are cut into equal ranges, one per CTA, whatever the lengths:
+// every CTA has the same work to within one tile. An item inside one range is
 // written directly; an item that ranges cut leaves one fp32 partial per range
 // (normalised, with its log-sum-exp) in the workspace, at most two per CTA,
 // and a second kernel merges them in the order of the keys. The cuts follow
@@ -98,22 +98,31 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
   return sum;
 }
 
-// Key tiles of the items before row block `rb` of one KV head of a sequence.
-__device__ __forceinline__ long long tiles_before(const PagedAttnParams &p, const Seq &s, int rb) {
+// The cost of an item is its key tiles and kItemCost more, for what comes once
+// per item: Q, the first scores' and the last product's way through the empty
+// pipeline, the epilogue (14,000 to 18,000 clocks measured on items of 4 tiles,
+// of 3,600 to 4,500 each). An item that sees no key costs nothing.
+constexpr int kItemCost = 4;
+__device__ __forceinline__ int item_cost(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
+
+// Cost of the items before row block `rb` of one KV head of a sequence.
+__device__ __forceinline__ long long cost_before(const PagedAttnParams &p, const Seq &s, int rb) {
   if (rb <= 0 || s.kv_len <= 0) return 0;
   const int rbs = row_blocks(p, s);
-  if (!p.causal) return static_cast<long long>(min(rb, rbs)) * tiles_seen(p, s, s.q_len);
+  rb = min(rb, rbs);
+  if (rbs == 1) return item_cost(tiles_seen(p, s, s.q_len));
+  if (!p.causal) return static_cast<long long>(rb) * item_cost(tiles_seen(p, s, s.q_len));
   // row block i < rbs - 1 sees ceil((c + i w) / 128) tiles, w = 2 tok rows, where c + i w > 0
   const int w = 2 * p.tok, n = min(rb, rbs - 1);
   const long long c = static_cast<long long>(s.kv_len) - s.q_len + w;
   long long sum = 0;
   const long long first = c > 0 ? 0 : (-c) / w + 1;  // first block that sees a key
-  if (first < n) sum = floor_sum(n - first, kRowsPerTile, w, c + first * w + kRowsPerTile - 1);
-  if (rb >= rbs) sum += tiles_seen(p, s, s.q_len);
+  if (first < n) sum = floor_sum(n - first, kRowsPerTile, w, c + first * w + kRowsPerTile - 1) + (n - first) * kItemCost;
+  if (rb == rbs) sum += item_cost(tiles_seen(p, s, s.q_len));
   return sum;
 }
 
-// prefix[0 .. B]: key tiles of all KV heads of the sequences before each, by
+// prefix[0 .. B]: cost of all KV heads of the sequences before each, by
 // every thread of the CTA; returns the most new tokens of a sequence. warp_sums
 // has 24 entries.
 __device__ __forceinline__ int prefix_tiles(const PagedAttnParams &p, int *prefix, int *warp_sums) {
@@ -125,7 +134,7 @@ __device__ __forceinline__ int prefix_tiles(const PagedAttnParams &p, int *prefi
     const Seq s = sequence(p, b);
     most = max(most, s.q_len);
     prefix[b] = sum;
-    if (s.q_len > 0) sum += static_cast<int>(tiles_before(p, s, row_blocks(p, s))) * p.cache.Hkv;
+    if (s.q_len > 0) sum += static_cast<int>(cost_before(p, s, row_blocks(p, s))) * p.cache.Hkv;
   }
   int incl = sum;
 #pragma unroll
@@ -148,7 +157,7 @@ __device__ __forceinline__ int prefix_tiles(const PagedAttnParams &p, int *prefi
   return most;
 }
 
-// The sequence whose range of tiles has `pos`.
+// The sequence whose range of the line of all costs has `pos`.
 __device__ __forceinline__ int seq_of(const int *prefix, int B, int pos) {
   int lo = 0, hi = B - 1;
   while (lo < hi) {
@@ -159,10 +168,10 @@ __device__ __forceinline__ int seq_of(const int *prefix, int B, int pos) {
   return lo;
 }
 
-// Key tiles per CTA of a launch of n_ctas.
-__device__ __forceinline__ int tiles_per_cta(int total, int n_ctas) { return total / n_ctas + (total % n_ctas != 0); }
+// Cost per CTA of a launch of n_ctas.
+__device__ __forceinline__ int cost_per_cta(int total, int n_ctas) { return total / n_ctas + (total % n_ctas != 0); }
 
-// An item and the tile within it at a position of the line of all tiles.
+// An item and the cost before a position within it.
 struct Place {
   int b, h, rb, r;
 };
@@ -174,28 +183,29 @@ __device__ __forceinline__ Place place_of(const PagedAttnParams &p, const int *p
   int rest = off - h * per_head, rb = 0;
   const int rbs = row_blocks(p, s);
   for (; rb < rbs; ++rb) {
-    const int n = item_tiles(p, s, rb);
+    const int n = item_cost(item_tiles(p, s, rb));
     if (rest < n) break;
     rest -= n;
   }
   return {b, h, rb, rest};
 }
 
-// A CTA's part of one work item: key tiles [j0, j1) of row block rb.
+// A CTA's part of one work item: key tiles [j0, j1) of row block rb. The first
+// kItemCost units of an item's stretch of the line stand for no tile.
 struct Segment {
   Seq s;
-  int b, h, rb, j0, j1;
+  int b, rbs, h, rb, j0, j1;  // rbs: row blocks of the sequence
   int slot;  // partial written, -1: the whole item, written directly
-  int last_cta;  // the CTA that has the item's last tile
+  int next;  // position of the line behind the segment
 };
 __device__ __forceinline__ const int *page_row(const PagedAttnParams &p, const Segment &g) {
   return p.cache.page_table + g.b * p.cache.table_stride;
 }
 
-// Walks the segments of a CTA's range of tiles in order; every role walks its own.
-// The first one is found once, by the producer warp, and read by every role from
-// shared memory; the code for the others is one copy for all roles: what runs
-// once per CTA costs its instruction fetches more than its work.
+// Walks the segments of a CTA's range of the line in order; every role walks its
+// own. The first one is found once, by the producer warp, and read by every role
+// from shared memory; the code for the others is one copy for all roles: what
+// runs once per CTA costs its instruction fetches more than its work.
 struct Walk {
   int pos, end, per;
   const int *prefix;
@@ -203,53 +213,58 @@ struct Walk {
   bool fresh;
   __device__ __forceinline__ Walk(const int *prefix_, const Segment *first_, int B, int n_ctas)
       : prefix(prefix_), first(first_), fresh(true) {
-    per = tiles_per_cta(prefix[B], n_ctas);
+    per = cost_per_cta(prefix[B], n_ctas);
     pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(prefix[B])));
     end = static_cast<int>(min(static_cast<long long>(pos) + per, static_cast<long long>(prefix[B])));
   }
-  // The segment at position `pos` of the line, which is tile at.r of its item.
-  __device__ __forceinline__ bool make(const PagedAttnParams &p, const Place &at, Segment &g) const {
-    // (the bounds on b and rb only matter when the lengths change during the
-    // call, which must not happen: then the walk ends instead of running on)
-    const int n = at.rb < row_blocks(p, g.s) ? item_tiles(p, g.s, at.rb) : 0;
-    if (n <= at.r) return false;
-    g.b = at.b;
-    g.h = at.h;
-    g.rb = at.rb;
-    g.j0 = at.r;
-    g.j1 = min(n, at.r + (end - pos));
+  // The segment of row block rb at cost `within` of it, which is position `pos`
+  // (j0 == j1 if the range ends before its first tile).
+  __device__ __forceinline__ void make(const PagedAttnParams &p, int rb, int within, Segment &g) const {
+    const int n = item_tiles(p, g.s, rb), stop = min(n + kItemCost, within + (end - pos));
+    g.rb = rb;
+    g.j0 = max(0, within - kItemCost);
+    g.j1 = max(g.j0, stop - kItemCost);
     g.slot = g.j0 == 0 && g.j1 == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (g.j0 == 0 ? 1 : 0);
-    g.last_cta = (pos - g.j0 + n - 1) / per;
-    return true;
+    g.next = pos + (stop - within);
   }
   __device__ __forceinline__ bool next(const PagedAttnParams &p, Segment &g) {
     if (pos >= end) return false;
     if (fresh) {
       g = *first;
       fresh = false;
-      pos += g.j1 - g.j0;
-      return g.j1 > g.j0;
+      pos = g.next;
+      if (g.j1 > g.j0) return true;
     }
     return next_item(p, g);
   }
   __device__ __noinline__ bool next_item(const PagedAttnParams &p, Segment &g) {
-    // the item after the last one, skipping those that see no key
-    Place at{g.b, g.h, g.rb + 1, 0};
-    if (at.rb >= row_blocks(p, g.s)) {
-      at.rb = 0;
-      if (++at.h >= p.cache.Hkv) {
-        at.h = 0;
-        do ++at.b;
-        while (at.b < p.cache.B && prefix[at.b + 1] == prefix[at.b]);
-        if (at.b >= p.cache.B) return false;
-        g.s = sequence(p, at.b);
+    while (pos < end) {
+      // the item after the last one, skipping those that see no key
+      int rb = g.rb + 1;
+      if (rb >= g.rbs) {
+        rb = 0;
+        if (++g.h >= p.cache.Hkv) {
+          g.h = 0;
+          do ++g.b;
+          while (g.b < p.cache.B && prefix[g.b + 1] == prefix[g.b]);
+          if (g.b >= p.cache.B) return false;
+          g.s = sequence(p, g.b);
+          g.rbs = row_blocks(p, g.s);
+        }
       }
+      // (the bounds on b and rb only matter when the lengths change during the
+      // call, which must not happen: then the walk ends instead of running on)
+      while (rb < g.rbs && item_tiles(p, g.s, rb) == 0) ++rb;
+      if (rb >= g.rbs) return false;
+      make(p, rb, 0, g);
+      pos = g.next;
+      if (g.j1 > g.j0) return true;
     }
-    const int rbs = row_blocks(p, g.s);
-    while (at.rb < rbs && item_tiles(p, g.s, at.rb) == 0) ++at.rb;
-    if (!make(p, at, g)) return false;
-    pos += g.j1 - g.j0;
-    return true;
+    return false;
+  }
+  // The last CTA of an item that this one begins with segment g.
+  __device__ __forceinline__ int last_cta(const PagedAttnParams &p, const Segment &g) const {
+    return (g.next - (g.j1 + kItemCost) + item_tiles(p, g.s, g.rb) + kItemCost - 1) / per;
   }
   // Key tiles of segment g that query tile t goes through, counted from g.j0.
   static __device__ __forceinline__ int tiles(const PagedAttnParams &p, const Segment &g, int t) {
@@ -332,7 +347,8 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
   const int tok = (2 * g.rb + t) * p.tok + r / p.G;  // within the sequence
   const bool row_valid = r < p.tok * p.G && tok < g.s.q_len;
   const bool warp_valid = __any_sync(0xffffffffu, row_valid);
-  const int row_last = !row_valid ? -1 : (p.causal ? g.s.kv_len - g.s.q_len + tok : g.s.kv_len - 1);
+  // rows of no token (zeros, or other sequences' rows) see every key: nothing of them is written
+  const int row_last = row_valid && p.causal ? g.s.kv_len - g.s.q_len + tok : g.s.kv_len - 1;
   const float c2 = p.scale_log2;
   PageBits bits(p);
   float m = -INFINITY, l = 0.f;
@@ -377,7 +393,7 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
       if (j > 0) {
         // as in the dense forward: the reference moves, and O with it, only
         // when the tile's P would sum to more than 2^8 or there is none yet
-        const bool big = !(rowsum <= kRescaleSum) || (m == -INFINITY && rowsum > 0.f);
+        const bool big = row_valid && (!(rowsum <= kRescaleSum) || (m == -INFINITY && rowsum > 0.f));
         if (__any_sync(0xffffffffu, big)) {
           float mx = -INFINITY;  // 32 columns at a time: few live registers
 #pragma unroll 1
@@ -529,7 +545,7 @@ __device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, 
   int4 cut = make_int4(0, 0, 0, 0);
   while (ok && walk.next(p, g)) {
     if (g.j0 == 0 && g.slot >= 0)
-      cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, g.last_cta);
+      cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, walk.last_cta(p, g));
     const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
     const bool two = Walk::tiles(p, g, 1) > 0;
     const int *row = page_row(p, g);
@@ -684,8 +700,11 @@ __device__ __noinline__ void wide_softmax(const PagedAttnParams &p, Walk walk, i
   const uint32_t lane_off = static_cast<uint32_t>(r & ~31) << 16;
   int steps = 0, ring = 0;
   uint32_t u = 0;
-  Segment g;
-  while (walk.next(p, g)) {
+  Segment g, ahead;  // the next segment is found before this one's first scores are there
+  bool more = walk.next(p, ahead);
+  while (more) {
+    g = ahead;
+    more = walk.next(p, ahead);
     const int n = Walk::tiles(p, g, t), n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
     if (!softmax_segment<D>(p, g, t, n, r, s_column(tmem, t) + lane_off, o_column(tmem, t) + lane_off,
                             bar(W::kSFull + t), bar(W::kPFull + t), bar(W::kOFull + t), bar(W::kFull), sRing, ring, steps,
@@ -747,8 +766,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kTmaWarp && walk.pos < walk.end) {
     Segment g;
     const Place at = place_of(p, prefix, walk.pos, g.s);
-    if (!walk.make(p, at, g)) g.j0 = g.j1 = 0;
-    else first_entry = page_entry(p, page_row(p, g), g.s.kv_len, g.j0, lane);
+    g.b = at.b;
+    g.h = at.h;
+    g.rbs = row_blocks(p, g.s);
+    walk.make(p, at.rb, at.r, g);
+    first_entry = page_entry(p, page_row(p, g), g.s.kv_len, g.j0, lane);
     if (lane == 0) *first = g;
   }
   if (threadIdx.x == 0) {
@@ -785,10 +807,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     *turn = 0;
     fence_barrier_init();
   }
-  if (narrow) {
+  {
     // rows of Q that no token fills: zeros, not whatever was there
-    for (int i = threadIdx.x; i < sh.q_bufs * sh.q_bytes() / 16; i += kThreads)
-      st_shared_v4(base + sh.q_at() + 16 * i, 0u, 0u, 0u, 0u);
+    const uint32_t at = base + (narrow ? sh.q_at() : 0);
+    const int pieces = (narrow ? sh.q_bufs * sh.q_bytes() : 2 * C::kTileBytes) / 16;
+    for (int i = threadIdx.x; i < pieces; i += kThreads) st_shared_v4(at + 16 * i, 0u, 0u, 0u, 0u);
     fence_proxy_async_shared();
   }
   tc_fence_before();

@@ -85,7 +85,7 @@ __device__ __noinline__ void narrow_producer(const PagedAttnParams &p, const Nar
   Segment g;
   int4 cut = make_int4(0, 0, 0, 0);
   while (ok && walk.next(p, g)) {
-    if (g.j0 == 0 && g.slot >= 0) cut = make_int4(g.s.q0, g.s.q_len * p.G, g.h, g.last_cta);
+    if (g.j0 == 0 && g.slot >= 0) cut = make_int4(g.s.q0, g.s.q_len * p.G, g.h, walk.last_cta(p, g));
     const int n = g.j1 - g.j0;
     const int *row = page_row(p, g);
     // n_pages (read as zeros) where there is none
