@@ -43,11 +43,11 @@ struct Cfg {
   static constexpr int kTileBytes = kRowsPerTile * D * 2;
   static constexpr int kStages = 131072 / kTileBytes;
   static constexpr int kNumBarriers = 2 + 2 * kStages + 7;
-  // tiles of the wide form (Q, ring) or of the narrow one (ring, P, Q), then
+  // tiles of the wide form (Q, ring, epilogue) or of the narrow one (ring, P, Q), then
   // barriers, three words, warp sums, the first segment, the narrow form's
   // reductions, prefix sums
   static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 2 * 16 * D * 2;
-  static_assert(2 * kTileBytes + kStages * kTileBytes <= kAreaBytes, "wide layout");
+  static_assert(2 * kTileBytes + kStages * kTileBytes + 8 * 2560 <= kAreaBytes, "wide layout");
   static constexpr int kMaxBarriers = 2 * (196608 / kTileBytes) + 10;
   static constexpr int kRedFloats = 2 * 6 * 32;
   static constexpr int kSmemBytes =
@@ -283,24 +283,31 @@ __device__ __forceinline__ int page_entry(const PagedAttnParams &p, const int *r
   return (i << p.page_log2) < kv_len ? row[i] : -1;
 }
 
-// The pages of a key tile and which of them are there. Each lane of a warp
-// looks one up ahead of time; `mask` then has one bit per page.
+// Which pages of a segment's key tiles are there: each lane of a warp looks one
+// up a tile ahead; `mask` has one bit per page of the tile (set past them).
 struct PageBits {
-  int per_tile;  // pages of a key tile, 1 if a page has 128 keys or more
-  int entry;     // this lane's entry of the next tile
-  __device__ __forceinline__ PageBits(const PagedAttnParams &p)
-      : per_tile(p.page_log2 < 7 ? kRowsPerTile >> p.page_log2 : 1), entry(0) {}
-  __device__ __forceinline__ void look_up(const PagedAttnParams &p, const Segment &g, int j) {
-    const int lane = threadIdx.x & 31;
-    entry = 0;
-    if (lane < per_tile) {
-      const int i = p.page_log2 < 7 ? j * per_tile + lane : (j * kRowsPerTile) >> p.page_log2;
-      if ((i << p.page_log2) < g.s.kv_len) entry = page_row(p, g)[i];
-    }
+  const int *at;    // this lane's entry of the tile after the next
+  int left;         // its distance to the end of the sequence's pages
+  int entry;        // of the next tile
+  __device__ __forceinline__ PageBits(const PagedAttnParams &p, const Segment &g) {
+    const bool small = p.page_log2 < 7;
+    const int lane = threadIdx.x & 31, per_tile = small ? kRowsPerTile >> p.page_log2 : 1;
+    const int first = small ? g.j0 * per_tile + lane : (g.j0 * kRowsPerTile) >> p.page_log2;
+    const int pages = (g.s.kv_len + (1 << p.page_log2) - 1) >> p.page_log2;
+    at = page_row(p, g) + first;
+    left = lane < per_tile ? pages - first : 0;
+    entry = left > 0 ? *at : 0;
   }
-  __device__ __forceinline__ unsigned mask(const PagedAttnParams &p) const {
-    const int lane = threadIdx.x & 31;
-    return __ballot_sync(0xffffffffu, lane >= per_tile || (entry >= 0 && entry < p.cache.n_pages));
+  // The mask of key tile j; then on to the next.
+  __device__ __forceinline__ unsigned next(const PagedAttnParams &p, int j) {
+    const unsigned mask = __ballot_sync(0xffffffffu, static_cast<unsigned>(entry) < static_cast<unsigned>(p.cache.n_pages));
+    const bool small = p.page_log2 < 7;
+    const int step = small ? kRowsPerTile >> p.page_log2
+                           : (((j + 1) * kRowsPerTile & ((1 << p.page_log2) - 1)) == 0 ? 1 : 0);
+    at += step;
+    left -= step;
+    entry = left > 0 ? *at : 0;
+    return mask;
   }
 };
 
@@ -342,40 +349,40 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
                                                 uint32_t s_addr, uint32_t o_addr, uint32_t bar_sfull,
                                                 uint32_t bar_pfull, uint32_t bar_ofull, uint32_t bar_full0,
                                                 uint32_t ring_base, int ring, int step_base, uint32_t ofull_parity,
+                                                uint32_t stage, Walk &walk, Segment &ahead, bool &more,
                                                 volatile int *abort_flag, int *err) {
   const int lane = threadIdx.x & 31;
   const int tok = (2 * g.rb + t) * p.tok + r / p.G;  // within the sequence
   const bool row_valid = r < p.tok * p.G && tok < g.s.q_len;
-  const bool warp_valid = __any_sync(0xffffffffu, row_valid);
   // rows of no token (zeros, or other sequences' rows) see every key: nothing of them is written
   const int row_last = row_valid && p.causal ? g.s.kv_len - g.s.q_len + tok : g.s.kv_len - 1;
   const float c2 = p.scale_log2;
-  PageBits bits(p);
+  const int tile_last = p.causal ? g.s.kv_len - g.s.q_len + (2 * g.rb + t) * p.tok : g.s.kv_len - 1;  // of its first token
+  const bool warp_valid = __any_sync(0xffffffffu, row_valid);
+  PageBits bits(p, g);
   float m = -INFINITY, l = 0.f;
   bool ok = true;
-  if (warp_valid && n > 0) bits.look_up(p, g, g.j0);
 
   for (int j = 0; j < n; ++j) {
-    const unsigned now = warp_valid ? bits.mask(p) : 0xffffffffu;
-    if (warp_valid && j + 1 < n) bits.look_up(p, g, g.j0 + j + 1);
+    const unsigned there = bits.next(p, g.j0 + j);
     ok = __all_sync(0xffffffffu, mbar_wait(bar_sfull, static_cast<uint32_t>(step_base + j) & 1u, abort_flag, err));
     if (!ok) break;
     tc_fence_after();
     const int kv0 = (g.j0 + j) * kRowsPerTile;
     if (warp_valid) {
-      const int last = max(-1, min(row_last - kv0, kRowsPerTile - 1));
-      const bool cut = __any_sync(0xffffffffu, last < kRowsPerTile - 1);
-      const bool holes = now != 0xffffffffu;
+      const bool cut = kv0 + kRowsPerTile - 1 > tile_last;  // some row does not see all keys of the tile
+      const int last = min(row_last, g.s.kv_len - 1) - kv0;  // the last one that this row sees
       auto mask_scores = [&](uint32_t *x, int c0, int cols) {
         if (cut) {
 #pragma unroll
           for (int c = 0; c < cols; ++c)
             if (c0 + c > last) x[c] = __float_as_uint(-INFINITY);
         }
-        if (holes) {
+        if (there != 0xffffffffu) {
+          const int shift = p.page_log2 < 7 ? p.page_log2 : 31;  // a larger page: bit 0
 #pragma unroll
           for (int c = 0; c < cols; ++c)
-            if (!((now >> (bits.per_tile == 1 ? 0 : (c0 + c) >> p.page_log2)) & 1u)) x[c] = __float_as_uint(-INFINITY);
+            if (!((there >> ((c0 + c) >> shift)) & 1u)) x[c] = __float_as_uint(-INFINITY);
         }
       };
       auto load_scores = [&](uint32_t(&sr)[128]) {
@@ -430,6 +437,7 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
     if (lane == 0) mbar_arrive(bar_pfull);  // one arrival per warp
   }
 
+  more = walk.next(p, ahead);  // the next segment, while the last product runs
   bool have_o = false;
   if (ok && n > 0) {
     have_o = __all_sync(0xffffffffu, mbar_wait(bar_ofull, ofull_parity, abort_flag, err));
@@ -437,59 +445,82 @@ __device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const 
   }
   const bool done = named_bar_and(1 + t, 128, ok && (n == 0 || have_o));
   if (!warp_valid) return done;
-  const int head = g.h * p.G + r % p.G;
-  const int row = g.s.q0 + tok;
   const float inv_l = l > 0.f ? 1.f / l : 0.f;
   const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  const unsigned valid = __ballot_sync(0xffffffffu, row_valid);
+  // Rows leave through shared memory, 64 bytes of each at a time, so that a
+  // store instruction writes 64 bytes of eight rows (each lane its own row, 16
+  // bytes at a time, cost twice the sectors: 10,000 clocks a segment, now
+  // about half). `stage`: 32 rows of this warp, 80 bytes apart.
+  const uint32_t mine = stage + lane * 80u;
+  const int sub = lane >> 2, quad = lane & 3;
+  long long off;  // this lane's row in the output, elements
   if (g.slot >= 0) {
     const size_t at = static_cast<size_t>(g.slot) * p.part_rows + t * p.tok * p.G + r;
     if (row_valid) p.part_lse[at] = lse;
-    if (have_o) {
+    if (!have_o) return done;  // no key seen: the merge does not read O
+    off = static_cast<long long>(at) * D;
 #pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) {
-        uint32_t v[32];
-        tmem_ld32(o_addr + 32 * cb, v);
-        tmem_ld_wait(v);
-        if (row_valid) {
-          float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D + cb * 32);
+    for (int c0 = 0; c0 < D; c0 += 16) {
+      uint32_t v[16];
+      tmem_ld16(o_addr + c0, v);
+      tmem_ld_wait(v);
+      __syncwarp();  // the stage has been read
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(v[4 * i]) * inv_l, __uint_as_float(v[4 * i + 1]) * inv_l,
-                                 __uint_as_float(v[4 * i + 2]) * inv_l, __uint_as_float(v[4 * i + 3]) * inv_l);
-        }
-        __syncwarp();
+      for (int i = 0; i < 4; ++i)
+        st_shared_v4(mine + 16 * i, __float_as_uint(__uint_as_float(v[4 * i]) * inv_l),
+                     __float_as_uint(__uint_as_float(v[4 * i + 1]) * inv_l),
+                     __float_as_uint(__uint_as_float(v[4 * i + 2]) * inv_l),
+                     __float_as_uint(__uint_as_float(v[4 * i + 3]) * inv_l));
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + sub;
+        const long long to = __shfl_sync(0xffffffffu, off, row);
+        const uint4 x = ld_shared_v4(stage + row * 80u + quad * 16u);
+        if ((valid >> row) & 1u) *reinterpret_cast<uint4 *>(p.part_o + to + c0 + 4 * quad) = x;
       }
     }
+    __syncwarp();
     return done;
   }
-  if (row_valid && p.lse) p.lse[static_cast<size_t>(head) * p.total_q + row] = lse;
+  const int head = g.h * p.G + r % p.G, row_at = g.s.q0 + tok;
+  if (row_valid && p.lse) p.lse[static_cast<size_t>(head) * p.total_q + row_at] = lse;
+  off = head * p.o_h + row_at * p.o_s;
 #pragma unroll 1
-  for (int cb = 0; cb < D / 32; ++cb) {
+  for (int c0 = 0; c0 < D; c0 += 32) {
     uint32_t v[32];
     if (have_o) {
-      tmem_ld32(o_addr + 32 * cb, v);
+      tmem_ld32(o_addr + c0, v);
       tmem_ld_wait(v);
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0u;
     }
-    if (row_valid) {
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h + row * p.o_s + cb * 32);
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[4];
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // the one rounding of O to its own type
-          __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * k]) * inv_l,
-                                                   __uint_as_float(v[8 * i + 2 * k + 1]) * inv_l);
-          w[k] = *reinterpret_cast<uint32_t *>(&x);
-        }
-        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int k = 0; k < 4; ++k) {
+        // the one rounding of O to its own type
+        __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * k]) * inv_l,
+                                                 __uint_as_float(v[8 * i + 2 * k + 1]) * inv_l);
+        w[k] = *reinterpret_cast<uint32_t *>(&x);
       }
+      st_shared_v4(mine + 16 * i, w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * i + sub;
+      const long long to = __shfl_sync(0xffffffffu, off, row);
+      const uint4 x = ld_shared_v4(stage + row * 80u + quad * 16u);
+      if ((valid >> row) & 1u)
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + to + c0 + 8 * quad) = x;
+    }
   }
+  __syncwarp();
   return done;
 }
 
@@ -534,7 +565,8 @@ __device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, 
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
   Segment g;
-  const uint64_t pol_q = l2_policy_evict_last(), pol_kv = l2_policy_evict_first();
+  // K and V are read again by the other row blocks of their sequence, Q is not
+  const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
   const int page_size = 1 << p.page_log2;
   const bool small = page_size < kRowsPerTile;
   const int boxes = small ? kRowsPerTile >> p.page_log2 : 1;  // pages of a key tile
@@ -698,17 +730,17 @@ __device__ __noinline__ void wide_softmax(const PagedAttnParams &p, Walk walk, i
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
   const int r = threadIdx.x & 127;
   const uint32_t lane_off = static_cast<uint32_t>(r & ~31) << 16;
+  const uint32_t stage = sRing + Cfg<D>::kStages * Cfg<D>::kTileBytes + (threadIdx.x >> 5) * 2560u;
   int steps = 0, ring = 0;
   uint32_t u = 0;
-  Segment g, ahead;  // the next segment is found before this one's first scores are there
+  Segment g, ahead;
   bool more = walk.next(p, ahead);
   while (more) {
     g = ahead;
-    more = walk.next(p, ahead);
     const int n = Walk::tiles(p, g, t), n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
     if (!softmax_segment<D>(p, g, t, n, r, s_column(tmem, t) + lane_off, o_column(tmem, t) + lane_off,
                             bar(W::kSFull + t), bar(W::kPFull + t), bar(W::kOFull + t), bar(W::kFull), sRing, ring, steps,
-                            u & 1u, abort_flag, err))
+                            u & 1u, stage, walk, ahead, more, abort_flag, err))
       return;
     ring += 2 * n_max;
     steps += n;

@@ -7,12 +7,15 @@
 // 10^6 costs no precision; the signed fraction, as a float, goes through
 // sincospif.
 //
-// Memory-bound: every element is read and written once. A CTA takes a tile of
-// kTok tokens and a share of the heads: the tile's sines and cosines are
-// formed once in shared memory (D / 2 per token, instead of per head and
-// token), then each thread takes 16 elements of one (head, token) row -- eight
-// pairs, two 16-byte pieces in bf16, four in fp32 -- so that D / 16 threads
-// cover a row with whole 32-byte sectors in either pairing.
+// Memory-bound: every element is read and written once. A thread takes one
+// slice of 16 elements -- eight pairs, two 16-byte pieces in bf16, four in fp32
+// -- of one token, forms its eight sines and cosines once, in registers, and
+// goes over heads with them, four rows in flight; D / 16 threads cover a row
+// with whole 32-byte sectors in either pairing. (Sines in shared memory, shared
+// by the CTA, cost more in reads than they save: 109 us instead of 91 for
+// 32,768 tokens of 32 heads of 128 in bf16, 5.9 TB/s of the 6.8 that a copy
+// reaches.) The heads of a token are dealt over the CTA and, with few tokens, over
+// the grid.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -88,115 +91,96 @@ __device__ __forceinline__ int piece_at(int sl, int i) {
   return 8 * sl + (i / kHalf) * (D / 2) + kPer * (i % kHalf);
 }
 
-// The rows of one launch: heads [0, q.H) of q, then those of k, then those of v
-// (v only in an append).
+// The slot of token t of an append: its element offset in the pools, -1 if it has
+// none; *live: whether the token belongs to a sequence.
+__device__ __forceinline__ long long slot_of(const PagedView &c, long long t, long long n_tok, int D, bool *live) {
+  int lo = 0, hi = c.B;  // the first sequence that ends behind t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (c.cu_seqlens[mid + 1] <= t) lo = mid + 1;
+    else hi = mid;
+  }
+  *live = lo < c.B && c.cu_seqlens[lo] <= t;
+  if (!*live) return -1;
+  const long long max_keys = static_cast<long long>(c.max_pages) * c.page_size;
+  long long len = c.kv_lens[lo];
+  len = len < 0 ? 0 : (len > max_keys ? max_keys : len);
+  const long long end = c.cu_seqlens[lo + 1] < n_tok ? c.cu_seqlens[lo + 1] : n_tok;
+  const long long slot = len - (end - t);
+  if (slot < 0) return -1;
+  const int page = c.page_table[lo * c.table_stride + slot / c.page_size];
+  if (page < 0 || page >= c.n_pages) return -1;
+  return static_cast<long long>(page) * c.page_stride + (slot % c.page_size) * D;
+}
+
+// blockIdx.x: tile of kTok tokens; blockIdx.y: share of the heads (those of q,
+// then k, then, in an append, v).
 template <typename T, int D, bool kInterleaved, bool kAppend, int kTok>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopeTable tbl) {
-  __shared__ float2 cs[kTok][D / 2];
-  __shared__ long long slot_at[kTok];  // append: element offset of the token's slot in the pools, -1: dropped
-  __shared__ int live[kTok];           // append: the token belongs to a sequence
-  const long long t0 = static_cast<long long>(blockIdx.x) * kTok;
-  const long long n_tok = static_cast<long long>(p.B) * p.S;
-  if (kAppend && threadIdx.x < kTok) {
-    const long long t = t0 + threadIdx.x;
-    const PagedView &c = p.cache;
-    long long at = -1;
-    int in = 0;
-    if (t < n_tok) {
-      // the last sequence that starts at or before t
-      int lo = 0, hi = c.B;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (c.cu_seqlens[mid + 1] <= t) lo = mid + 1;
-        else hi = mid;
-      }
-      if (lo < c.B && c.cu_seqlens[lo] <= t) {
-        in = 1;
-        const long long max_keys = static_cast<long long>(c.max_pages) * c.page_size;
-        long long len = c.kv_lens[lo];
-        len = len < 0 ? 0 : (len > max_keys ? max_keys : len);
-        const long long end = c.cu_seqlens[lo + 1] < n_tok ? c.cu_seqlens[lo + 1] : n_tok;
-        const long long slot = len - (end - t);
-        if (slot >= 0) {
-          const long long pi = slot / c.page_size;
-          const int page = c.page_table[lo * c.table_stride + pi];
-          if (page >= 0 && page < c.n_pages)
-            at = static_cast<long long>(page) * c.page_stride + (slot % c.page_size) * D;
-        }
-      }
-    }
-    slot_at[threadIdx.x] = at;
-    live[threadIdx.x] = in;
-  }
-  if (p.positions != nullptr) {
-    for (int i = threadIdx.x; i < kTok * (D / 2); i += kRopeThreads) {
-      const int tt = i / (D / 2), pr = i % (D / 2);
-      const long long t = t0 + tt;
-      if (t >= n_tok) break;
-      const long long b = kAppend ? 0 : t / p.S, s = kAppend ? t : t - b * p.S;
-      const int axis = tbl.axis[pr];
-      const long long pos = axis < 0 ? 0 : p.positions[axis * p.pos_axis + b * p.pos_b + s];
-      // position times turns per position, whole turns dropped: [-1/2, 1/2) turns in 64 bits
-      const long long turn = static_cast<long long>(static_cast<uint64_t>(pos) * tbl.turns[pr]);
-      float sn, cn;
-      sincospif(static_cast<float>(turn) * 0x1p-63f, &sn, &cn);
-      cs[tt][pr] = make_float2(cn, p.inverse ? -sn : sn);
-    }
-  }
-  __syncthreads();
-
-  constexpr int kSlices = D / 16;                          // threads per row
-  constexpr int kRowsPerPass = kRopeThreads / kSlices;
+  constexpr int kSlices = D / 16;                               // threads per row
+  constexpr int kHeads = kRopeThreads / (kSlices * kTok);       // heads of a CTA at a time
+  constexpr int kPieces = Vec16<T>::kPieces;
   const int sl = threadIdx.x % kSlices;
+  const long long t = static_cast<long long>(blockIdx.x) * kTok + threadIdx.x / kSlices % kTok;
+  const long long n_tok = static_cast<long long>(p.B) * p.S;
+  if (t >= n_tok) return;
+  const long long b = kAppend ? 0 : t / p.S, s = kAppend ? t : t - b * p.S;
+  bool live = true;
+  const long long slot = kAppend ? slot_of(p.cache, t, n_tok, D, &live) : -1;
+  float cn[8], sn[8];
+  if (p.positions != nullptr) {
+    const int *pos = p.positions + b * p.pos_b + s;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int axis = tbl.axis[8 * sl + k];
+      const long long at = axis < 0 ? 0 : pos[axis * p.pos_axis];
+      // position times turns per position, whole turns dropped: [-1/2, 1/2) turns in 64 bits
+      const long long turn = static_cast<long long>(static_cast<uint64_t>(at) * tbl.turns[8 * sl + k]);
+      sincospif(static_cast<float>(turn) * 0x1p-63f, &sn[k], &cn[k]);
+      if (p.inverse) sn[k] = -sn[k];
+    }
+  }
   const int heads = p.q.heads + p.k.heads + (kAppend ? p.v.heads : 0);
   const int h_per = (heads + gridDim.y - 1) / gridDim.y;
-  const int h0 = blockIdx.y * h_per, h1 = min(heads, h0 + h_per);
-  const int n_rows = (h1 - h0) * kTok;
-#pragma unroll 2
-  for (int r = threadIdx.x / kSlices; r < n_rows; r += kRowsPerPass) {
-    const int h = h0 + r / kTok, tt = r % kTok;
-    const long long t = t0 + tt;
-    if (t >= n_tok) continue;
-    const bool is_q = h < p.q.heads;
-    const bool is_v = kAppend && h >= p.q.heads + p.k.heads;
-    const RopeView &x = is_q ? p.q : (is_v ? p.v : p.k);
-    const int hh = is_q ? h : (is_v ? h - p.q.heads - p.k.heads : h - p.q.heads);
-    const long long b = kAppend ? 0 : t / p.S, s = kAppend ? t : t - b * p.S;
-    T *dst;
-    if (kAppend) {
-      if (is_q) {
-        if (!live[tt]) continue;
-        dst = static_cast<T *>(x.out) + hh * x.out_h + s * x.out_s;
-      } else {
-        if (slot_at[tt] < 0) continue;
-        dst = static_cast<T *>(is_v ? p.cache.v_pages : p.cache.k_pages) + slot_at[tt] +
-              static_cast<long long>(hh) * p.cache.page_size * D;
+  const int h0 = blockIdx.y * h_per + threadIdx.x / (kSlices * kTok), h1 = min(heads, static_cast<int>(blockIdx.y + 1) * h_per);
+  // this thread's heads among those of one tensor, which are first .. first + n - 1 of all
+  auto rows = [&](int first, int n, const T *src, long long src_h, T *dst, long long dst_h, bool turned) {
+    const int lo = h0 >= first ? h0 : first + (kHeads - (first - h0) % kHeads) % kHeads;
+    const int hi = min(h1, first + n);
+#pragma unroll 4
+    for (int h = lo; h < hi; h += kHeads) {
+      const T *from = src + (h - first) * src_h;
+      T *to = dst + (h - first) * dst_h;
+      uint4 w[kPieces];
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        w[i] = __ldcs(reinterpret_cast<const uint4 *>(from + piece_at<T, D, kInterleaved>(sl, i)));
+      if (turned) {
+        float v[16], y[16];
+        unpack(w, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int i1 = kInterleaved ? 2 * k : k, i2 = kInterleaved ? 2 * k + 1 : k + 8;
+          y[i1] = fmaf(v[i1], cn[k], -v[i2] * sn[k]);
+          y[i2] = fmaf(v[i1], sn[k], v[i2] * cn[k]);
+        }
+        pack(y, w);
       }
-    } else {
-      dst = static_cast<T *>(x.out) + b * x.out_b + hh * x.out_h + s * x.out_s;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        *reinterpret_cast<uint4 *>(to + piece_at<T, D, kInterleaved>(sl, i)) = w[i];
     }
-    const T *src = static_cast<const T *>(x.in) + (kAppend ? 0 : b * x.in_b) + hh * x.in_h + s * x.in_s;
-    constexpr int kPieces = Vec16<T>::kPieces;
-    uint4 w[kPieces];
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      w[i] = __ldcs(reinterpret_cast<const uint4 *>(src + piece_at<T, D, kInterleaved>(sl, i)));
-    if (p.positions != nullptr && !is_v) {
-      float v[16], y[16];
-      unpack(w, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 c = cs[tt][8 * sl + k];
-        const int i1 = kInterleaved ? 2 * k : k, i2 = kInterleaved ? 2 * k + 1 : k + 8;
-        y[i1] = fmaf(v[i1], c.x, -v[i2] * c.y);
-        y[i2] = fmaf(v[i1], c.y, v[i2] * c.x);
-      }
-      pack(y, w);
-    }
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      *reinterpret_cast<uint4 *>(dst + piece_at<T, D, kInterleaved>(sl, i)) = w[i];
+  };
+  auto in = [&](const RopeView &x) { return static_cast<const T *>(x.in) + (kAppend ? 0 : b * x.in_b) + s * x.in_s; };
+  auto out = [&](const RopeView &x) { return static_cast<T *>(x.out) + (kAppend ? 0 : b * x.out_b) + s * x.out_s; };
+  if (live) rows(0, p.q.heads, in(p.q), p.q.in_h, out(p.q), p.q.out_h, true);
+  if (!kAppend) {
+    rows(p.q.heads, p.k.heads, in(p.k), p.k.in_h, out(p.k), p.k.out_h, true);
+  } else if (slot >= 0) {
+    const long long page_h = static_cast<long long>(p.cache.page_size) * D;
+    rows(p.q.heads, p.k.heads, in(p.k), p.k.in_h, static_cast<T *>(p.cache.k_pages) + slot, page_h, p.positions != nullptr);
+    rows(p.q.heads + p.k.heads, p.v.heads, in(p.v), p.v.in_h, static_cast<T *>(p.cache.v_pages) + slot, page_h, false);
   }
 }
 
@@ -205,12 +189,11 @@ cudaError_t launch_tile(const RopeParams &p, const RopeTable &tbl, cudaStream_t 
   const long long n_tok = static_cast<long long>(p.B) * p.S;
   const long long tiles = (n_tok + kTok - 1) / kTok;
   const int heads = p.q.heads + p.k.heads + (kAppend ? p.v.heads : 0);
-  constexpr int kRowsPerPass = kRopeThreads / (D / 16);
-  // few tiles: the heads are dealt over more CTAs, down to one pass each
+  constexpr int kHeads = kRopeThreads / (D / 16 * kTok);
+  // few tiles: the heads are dealt over more CTAs, down to one row a thread
   long long want = static_cast<long long>(device_sm_count()) * 4 / tiles;
-  const long long most = (static_cast<long long>(heads) * kTok + kRowsPerPass - 1) / kRowsPerPass;
+  const long long most = (heads + kHeads - 1) / kHeads;
   want = want < 1 ? 1 : (want > most ? most : want);
-  if (want > heads) want = heads;
   if (tiles > 0x7fffffffll || want > 65535) return cudaErrorInvalidValue;
   rope_kernel<T, D, kInterleaved, kAppend, kTok>
       <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(want)), kRopeThreads, 0, stream>>>(p, tbl);
@@ -219,12 +202,13 @@ cudaError_t launch_tile(const RopeParams &p, const RopeTable &tbl, cudaStream_t 
 
 template <typename T, int D, bool kAppend>
 cudaError_t launch_typed_rope(const RopeParams &p, const RopeTable &tbl, bool interleaved, cudaStream_t stream) {
-  // Tiles of 16 tokens share their sines among the heads; with few tokens
-  // tiles of 4 give more CTAs.
-  const bool small = static_cast<long long>(p.B) * p.S < 16ll * 4 * device_sm_count();
+  // Tiles of 32 tokens give a thread the most heads to its sines (32,768 tokens
+  // of 32 heads in bf16: 91 us; tiles of 16 and 8: 95 us); with fewer tokens than
+  // one such tile an SM, tiles of 4 give more CTAs.
+  const bool small = static_cast<long long>(p.B) * p.S < 32ll * device_sm_count();
   if (interleaved)
-    return small ? launch_tile<T, D, true, kAppend, 4>(p, tbl, stream) : launch_tile<T, D, true, kAppend, 16>(p, tbl, stream);
-  return small ? launch_tile<T, D, false, kAppend, 4>(p, tbl, stream) : launch_tile<T, D, false, kAppend, 16>(p, tbl, stream);
+    return small ? launch_tile<T, D, true, kAppend, 4>(p, tbl, stream) : launch_tile<T, D, true, kAppend, 32>(p, tbl, stream);
+  return small ? launch_tile<T, D, false, kAppend, 4>(p, tbl, stream) : launch_tile<T, D, false, kAppend, 32>(p, tbl, stream);
 }
 
 }  // namespace

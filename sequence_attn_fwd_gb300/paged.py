@@ -143,25 +143,31 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, pa
     if d != D or Hkv == 0 or Hq % Hkv != 0:
         raise ValueError("q must have the cache's D and a multiple of its heads")
     sq = _packed(q, total, D, "q")
+    where, used = q.device, [k_pages, q]
     if out is None:
-        out = torch.empty((Hq, total, D), dtype=_BF16, device=q.device)
+        out, so = torch.empty((Hq, total, D), dtype=_BF16, device=where), (total * D, D)
     else:
         _distinct_memory(out, "out")
+        so = _packed(out, total, D, "out")
+        if out.shape[0] != Hq:
+            raise ValueError("bad out")
+        used.append(out)
     if lse is None:
-        lse = torch.empty((Hq, total), dtype=_F32, device=q.device)
-    so = _packed(out, total, D, "out")
-    if out.shape[0] != Hq:
-        raise ValueError("bad out")
-    if lse.dtype != _F32 or lse.shape != (Hq, total) or not lse.is_contiguous():
-        raise ValueError("bad lse")
+        lse = torch.empty((Hq, total), dtype=_F32, device=where)
+    else:
+        if lse.dtype != _F32 or lse.shape != (Hq, total) or not lse.is_contiguous():
+            raise ValueError("bad lse")
+        used.append(lse)
     if total == 0 or B == 0:
         return out, lse
     need = lib.attn_paged_workspace_bytes(Hq, Hkv, total, D)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
-        raise ValueError("workspace must be a contiguous uint8 tensor of attn_paged_workspace_bytes(...) bytes")
-    _one_device("attn_paged", k_pages, q, out, lse, workspace)
+        workspace = torch.empty(need, dtype=torch.uint8, device=where)
+    else:
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
+            raise ValueError("workspace must be a contiguous uint8 tensor of attn_paged_workspace_bytes(...) bytes")
+        used.append(workspace)
+    _one_device("attn_paged", *used)
     _call(lib.attn_paged, "attn_paged", dev, q.data_ptr(), sq[0], sq[1], view, out.data_ptr(), so[0], so[1],
           lse.data_ptr(), workspace.data_ptr(), workspace.numel(), Hq, total, 1 if causal else 0,
           1.0 / math.sqrt(D) if scale is None else float(scale))
