@@ -557,7 +557,7 @@ __device__ __forceinline__ uint32_t o_column(uint32_t tmem, int t) { return tmem
 // Producer: the whole warp. sQ [tile][col block][128 rows][128 B], sRing
 // [slot][col block][128 rows][128 B].
 template <int D>
-__device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, const CUtensorMap *tm_q,
+__device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk walk, const CUtensorMap *tm_q,
                                            const CUtensorMap *tm_k, const CUtensorMap *tm_v, uint32_t bar0, uint32_t sQ,
                                            uint32_t sRing, int first_entry, volatile int *abort_flag, int *err) {
   using C = Cfg<D>;
@@ -632,7 +632,7 @@ __device__ __noinline__ void wide_producer(const PagedAttnParams &p, Walk walk, 
 
 // MMA issuer of query tile t, one thread (the dense forward's scheme).
 template <int D>
-__device__ __noinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, int t, uint32_t bar0,
+__device__ __forceinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, int t, uint32_t bar0,
                                          uint32_t sQ, uint32_t sRing, uint32_t tmem, volatile int *turn,
                                          volatile int *abort_flag, int *err) {
   using C = Cfg<D>;
@@ -724,7 +724,7 @@ __device__ __noinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, in
 
 // Softmax warpgroup of query tile t.
 template <int D>
-__device__ __noinline__ void wide_softmax(const PagedAttnParams &p, Walk walk, int t, uint32_t bar0,
+__device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, Walk walk, int t, uint32_t bar0,
                                           uint32_t sRing, uint32_t tmem, volatile int *abort_flag, int *err) {
   using W = WideBars<D>;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -892,62 +892,84 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The rows of the items that were cut. CTA blockIdx.x of the attention began
 // such an item and described it (first token, rows, KV head, last CTA); a warp
-// takes a row (blockIdx.y: 8 rows): the weights exp(lse_i - max) of the row's
-// partials, then their weighted sum in the order of the keys, four (D = 128)
-// or two columns a lane.
-constexpr int kMergeThreads = 256;
+// takes four rows at a time (blockIdx.y: 32 rows), so that their loads overlap:
+// the weights exp(lse_i - max) of each row's partials, lane i the i-th, then
+// their weighted sum in the order of the keys, four (D = 128) or two columns a
+// lane. Bound by latency: two dependent loads.
+constexpr int kMergeThreads = 256, kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PagedAttnParams p) {
   wait_prerequisites();
   const int4 cut = p.cuts[blockIdx.x];
-  const int lane = threadIdx.x & 31, r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  if (r >= cut.y) return;
+  const int lane = threadIdx.x & 31;
+  const int r0 = (blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5)) * kMergeRows;
+  if (r0 >= cut.y) return;
   const int c0 = blockIdx.x, c1 = cut.w;
   constexpr int kCols = D / 32;
-  float acc[kCols] = {};
-  float m = -INFINITY, sum = 0.f;
-  auto part = [&](int c) -> size_t { return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + r; };
+  // the partial of row r0 + u (the last row again past it) that CTA c left
+  auto part = [&](int c, int u) -> size_t {
+    return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + min(r0 + u, cut.y - 1);
+  };
+  float acc[kMergeRows][kCols] = {};
+  float m[kMergeRows], sum[kMergeRows] = {};
+#pragma unroll
+  for (int u = 0; u < kMergeRows; ++u) m[u] = -INFINITY;
   // a timeout somewhere: the partials may be missing, the rows come out empty
   const bool failed = *reinterpret_cast<volatile int *>(&g_device_error) != kErrNone;
   if (!failed) {
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[part(c)]);
+    for (int c = c0 + lane; c <= c1; c += 32)
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  }
-  if (m != -INFINITY) {
+      for (int u = 0; u < kMergeRows; ++u) m[u] = fmaxf(m[u], p.part_lse[part(c, u)]);
+#pragma unroll
+    for (int u = 0; u < kMergeRows; ++u)
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], off));
     for (int cb = c0; cb <= c1; cb += 32) {
-      const float w = cb + lane <= c1 ? expf(p.part_lse[part(cb + lane)] - m) : 0.f;
-      sum += w;
+      float w[kMergeRows];
+#pragma unroll
+      for (int u = 0; u < kMergeRows; ++u) {
+        const float lse = cb + lane <= c1 ? p.part_lse[part(cb + lane, u)] : -INFINITY;
+        w[u] = lse == -INFINITY ? 0.f : expf(lse - m[u]);
+        sum[u] += w[u];
+      }
       const int k_end = min(32, c1 - cb + 1);
-#pragma unroll 8
+#pragma unroll 2
       for (int k = 0; k < k_end; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        if (wk == 0.f) continue;  // a partial that saw no key has no O
-        const float *x = p.part_o + part(cb + k) * D + lane * kCols;
-        if constexpr (kCols == 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(x);
-          acc[0] = fmaf(wk, v.x, acc[0]);
-          acc[1] = fmaf(wk, v.y, acc[1]);
-          acc[2] = fmaf(wk, v.z, acc[2]);
-          acc[3] = fmaf(wk, v.w, acc[3]);
-        } else {
-          const float2 v = *reinterpret_cast<const float2 *>(x);
-          acc[0] = fmaf(wk, v.x, acc[0]);
-          acc[1] = fmaf(wk, v.y, acc[1]);
+#pragma unroll
+        for (int u = 0; u < kMergeRows; ++u) {
+          const float wk = __shfl_sync(0xffffffffu, w[u], k);
+          if (wk == 0.f) continue;  // a partial that saw no key has no O
+          const float *x = p.part_o + part(cb + k, u) * D + lane * kCols;
+          if constexpr (kCols == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(x);
+            acc[u][0] = fmaf(wk, v.x, acc[u][0]);
+            acc[u][1] = fmaf(wk, v.y, acc[u][1]);
+            acc[u][2] = fmaf(wk, v.z, acc[u][2]);
+            acc[u][3] = fmaf(wk, v.w, acc[u][3]);
+          } else {
+            const float2 v = *reinterpret_cast<const float2 *>(x);
+            acc[u][0] = fmaf(wk, v.x, acc[u][0]);
+            acc[u][1] = fmaf(wk, v.y, acc[u][1]);
+          }
         }
       }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const int head = cut.z * p.G + r % p.G, row = cut.x + r / p.G;
-  __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h +
-                                                           row * p.o_s + lane * kCols);
 #pragma unroll
-  for (int i = 0; i < kCols / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-  if (lane == 0 && p.lse)
-    p.lse[static_cast<size_t>(head) * p.total_q + row] = sum > 0.f ? m + logf(sum) : -INFINITY;
+  for (int u = 0; u < kMergeRows; ++u) {
+    const int r = r0 + u;
+    if (r >= cut.y) break;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], off);
+    const float inv = sum[u] > 0.f ? 1.f / sum[u] : 0.f;
+    const int head = cut.z * p.G + r % p.G, row = cut.x + r / p.G;
+    __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h +
+                                                             row * p.o_s + lane * kCols);
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[u][2 * i] * inv, acc[u][2 * i + 1] * inv);
+    if (lane == 0 && p.lse)
+      p.lse[static_cast<size_t>(head) * p.total_q + row] = sum[u] > 0.f ? m[u] + logf(sum[u]) : -INFINITY;
+  }
 }
 
 template <int D>
@@ -963,7 +985,8 @@ cudaError_t launch_typed(const QueryMaps &tq, const CUtensorMap &tk, const CUten
   if (e != cudaSuccess || n_ctas == 1) return e;
   // the merge starts while the attention still runs and waits for its end inside
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(n_ctas - 1, (p.part_rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32));
+  constexpr int kRows = kMergeThreads / 32 * kMergeRows;
+  cfg.gridDim = dim3(n_ctas - 1, (p.part_rows + kRows - 1) / kRows);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};

@@ -65,7 +65,7 @@ __device__ __forceinline__ uint32_t idesc_narrow(int N, bool pv) {
 
 // Producer: the whole warp.
 template <int D>
-__device__ __noinline__ void narrow_producer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
+__device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
                                              const CUtensorMap *tm_q, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
                                              uint32_t bar0, uint32_t smem, int first_entry, volatile int *abort_flag,
                                              int *err) {
@@ -142,7 +142,7 @@ __device__ __noinline__ void narrow_producer(const PagedAttnParams &p, const Nar
 
 // MMA issuer: one thread.
 template <int D>
-__device__ __noinline__ void narrow_issuer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
+__device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
                                            uint32_t bar0, uint32_t smem, uint32_t tmem, volatile int *abort_flag,
                                            int *err) {
   using C = Narrow<D>;
@@ -238,7 +238,7 @@ constexpr float kNoReference = -1e30f;
 // floats of shared memory, `gi` its number. Every warp goes through the same
 // barriers whatever fails: a wait that runs out is carried to the next vote.
 template <int D, int C>
-__device__ __noinline__ void narrow_softmax(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
+__device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
                                             int gi, uint32_t bar0, uint32_t smem, uint32_t tmem, float *red,
                                             volatile int *abort_flag, int *err) {
   using L = Narrow<D>;
