@@ -890,73 +890,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The rows of the items that were cut. CTA blockIdx.x of the attention began
-// such an item and described it (first token, rows, KV head, last CTA); a warp
-// takes four rows at a time (blockIdx.y: 32 rows), so that their loads overlap:
-// the weights exp(lse_i - max) of each row's partials, lane i the i-th, then
-// their weighted sum in the order of the keys, four (D = 128) or two columns a
-// lane. Bound by latency: two dependent loads.
-constexpr int kMergeThreads = 256, kMergeRows = 4;
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PagedAttnParams p) {
-  wait_prerequisites();
-  const int4 cut = p.cuts[blockIdx.x];
+// Rows [r0, r0 + kRows) of a cut item, by one warp, its loads overlapping: the
+// weights exp(lse_i - max) of each row's partials, lane i the i-th, then their
+// weighted sum in the order of the keys, four (D = 128) or two columns a lane.
+template <int D, int kRows, int kUnroll>
+__device__ __forceinline__ void merge_rows(const PagedAttnParams &p, const int4 &cut, int r0) {
   const int lane = threadIdx.x & 31;
-  const int r0 = (blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5)) * kMergeRows;
-  if (r0 >= cut.y) return;
   const int c0 = blockIdx.x, c1 = cut.w;
   constexpr int kCols = D / 32;
   // the partial of row r0 + u (the last row again past it) that CTA c left
   auto part = [&](int c, int u) -> size_t {
     return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + min(r0 + u, cut.y - 1);
   };
-  float acc[kMergeRows][kCols] = {};
-  float m[kMergeRows], sum[kMergeRows] = {};
+  float acc[kRows][kCols] = {};
+  float m[kRows], sum[kRows] = {};
 #pragma unroll
-  for (int u = 0; u < kMergeRows; ++u) m[u] = -INFINITY;
+  for (int u = 0; u < kRows; ++u) m[u] = -INFINITY;
   // a timeout somewhere: the partials may be missing, the rows come out empty
   const bool failed = *reinterpret_cast<volatile int *>(&g_device_error) != kErrNone;
   if (!failed) {
     for (int c = c0 + lane; c <= c1; c += 32)
 #pragma unroll
-      for (int u = 0; u < kMergeRows; ++u) m[u] = fmaxf(m[u], p.part_lse[part(c, u)]);
+      for (int u = 0; u < kRows; ++u) m[u] = fmaxf(m[u], p.part_lse[part(c, u)]);
 #pragma unroll
-    for (int u = 0; u < kMergeRows; ++u)
+    for (int u = 0; u < kRows; ++u)
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], off));
     for (int cb = c0; cb <= c1; cb += 32) {
-      float w[kMergeRows];
+      float w[kRows];
 #pragma unroll
-      for (int u = 0; u < kMergeRows; ++u) {
+      for (int u = 0; u < kRows; ++u) {
         const float lse = cb + lane <= c1 ? p.part_lse[part(cb + lane, u)] : -INFINITY;
         w[u] = lse == -INFINITY ? 0.f : expf(lse - m[u]);
         sum[u] += w[u];
       }
       const int k_end = min(32, c1 - cb + 1);
-#pragma unroll 2
+#pragma unroll kUnroll
       for (int k = 0; k < k_end; ++k) {
 #pragma unroll
-        for (int u = 0; u < kMergeRows; ++u) {
+        for (int u = 0; u < kRows; ++u) {
           const float wk = __shfl_sync(0xffffffffu, w[u], k);
-          if (wk == 0.f) continue;  // a partial that saw no key has no O
-          const float *x = p.part_o + part(cb + k, u) * D + lane * kCols;
-          if constexpr (kCols == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(x);
-            acc[u][0] = fmaf(wk, v.x, acc[u][0]);
-            acc[u][1] = fmaf(wk, v.y, acc[u][1]);
-            acc[u][2] = fmaf(wk, v.z, acc[u][2]);
-            acc[u][3] = fmaf(wk, v.w, acc[u][3]);
-          } else {
-            const float2 v = *reinterpret_cast<const float2 *>(x);
-            acc[u][0] = fmaf(wk, v.x, acc[u][0]);
-            acc[u][1] = fmaf(wk, v.y, acc[u][1]);
+          float v[kCols] = {};
+          if (wk != 0.f) {  // a partial that saw no key has no O
+            const float *x = p.part_o + part(cb + k, u) * D + lane * kCols;
+            if constexpr (kCols == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(x);
+            else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(x);
           }
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) acc[u][i] = fmaf(wk, v[i], acc[u][i]);
         }
       }
     }
   }
 #pragma unroll
-  for (int u = 0; u < kMergeRows; ++u) {
+  for (int u = 0; u < kRows; ++u) {
     const int r = r0 + u;
     if (r >= cut.y) break;
 #pragma unroll
@@ -969,6 +956,24 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     for (int i = 0; i < kCols / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[u][2 * i] * inv, acc[u][2 * i + 1] * inv);
     if (lane == 0 && p.lse)
       p.lse[static_cast<size_t>(head) * p.total_q + row] = sum[u] > 0.f ? m[u] + logf(sum[u]) : -INFINITY;
+  }
+}
+
+// The rows of the items that were cut: CTA blockIdx.x of the attention began such
+// an item and described it (first token, rows, KV head, last CTA). Bound by
+// latency, two dependent loads: an item of few rows, which can have many
+// partials, takes a row a warp and eight partials at a time, one of many rows,
+// which has few, four rows a warp.
+constexpr int kMergeThreads = 256, kMergeRows = 4;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PagedAttnParams p) {
+  wait_prerequisites();
+  const int4 cut = p.cuts[blockIdx.x];
+  const int warp = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5), warps = gridDim.y * (kMergeThreads / 32);
+  if (cut.y <= warps) {
+    if (warp < cut.y) merge_rows<D, 1, 8>(p, cut, warp);
+  } else if (warp * kMergeRows < cut.y) {
+    merge_rows<D, kMergeRows, 2>(p, cut, warp * kMergeRows);
   }
 }
 
