@@ -47,7 +47,7 @@ struct Cfg {
   // barriers, three words, warp sums, the first segment, the narrow form's
   // reductions, prefix sums
   static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 2 * 16 * D * 2;
-  static_assert(2 * kTileBytes + kStages * kTileBytes + 8 * 2560 <= kAreaBytes, "wide layout");
+  static_assert(2 * kTileBytes + kStages * kTileBytes + 8 * 2688 <= kAreaBytes, "wide layout");
   static constexpr int kMaxBarriers = 2 * (196608 / kTileBytes) + 10;
   static constexpr int kRedFloats = 2 * 6 * 32;
   static constexpr int kSmemBytes =
@@ -283,33 +283,29 @@ __device__ __forceinline__ int page_entry(const PagedAttnParams &p, const int *r
   return (i << p.page_log2) < kv_len ? row[i] : -1;
 }
 
-// Which pages of a segment's key tiles are there: each lane of a warp looks one
-// up a tile ahead; `mask` has one bit per page of the tile (set past them).
-struct PageBits {
-  const int *at;    // this lane's entry of the tile after the next
-  int left;         // its distance to the end of the sequence's pages
-  int entry;        // of the next tile
-  __device__ __forceinline__ PageBits(const PagedAttnParams &p, const Segment &g) {
-    const bool small = p.page_log2 < 7;
-    const int lane = threadIdx.x & 31, per_tile = small ? kRowsPerTile >> p.page_log2 : 1;
-    const int first = small ? g.j0 * per_tile + lane : (g.j0 * kRowsPerTile) >> p.page_log2;
-    const int pages = (g.s.kv_len + (1 << p.page_log2) - 1) >> p.page_log2;
-    at = page_row(p, g) + first;
-    left = lane < per_tile ? pages - first : 0;
-    entry = left > 0 ? *at : 0;
-  }
-  // The mask of key tile j; then on to the next.
-  __device__ __forceinline__ unsigned next(const PagedAttnParams &p, int j) {
-    const unsigned mask = __ballot_sync(0xffffffffu, static_cast<unsigned>(entry) < static_cast<unsigned>(p.cache.n_pages));
-    const bool small = p.page_log2 < 7;
-    const int step = small ? kRowsPerTile >> p.page_log2
-                           : (((j + 1) * kRowsPerTile & ((1 << p.page_log2) - 1)) == 0 ? 1 : 0);
-    at += step;
-    left -= step;
-    entry = left > 0 ? *at : 0;
-    return mask;
-  }
-};
+// Whether a page of a segment's key tiles is missing, found by a warp at the
+// segment's start, so that the tiles of a whole sequence look nothing up.
+__device__ __forceinline__ bool pages_missing(const PagedAttnParams &p, const Segment &g) {
+  const int lane = threadIdx.x & 31;
+  const int first = (g.j0 * kRowsPerTile) >> p.page_log2;
+  const int end = (min(g.j1 * kRowsPerTile, g.s.kv_len) + (1 << p.page_log2) - 1) >> p.page_log2;
+  const int *row = page_row(p, g);
+  bool missing = false;
+#pragma unroll 8
+  for (int i = first + lane; i < end; i += 32)
+    missing |= static_cast<unsigned>(row[i]) >= static_cast<unsigned>(p.cache.n_pages);
+  return __any_sync(0xffffffffu, missing);
+}
+// The pages of key tile j that are there, one bit each (set past them).
+__device__ __forceinline__ unsigned pages_there(const PagedAttnParams &p, const int *row, int kv_len, int j) {
+  const int lane = threadIdx.x & 31;
+  const bool small = p.page_log2 < 7;
+  const int i = small ? j * (kRowsPerTile >> p.page_log2) + lane : (j * kRowsPerTile) >> p.page_log2;
+  bool there = true;
+  if (lane < (small ? kRowsPerTile >> p.page_log2 : 1) && (i << p.page_log2) < kv_len)
+    there = static_cast<unsigned>(row[i]) < static_cast<unsigned>(p.cache.n_pages);
+  return __ballot_sync(0xffffffffu, there);
+}
 
 // V slots past kv_len may hold anything, NaN too, and 0 * NaN would reach O:
 // they are zeroed in shared memory, by the 128 threads of a warpgroup, before
@@ -339,189 +335,6 @@ __device__ __forceinline__ void scale_o(uint32_t o_addr, float alpha) {
     tmem_st32(o_addr + 32 * cb, v);
   }
   tmem_st_wait();
-}
-
-// Softmax and epilogue of one row of query tile t over a segment (one thread a
-// row, TMEM lane = tile row; the dense forward's scheme). `ring` is the ring
-// position of the segment's first K tile.
-template <int D>
-__device__ __forceinline__ bool softmax_segment(const PagedAttnParams &p, const Segment &g, int t, int n, int r,
-                                                uint32_t s_addr, uint32_t o_addr, uint32_t bar_sfull,
-                                                uint32_t bar_pfull, uint32_t bar_ofull, uint32_t bar_full0,
-                                                uint32_t ring_base, int ring, int step_base, uint32_t ofull_parity,
-                                                uint32_t stage, Walk &walk, Segment &ahead, bool &more,
-                                                volatile int *abort_flag, int *err) {
-  const int lane = threadIdx.x & 31;
-  const int tok = (2 * g.rb + t) * p.tok + r / p.G;  // within the sequence
-  const bool row_valid = r < p.tok * p.G && tok < g.s.q_len;
-  // rows of no token (zeros, or other sequences' rows) see every key: nothing of them is written
-  const int row_last = row_valid && p.causal ? g.s.kv_len - g.s.q_len + tok : g.s.kv_len - 1;
-  const float c2 = p.scale_log2;
-  const int tile_last = p.causal ? g.s.kv_len - g.s.q_len + (2 * g.rb + t) * p.tok : g.s.kv_len - 1;  // of its first token
-  const bool warp_valid = __any_sync(0xffffffffu, row_valid);
-  PageBits bits(p, g);
-  float m = -INFINITY, l = 0.f;
-  bool ok = true;
-
-  for (int j = 0; j < n; ++j) {
-    const unsigned there = bits.next(p, g.j0 + j);
-    ok = __all_sync(0xffffffffu, mbar_wait(bar_sfull, static_cast<uint32_t>(step_base + j) & 1u, abort_flag, err));
-    if (!ok) break;
-    tc_fence_after();
-    const int kv0 = (g.j0 + j) * kRowsPerTile;
-    if (warp_valid) {
-      const bool cut = kv0 + kRowsPerTile - 1 > tile_last;  // some row does not see all keys of the tile
-      const int last = min(row_last, g.s.kv_len - 1) - kv0;  // the last one that this row sees
-      auto mask_scores = [&](uint32_t *x, int c0, int cols) {
-        if (cut) {
-#pragma unroll
-          for (int c = 0; c < cols; ++c)
-            if (c0 + c > last) x[c] = __float_as_uint(-INFINITY);
-        }
-        if (there != 0xffffffffu) {
-          const int shift = p.page_log2 < 7 ? p.page_log2 : 31;  // a larger page: bit 0
-#pragma unroll
-          for (int c = 0; c < cols; ++c)
-            if (!((there >> ((c0 + c) >> shift)) & 1u)) x[c] = __float_as_uint(-INFINITY);
-        }
-      };
-      auto load_scores = [&](uint32_t(&sr)[128]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * i]));
-        tmem_ld_wait(sr);
-        mask_scores(sr, 0, 128);
-      };
-      uint32_t pk[64];
-      uint32_t sr[128];
-      load_scores(sr);
-      float rowsum;
-      if (j == 0) m = row_max(reinterpret_cast<const float *>(sr)) * c2;
-      rowsum = exp_row<false, 0>(reinterpret_cast<const float *>(sr), c2, (m == -INFINITY) ? 0.f : m, pk);
-      if (j > 0) {
-        // as in the dense forward: the reference moves, and O with it, only
-        // when the tile's P would sum to more than 2^8 or there is none yet
-        const bool big = row_valid && (!(rowsum <= kRescaleSum) || (m == -INFINITY && rowsum > 0.f));
-        if (__any_sync(0xffffffffu, big)) {
-          float mx = -INFINITY;  // 32 columns at a time: few live registers
-#pragma unroll 1
-          for (int cb = 0; cb < 4; ++cb) {
-            uint32_t x[32];
-            tmem_ld32(s_addr + 32 * cb, x);
-            tmem_ld_wait(x);
-            mask_scores(x, 32 * cb, 32);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) mx = fmaxf(mx, __uint_as_float(x[c]));
-          }
-          const float m_new = fmaxf(m, mx * c2);
-          const float alpha = (m_new == -INFINITY) ? 1.f : ex2_approx(m - m_new);
-          m = m_new;
-          l *= alpha;
-          scale_o<D>(o_addr, alpha);
-          load_scores(sr);
-          rowsum = exp_row<false, 0>(reinterpret_cast<const float *>(sr), c2, (m == -INFINITY) ? 0.f : m, pk);
-        }
-      }
-      l += rowsum;
-      tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-      tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-      tmem_st_wait();
-    }
-    if (g.s.kv_len - kv0 < kRowsPerTile) {
-      const int cv = ring + 2 * j + 1, slot = cv % Cfg<D>::kStages;  // ring position of the V tile
-      ok = clear_tail<D>(g.s.kv_len - kv0, ring_base + slot * Cfg<D>::kTileBytes, bar_full0 + 8u * slot,
-                         (cv / Cfg<D>::kStages) & 1, abort_flag, err);
-      if (!ok) break;
-    }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_pfull);  // one arrival per warp
-  }
-
-  more = walk.next(p, ahead);  // the next segment, while the last product runs
-  bool have_o = false;
-  if (ok && n > 0) {
-    have_o = __all_sync(0xffffffffu, mbar_wait(bar_ofull, ofull_parity, abort_flag, err));
-    tc_fence_after();
-  }
-  const bool done = named_bar_and(1 + t, 128, ok && (n == 0 || have_o));
-  if (!warp_valid) return done;
-  const float inv_l = l > 0.f ? 1.f / l : 0.f;
-  const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-  const unsigned valid = __ballot_sync(0xffffffffu, row_valid);
-  // Rows leave through shared memory, 64 bytes of each at a time, so that a
-  // store instruction writes 64 bytes of eight rows (each lane its own row, 16
-  // bytes at a time, cost twice the sectors: 10,000 clocks a segment, now
-  // about half). `stage`: 32 rows of this warp, 80 bytes apart.
-  const uint32_t mine = stage + lane * 80u;
-  const int sub = lane >> 2, quad = lane & 3;
-  long long off;  // this lane's row in the output, elements
-  if (g.slot >= 0) {
-    const size_t at = static_cast<size_t>(g.slot) * p.part_rows + t * p.tok * p.G + r;
-    if (row_valid) p.part_lse[at] = lse;
-    if (!have_o) return done;  // no key seen: the merge does not read O
-    off = static_cast<long long>(at) * D;
-#pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += 16) {
-      uint32_t v[16];
-      tmem_ld16(o_addr + c0, v);
-      tmem_ld_wait(v);
-      __syncwarp();  // the stage has been read
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        st_shared_v4(mine + 16 * i, __float_as_uint(__uint_as_float(v[4 * i]) * inv_l),
-                     __float_as_uint(__uint_as_float(v[4 * i + 1]) * inv_l),
-                     __float_as_uint(__uint_as_float(v[4 * i + 2]) * inv_l),
-                     __float_as_uint(__uint_as_float(v[4 * i + 3]) * inv_l));
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 8 * i + sub;
-        const long long to = __shfl_sync(0xffffffffu, off, row);
-        const uint4 x = ld_shared_v4(stage + row * 80u + quad * 16u);
-        if ((valid >> row) & 1u) *reinterpret_cast<uint4 *>(p.part_o + to + c0 + 4 * quad) = x;
-      }
-    }
-    __syncwarp();
-    return done;
-  }
-  const int head = g.h * p.G + r % p.G, row_at = g.s.q0 + tok;
-  if (row_valid && p.lse) p.lse[static_cast<size_t>(head) * p.total_q + row_at] = lse;
-  off = head * p.o_h + row_at * p.o_s;
-#pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    uint32_t v[32];
-    if (have_o) {
-      tmem_ld32(o_addr + c0, v);
-      tmem_ld_wait(v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0u;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        // the one rounding of O to its own type
-        __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * k]) * inv_l,
-                                                 __uint_as_float(v[8 * i + 2 * k + 1]) * inv_l);
-        w[k] = *reinterpret_cast<uint32_t *>(&x);
-      }
-      st_shared_v4(mine + 16 * i, w[0], w[1], w[2], w[3]);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 8 * i + sub;
-      const long long to = __shfl_sync(0xffffffffu, off, row);
-      const uint4 x = ld_shared_v4(stage + row * 80u + quad * 16u);
-      if ((valid >> row) & 1u)
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + to + c0 + 8 * quad) = x;
-    }
-  }
-  __syncwarp();
-  return done;
 }
 
 // Rows of the items that see no key at all (every row, if `all`): O = 0, lse = -inf.
@@ -722,29 +535,222 @@ __device__ __forceinline__ void wide_issuer(const PagedAttnParams &p, Walk walk,
   mbar_drain(bar(W::kMmaDone), 0, err);
 }
 
-// Softmax warpgroup of query tile t.
+// What a softmax warp knows of its walk, in shared memory: it has no registers to
+// spare for it while it goes over a tile's scores (with the walk in registers the
+// main loop spilled, 15 % of the time of a long causal prompt).
+struct WarpWalk {
+  Walk walk;
+  Segment seg;
+  bool more;
+};
+constexpr int kStageBytes = 2560;  // 32 rows of a warp's epilogue, 80 bytes apart
+constexpr int kWarpBytes = 2688;   // and its WarpWalk
+static_assert(kStageBytes + sizeof(WarpWalk) <= kWarpBytes, "a softmax warp's shared memory");
+
+// Softmax warpgroup of query tile t: a thread has one row (TMEM lane = tile row),
+// the dense forward's scheme. own: this warp's kWarpBytes of shared memory.
 template <int D>
-__device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, Walk walk, int t, uint32_t bar0,
-                                          uint32_t sRing, uint32_t tmem, volatile int *abort_flag, int *err) {
+__device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Walk &walk0, int t, uint32_t bar0,
+                                             uint32_t sRing, uint32_t tmem, uint8_t *own, volatile int *abort_flag,
+                                             int *err) {
+  using C = Cfg<D>;
   using W = WideBars<D>;
-  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  const int lane = threadIdx.x & 31;
   const int r = threadIdx.x & 127;
+  const uint32_t bar_t = bar0 + 8u * t;
   const uint32_t lane_off = static_cast<uint32_t>(r & ~31) << 16;
-  const uint32_t stage = sRing + Cfg<D>::kStages * Cfg<D>::kTileBytes + (threadIdx.x >> 5) * 2560u;
-  int steps = 0, ring = 0;
-  uint32_t u = 0;
-  Segment g, ahead;
-  bool more = walk.next(p, ahead);
-  while (more) {
-    g = ahead;
-    const int n = Walk::tiles(p, g, t), n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
-    if (!softmax_segment<D>(p, g, t, n, r, s_column(tmem, t) + lane_off, o_column(tmem, t) + lane_off,
-                            bar(W::kSFull + t), bar(W::kPFull + t), bar(W::kOFull + t), bar(W::kFull), sRing, ring, steps,
-                            u & 1u, stage, walk, ahead, more, abort_flag, err))
-      return;
-    ring += 2 * n_max;
+  const uint32_t s_addr = s_column(tmem, t) + lane_off, o_addr = o_column(tmem, t) + lane_off;
+  WarpWalk &ww = *reinterpret_cast<WarpWalk *>(own + kStageBytes);
+  if (lane == 0) {
+    ww.walk = walk0;
+    ww.more = ww.walk.next(p, ww.seg);
+  }
+  __syncwarp();
+  int steps = 0, ring = 0;  // key tiles of this query tile so far; ring position of the segment's first K tile
+  uint32_t u = 0;           // segments in which it had any
+  while (ww.more) {
+    const int n = Walk::tiles(p, ww.seg, t);
+    const int first = (2 * ww.seg.rb + t) * p.tok;  // the tile's first token within the sequence
+    const bool row_valid = r < p.tok * p.G && first + r / p.G < ww.seg.s.q_len;
+    const bool warp_valid = __any_sync(0xffffffffu, row_valid);
+    const int kv_len = ww.seg.s.kv_len, j0 = ww.seg.j0;
+    // last key of the tile's first token, and of this row (rows of no token --
+    // zeros, or other sequences' rows -- see every key: nothing of them is written)
+    const int tile_last = p.causal ? kv_len - ww.seg.s.q_len + first : kv_len - 1;
+    const int row_last = row_valid && p.causal ? min(tile_last + r / p.G, kv_len - 1) : kv_len - 1;
+    const float c2 = p.scale_log2;
+    const int *row = n > 0 && pages_missing(p, ww.seg) ? page_row(p, ww.seg) : nullptr;  // to be looked up tile by tile
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const unsigned there = row ? pages_there(p, row, kv_len, j0 + j) : 0xffffffffu;
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait(bar_t + 8u * W::kSFull, static_cast<uint32_t>(steps + j) & 1u, abort_flag, err));
+      if (!ok) break;
+      tc_fence_after();
+      const int kv0 = (j0 + j) * kRowsPerTile;
+      if (warp_valid) {
+        const bool cut = kv0 + kRowsPerTile - 1 > tile_last;  // some row does not see all keys of the tile
+        const int last = row_last - kv0;
+        auto mask_scores = [&](uint32_t *x, int c0, int cols) {
+          if (cut) {
+#pragma unroll
+            for (int c = 0; c < cols; ++c)
+              if (c0 + c > last) x[c] = __float_as_uint(-INFINITY);
+          }
+          if (there != 0xffffffffu) {
+            const int shift = p.page_log2 < 7 ? p.page_log2 : 31;  // a larger page: bit 0
+#pragma unroll
+            for (int c = 0; c < cols; ++c)
+              if (!((there >> ((c0 + c) >> shift)) & 1u)) x[c] = __float_as_uint(-INFINITY);
+          }
+        };
+        auto load_scores = [&](uint32_t(&sr)[128]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * i]));
+          tmem_ld_wait(sr);
+          mask_scores(sr, 0, 128);
+        };
+        uint32_t pk[64];
+        uint32_t sr[128];
+        load_scores(sr);
+        float rowsum;
+        if (j == 0) m = row_max(reinterpret_cast<const float *>(sr)) * c2;
+        rowsum = exp_row<false, 0>(reinterpret_cast<const float *>(sr), c2, (m == -INFINITY) ? 0.f : m, pk);
+        if (j > 0) {
+          // as in the dense forward: the reference moves, and O with it, only
+          // when the tile's P would sum to more than 2^8 or there is none yet
+          const bool big = row_valid && (!(rowsum <= kRescaleSum) || (m == -INFINITY && rowsum > 0.f));
+          if (__any_sync(0xffffffffu, big)) {
+            float mx = -INFINITY;  // 32 columns at a time: few live registers
+#pragma unroll 1
+            for (int cb = 0; cb < 4; ++cb) {
+              uint32_t x[32];
+              tmem_ld32(s_addr + 32 * cb, x);
+              tmem_ld_wait(x);
+              mask_scores(x, 32 * cb, 32);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) mx = fmaxf(mx, __uint_as_float(x[c]));
+            }
+            const float m_new = fmaxf(m, mx * c2);
+            const float alpha = (m_new == -INFINITY) ? 1.f : ex2_approx(m - m_new);
+            m = m_new;
+            l *= alpha;
+            scale_o<D>(o_addr, alpha);
+            load_scores(sr);
+            rowsum = exp_row<false, 0>(reinterpret_cast<const float *>(sr), c2, (m == -INFINITY) ? 0.f : m, pk);
+          }
+        }
+        l += rowsum;
+        tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+        tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+        tmem_st_wait();
+      }
+      if (kv_len - kv0 < kRowsPerTile) {
+        const int cv = ring + 2 * j + 1, slot = cv % C::kStages;  // ring position of the V tile
+        ok = clear_tail<D>(kv_len - kv0, sRing + slot * C::kTileBytes, bar0 + 8u * (W::kFull + slot), (cv / C::kStages) & 1,
+                           abort_flag, err);
+        if (!ok) break;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_t + 8u * W::kPFull);  // one arrival per warp
+    }
+    // what the epilogue needs of the segment; then the next one, while the last product runs
+    const int slot = ww.seg.slot, h = ww.seg.h, q0 = ww.seg.s.q0;
+    ring += 2 * max(Walk::tiles(p, ww.seg, 0), Walk::tiles(p, ww.seg, 1));
     steps += n;
-    if (n > 0) ++u;
+    __syncwarp();
+    if (lane == 0) ww.more = ww.walk.next(p, ww.seg);
+    __syncwarp();
+    bool have_o = false;
+    if (ok && n > 0) {
+      have_o = __all_sync(0xffffffffu, mbar_wait(bar_t + 8u * W::kOFull, u & 1u, abort_flag, err));
+      tc_fence_after();
+      ++u;
+    }
+    if (!ok || (n > 0 && !have_o)) return;  // (a warp that gives up makes the others give up too)
+    if (!warp_valid) continue;
+    const float inv_l = l > 0.f ? 1.f / l : 0.f;
+    const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    const unsigned valid = __ballot_sync(0xffffffffu, row_valid);
+    // Rows leave through shared memory, 64 bytes of each at a time, so that a
+    // store instruction writes 64 bytes of eight rows (each lane its own row, 16
+    // bytes at a time, cost twice the sectors: 10,000 clocks a segment, now
+    // about half). `stage`: 32 rows of this warp, 80 bytes apart.
+    const uint32_t stage = smem_addr(own), mine = stage + lane * 80u;
+    const int sub = lane >> 2, quad = lane & 3;
+    long long off;  // this lane's row in the output, elements
+    if (slot >= 0) {
+      const size_t at = static_cast<size_t>(slot) * p.part_rows + t * p.tok * p.G + r;
+      if (row_valid) p.part_lse[at] = lse;
+      if (!have_o) continue;  // no key seen: the merge does not read O
+      off = static_cast<long long>(at) * D;
+      uint32_t v[16];
+      tmem_ld16(o_addr, v);
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 16) {
+        tmem_ld_wait(v);
+        __syncwarp();  // the stage has been read
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st_shared_v4(mine + 16 * i, __float_as_uint(__uint_as_float(v[4 * i]) * inv_l),
+                       __float_as_uint(__uint_as_float(v[4 * i + 1]) * inv_l),
+                       __float_as_uint(__uint_as_float(v[4 * i + 2]) * inv_l),
+                       __float_as_uint(__uint_as_float(v[4 * i + 3]) * inv_l));
+        if (c0 + 16 < D) tmem_ld16(o_addr + c0 + 16, v);  // the next columns meanwhile
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 8 * i + sub;
+          const long long to = __shfl_sync(0xffffffffu, off, row);
+          const uint4 x = ld_shared_v4(stage + row * 80u + quad * 16u);
+          if ((valid >> row) & 1u) *reinterpret_cast<uint4 *>(p.part_o + to + c0 + 4 * quad) = x;
+        }
+      }
+      tmem_ld_wait(v);
+      __syncwarp();
+      continue;
+    }
+    const int head = h * p.G + r % p.G, row_at = q0 + first + r / p.G;
+    if (row_valid && p.lse) p.lse[static_cast<size_t>(head) * p.total_q + row_at] = lse;
+    off = head * p.o_h + row_at * p.o_s;
+    uint32_t v[32];
+    if (have_o) {
+      tmem_ld32(o_addr, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0u;
+    }
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+      tmem_ld_wait(v);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // the one rounding of O to its own type
+          __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * k]) * inv_l,
+                                                   __uint_as_float(v[8 * i + 2 * k + 1]) * inv_l);
+          w[k] = *reinterpret_cast<uint32_t *>(&x);
+        }
+        st_shared_v4(mine + 16 * i, w[0], w[1], w[2], w[3]);
+      }
+      if (have_o && c0 + 32 < D) tmem_ld32(o_addr + c0 + 32, v);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + sub;
+        const long long to = __shfl_sync(0xffffffffu, off, row);
+        const uint4 x = ld_shared_v4(stage + row * 80u + quad * 16u);
+        if ((valid >> row) & 1u)
+          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + to + c0 + 8 * quad) = x;
+      }
+    }
+    tmem_ld_wait(v);
+    __syncwarp();
   }
 }
 
@@ -878,7 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) wide_issuer<D>(p, walk, warp == kMmaWarp ? 0 : 1, bar0, sQ, sRing, tmem, turn, abort_flag, err);
       __syncwarp();
     } else {
-      wide_softmax<D>(p, walk, warp >> 2, bar0, sRing, tmem, abort_flag, err);
+      wide_softmax<D>(p, walk, warp >> 2, bar0, sRing, tmem, smem + 2 * C::kTileBytes + C::kStages * C::kTileBytes + warp * kWarpBytes,
+                      abort_flag, err);
     }
   }
 
