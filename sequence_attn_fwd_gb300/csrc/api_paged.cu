@@ -184,7 +184,7 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
   const cuuint64_t qh = Hq > 1 ? static_cast<cuuint64_t>(q_head_stride) : uD;
   const cuuint64_t qs = total_q > 1 ? static_cast<cuuint64_t>(q_row_stride) : uD;
   const int tok = 128 / G;
-  CUtensorMap tq, tqn[3], tk, tv;
+  CUtensorMap tq{}, tqn[3] = {}, tk, tv;
   const cuuint64_t q_dims[4] = {uD, static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(total_q),
                                 static_cast<cuuint64_t>(cache->Hkv)};
   const cuuint64_t q_strides[3] = {qh * 2, qs * 2, qh * 2 * G};
@@ -192,11 +192,14 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
                                  static_cast<cuuint64_t>(cache->n_pages)};
   const cuuint64_t kv_strides[3] = {uD * 2, uD * 2 * cache->page_size, static_cast<cuuint64_t>(cache->page_stride) * 2};
   const unsigned box_rows = cache->page_size < 128 ? cache->page_size : 128;
+  // the maps that the call can need: no sequence has more rows than all have
+  const long long rows = static_cast<long long>(total_q) * G;
   for (int i = 0; i < 3; ++i) {
     const int few = (16 << i) / G;
-    if (!make_map_4d(&tqn[i], q, q_dims, q_strides, G, few > 0 ? few : 1)) return keep_cuda_error(cudaErrorInvalidValue);
+    if ((i == 0 || rows > (8 << i)) && !make_map_4d(&tqn[i], q, q_dims, q_strides, G, few > 0 ? few : 1))
+      return keep_cuda_error(cudaErrorInvalidValue);
   }
-  if (!make_map_4d(&tq, q, q_dims, q_strides, G, tok) ||
+  if ((rows > 64 && !make_map_4d(&tq, q, q_dims, q_strides, G, tok)) ||
       !make_map_4d(&tk, cache->k_pages, kv_dims, kv_strides, box_rows, 1) ||
       !make_map_4d(&tv, cache->v_pages, kv_dims, kv_strides, box_rows, 1))
     return keep_cuda_error(cudaErrorInvalidValue);

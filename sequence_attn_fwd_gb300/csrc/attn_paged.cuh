@@ -897,90 +897,126 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Rows [r0, r0 + kRows) of a cut item, by one warp, its loads overlapping: the
-// weights exp(lse_i - max) of each row's partials, lane i the i-th, then their
-// weighted sum in the order of the keys, four (D = 128) or two columns a lane.
-template <int D, int kRows, int kUnroll>
-__device__ __forceinline__ void merge_rows(const PagedAttnParams &p, const int4 &cut, int r0) {
-  const int lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x, c1 = cut.w;
+// A lane's columns of row `row` of the partial that CTA c left of the item begun by CTA c0.
+template <int D>
+struct Partials {
+  static constexpr int kCols = D / 32;  // columns of a lane
+  const float *o, *lse;
+  int rows, c0;
+  __device__ __forceinline__ Partials(const PagedAttnParams &p)
+      : o(p.part_o + (threadIdx.x & 31) * kCols), lse(p.part_lse), rows(p.part_rows), c0(blockIdx.x) {}
+  __device__ __forceinline__ size_t at(int c, int row) const {
+    return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * rows + row;
+  }
+  __device__ __forceinline__ void load(int c, int row, float (&v)[kCols]) const {
+    const float *x = o + at(c, row) * D;
+    if constexpr (kCols == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(x);
+    else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(x);
+  }
+};
+
+// One merged row of a cut item to O and lse: acc / sum, m + ln sum.
+template <int D>
+__device__ __forceinline__ void merged_row(const PagedAttnParams &p, const int4 &cut, int r, const float (&acc)[D / 32],
+                                           float m, float sum) {
   constexpr int kCols = D / 32;
-  // the partial of row r0 + u (the last row again past it) that CTA c left
-  auto part = [&](int c, int u) -> size_t {
-    return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + min(r0 + u, cut.y - 1);
-  };
-  float acc[kRows][kCols] = {};
-  float m[kRows], sum[kRows] = {};
+  const int lane = threadIdx.x & 31;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int head = cut.z * p.G + r % p.G, row = cut.x + r / p.G;
+  __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h + row * p.o_s +
+                                                           lane * kCols);
 #pragma unroll
-  for (int u = 0; u < kRows; ++u) m[u] = -INFINITY;
-  // a timeout somewhere: the partials may be missing, the rows come out empty
-  const bool failed = *reinterpret_cast<volatile int *>(&g_device_error) != kErrNone;
-  if (!failed) {
-    for (int c = c0 + lane; c <= c1; c += 32)
+  for (int i = 0; i < kCols / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if (lane == 0 && p.lse)
+    p.lse[static_cast<size_t>(head) * p.total_q + row] = sum > 0.f ? m + logf(sum) : -INFINITY;
+}
+
+// Rows of a cut item with at most kParts partials: a warp takes kRows of them and
+// loads lse and O of all at once.
+template <int D, int kParts, int kRows>
+__device__ __forceinline__ void merge_few(const PagedAttnParams &p, const int4 &cut, int n, bool failed, int warp,
+                                          int warps) {
+  const Partials<D> parts(p);
+  constexpr int kCols = D / 32;
+  for (int r0 = warp * kRows; r0 < cut.y; r0 += warps * kRows) {
+    float v[kParts][kRows][kCols], w[kParts][kRows];
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) m[u] = fmaxf(m[u], p.part_lse[part(c, u)]);
-#pragma unroll
-    for (int u = 0; u < kRows; ++u)
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], off));
-    for (int cb = c0; cb <= c1; cb += 32) {
-      float w[kRows];
+    for (int k = 0; k < kParts; ++k)
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
-        const float lse = cb + lane <= c1 ? p.part_lse[part(cb + lane, u)] : -INFINITY;
-        w[u] = lse == -INFINITY ? 0.f : expf(lse - m[u]);
-        sum[u] += w[u];
-      }
-      const int k_end = min(32, c1 - cb + 1);
-#pragma unroll kUnroll
-      for (int k = 0; k < k_end; ++k) {
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          const float wk = __shfl_sync(0xffffffffu, w[u], k);
-          float v[kCols] = {};
-          if (wk != 0.f) {  // a partial that saw no key has no O
-            const float *x = p.part_o + part(cb + k, u) * D + lane * kCols;
-            if constexpr (kCols == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(x);
-            else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(x);
-          }
-#pragma unroll
-          for (int i = 0; i < kCols; ++i) acc[u][i] = fmaf(wk, v[i], acc[u][i]);
+        w[k][u] = -INFINITY;
+        if (k < n && r0 + u < cut.y && !failed) {
+          w[k][u] = parts.lse[parts.at(blockIdx.x + k, r0 + u)];
+          parts.load(blockIdx.x + k, r0 + u, v[k][u]);
         }
       }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (r0 + u >= cut.y) break;
+      float m = w[0][u], acc[kCols] = {}, sum = 0.f;
+#pragma unroll
+      for (int k = 1; k < kParts; ++k) m = fmaxf(m, w[k][u]);
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        if (w[k][u] == -INFINITY) continue;  // a partial that saw no key has no O
+        const float wk = expf(w[k][u] - m);
+        sum += wk;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) acc[i] = fmaf(wk, v[k][u][i], acc[i]);
+      }
+      merged_row<D>(p, cut, r0 + u, acc, m, sum);
     }
-  }
-#pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    const int r = r0 + u;
-    if (r >= cut.y) break;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], off);
-    const float inv = sum[u] > 0.f ? 1.f / sum[u] : 0.f;
-    const int head = cut.z * p.G + r % p.G, row = cut.x + r / p.G;
-    __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h +
-                                                             row * p.o_s + lane * kCols);
-#pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[u][2 * i] * inv, acc[u][2 * i + 1] * inv);
-    if (lane == 0 && p.lse)
-      p.lse[static_cast<size_t>(head) * p.total_q + row] = sum[u] > 0.f ? m[u] + logf(sum[u]) : -INFINITY;
   }
 }
 
 // The rows of the items that were cut: CTA blockIdx.x of the attention began such
-// an item and described it (first token, rows, KV head, last CTA). Bound by
-// latency, two dependent loads: an item of few rows, which can have many
-// partials, takes a row a warp and eight partials at a time, one of many rows,
-// which has few, four rows a warp.
-constexpr int kMergeThreads = 256, kMergeRows = 4;
+// an item and described it (first token, rows, KV head, last CTA). Per row the
+// weights exp(lse_i - max) of its partials and their weighted sum in the order of
+// the keys. Bound by latency, so the loads are made to overlap: with two (four)
+// partials a warp takes four (two) rows at once; with more, one row, eight
+// partials at a time. (Loads that wait for the weights, two partials at a time:
+// 17 us behind the attention of a batch of drafts, this: 8.)
+constexpr int kMergeThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_constant__ PagedAttnParams p) {
   wait_prerequisites();
   const int4 cut = p.cuts[blockIdx.x];
+  const int lane = threadIdx.x & 31;
   const int warp = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5), warps = gridDim.y * (kMergeThreads / 32);
-  if (cut.y <= warps) {
-    if (warp < cut.y) merge_rows<D, 1, 8>(p, cut, warp);
-  } else if (warp * kMergeRows < cut.y) {
-    merge_rows<D, kMergeRows, 2>(p, cut, warp * kMergeRows);
+  const int c0 = blockIdx.x, n = cut.w - c0 + 1;
+  // a timeout somewhere: the partials may be missing, the rows come out empty
+  const bool failed = *reinterpret_cast<volatile int *>(&g_device_error) != kErrNone;
+  if (n <= 2) return merge_few<D, 2, 4>(p, cut, n, failed, warp, warps);
+  if (n <= 4) return merge_few<D, 4, 2>(p, cut, n, failed, warp, warps);
+  const Partials<D> parts(p);
+  constexpr int kCols = D / 32;
+  for (int r = warp; r < cut.y; r += warps) {
+    float m = -INFINITY, sum = 0.f, acc[kCols] = {};
+    if (!failed) {
+      for (int k = lane; k < n; k += 32) m = fmaxf(m, parts.lse[parts.at(c0 + k, r)]);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      for (int k0 = 0; k0 < n; k0 += 8) {
+        float v[8][kCols], w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          w[k] = -INFINITY;
+          if (k0 + k < n) {
+            w[k] = parts.lse[parts.at(c0 + k0 + k, r)];
+            parts.load(c0 + k0 + k, r, v[k]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (w[k] == -INFINITY) continue;
+          const float wk = expf(w[k] - m);
+          sum += wk;
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) acc[i] = fmaf(wk, v[k][i], acc[i]);
+        }
+      }
+    }
+    merged_row<D>(p, cut, r, acc, m, sum);
   }
 }
 
@@ -989,15 +1025,23 @@ cudaError_t launch_typed(const QueryMaps &tq, const CUtensorMap &tk, const CUten
                          cudaStream_t stream) {
   auto kernel = attn_paged_kernel<D>;
   constexpr int kSmem = Cfg<D>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  // once per device (the attribute holds for the kernel on the current device)
+  static std::atomic<bool> prepared[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !prepared[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) prepared[dev].store(true, std::memory_order_release);
+  }
   const int n_ctas = sm_count() < kPagedMaxCtas ? sm_count() : kPagedMaxCtas;
   kernel<<<n_ctas, kThreads, kSmem, stream>>>(tq, tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || n_ctas == 1) return e;
   // the merge starts while the attention still runs and waits for its end inside
   cudaLaunchConfig_t cfg{};
-  constexpr int kRows = kMergeThreads / 32 * kMergeRows;
+  constexpr int kRows = kMergeThreads / 32 * 4;
   cfg.gridDim = dim3(n_ctas - 1, (p.part_rows + kRows - 1) / kRows);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
