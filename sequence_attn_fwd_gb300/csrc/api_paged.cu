@@ -105,7 +105,7 @@ int make_table(seqattn::RopeTable *t, const double *inv_freq, const int *axes, i
     const double turns = inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
     double frac = turns - floor(turns);
     if (frac >= 1.0) frac = 0.0;  // a tiny negative rounds up to a whole turn
-    t->turns[i] = static_cast<uint64_t>(ldexp(frac, 64));  // below 2^64, as frac < 1
+    t->turns[i] = static_cast<uint64_t>(frac * 18446744073709551616.0);  // times 2^64, exact; below it, as frac < 1
     t->axis[i] = static_cast<signed char>(axes[i]);
   }
   return ATTN_OK;

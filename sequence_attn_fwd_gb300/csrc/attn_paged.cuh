@@ -1040,17 +1040,9 @@ cudaError_t launch_typed(const QueryMaps &tq, const CUtensorMap &tk, const CUten
   e = cudaGetLastError();
   if (e != cudaSuccess || n_ctas == 1) return e;
   // the merge starts while the attention still runs and waits for its end inside
-  cudaLaunchConfig_t cfg{};
   constexpr int kRows = kMergeThreads / 32 * 4;
-  cfg.gridDim = dim3(n_ctas - 1, (p.part_rows + kRows - 1) / kRows);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
+  return launch_dependent(merge_kernel<D>, dim3(n_ctas - 1, (p.part_rows + kRows - 1) / kRows), dim3(kMergeThreads), stream,
+                          p);
 }
 
 }  // namespace paged

@@ -206,6 +206,22 @@ cudaError_t launch_compact(const PoolList &pools, const int *page_table, int *ou
 
 size_t compact_workspace_ints(int n_pages);
 
+// Launches a kernel that may start before the one ahead of it on the stream has
+// finished; it calls wait_prerequisites() before it touches memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream, Args &&...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // Shared by the C-ABI files: keeps the error for attn_last_cuda_error() and
 // returns ATTN_ERR_CUDA; the driver's tensor-map encoder (null if not found).
 int keep_cuda_error(cudaError_t e);

@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace seqattn {
 namespace {
@@ -45,18 +46,26 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
   return incl - x + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
+// The free ones of this thread's eight pages from `at` on, one bit each.
+constexpr int kPagesPerThread = 8;
+__device__ __forceinline__ unsigned free_mask(const int *refs, int n_pages, int at) {
+  unsigned mask = 0;
+#pragma unroll
+  for (int i = 0; i < kPagesPerThread; ++i)
+    if (at + i < n_pages && refs[at + i] == 0) mask |= 1u << i;
+  return mask;
+}
+
 // Finds the `want` lowest free pages and calls give(rank, page) for each, until
 // they run out; returns how many there were (the same on every thread).
+// `ready`: free_mask of the first kPlanThreads * kPagesPerThread pages, which a
+// caller loads along with what it needs first.
 template <typename Give>
-__device__ int find_free(const int *refs, int n_pages, int want, int *warp_sums, Give give) {
-  constexpr int kPer = 8;
+__device__ int find_free(const int *refs, int n_pages, int want, unsigned ready, int *warp_sums, Give give) {
   int found = 0;
-  for (int base = 0; base < n_pages && found < want; base += kPlanThreads * kPer) {
-    const int at = base + threadIdx.x * kPer;
-    unsigned mask = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (at + i < n_pages && refs[at + i] == 0) mask |= 1u << i;
+  for (int base = 0; base < n_pages && found < want; base += kPlanThreads * kPagesPerThread) {
+    const int at = base + threadIdx.x * kPagesPerThread;
+    unsigned mask = base == 0 ? ready : free_mask(refs, n_pages, at);
     int total;
     int rank = found + block_scan(__popc(mask), warp_sums, &total);
     while (mask && rank < want) {
@@ -85,18 +94,19 @@ __device__ __forceinline__ int pages_for(long long tokens, int page_log2) {
   return static_cast<int>((tokens + (1ll << page_log2) - 1) >> page_log2);
 }
 
-// prefix[0..n] of need(i), n <= kPagedMaxRows (prefix saturates far above any pool).
-template <typename Need>
-__device__ void scan_needs(int *prefix, int n, int *warp_sums, Need need) {
+// prefix[0..n]: exclusive sums of the needs that prefix[i] holds at the start, n <= kPagedMaxRows.
+__device__ void scan_needs(int *prefix, int n, int *warp_sums) {
+  __syncthreads();
   const int per = (n + kPlanThreads - 1) / kPlanThreads;
   const int i0 = min(n, static_cast<int>(threadIdx.x) * per), i1 = min(n, i0 + per);
   int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += need(i);
+  for (int i = i0; i < i1; ++i) sum += prefix[i];
   int total;
   int at = block_scan(sum, warp_sums, &total);
   for (int i = i0; i < i1; ++i) {
+    const int need = prefix[i];
     prefix[i] = at;
-    at += need(i);
+    at += need;
   }
   if (threadIdx.x == 0) prefix[n] = total;
   __syncthreads();
@@ -104,40 +114,41 @@ __device__ void scan_needs(int *prefix, int n, int *warp_sums, Need need) {
 
 // One CTA: needs, prefix sums, then one walk over the reference counts that
 // gives rank r to the row whose range holds it. A row that the pool cannot
-// serve whole (only the last one reached can have got some pages) gives them back.
+// serve whole (only the last one reached can have got some pages) gives them
+// back. Bound by latency: lengths and the first counts are loaded together.
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(PageTables t, const int *n_new, int *status) {
   __shared__ int prefix[kPagedMaxRows + 1];
+  __shared__ int length[kPagedMaxRows];  // -1: the row's table has no room
   __shared__ int warp_sums[33];
   const long long room = static_cast<long long>(t.max_pages) << t.page_log2;
-  auto len_of = [&](int b) -> long long { return max(t.kv_lens[b], 0); };
-  auto more = [&](int b) -> long long { return max(n_new[b], 0); };
-  auto fits = [&](int b) { return len_of(b) + more(b) <= room; };
-  auto need = [&](int b) -> int {
-    if (!fits(b)) return 0;
-    const int n = pages_for(len_of(b) + more(b), t.page_log2) - pages_for(len_of(b), t.page_log2);
-    return min(n, t.n_pages + 1);  // a sum of more than the pool has is never served
-  };
-  scan_needs(prefix, t.B, warp_sums, need);
-  const int want = prefix[t.B];
-  const int got = find_free(t.page_refs, t.n_pages, want, warp_sums, [&](int rank, int page) {
+  const unsigned ready = free_mask(t.page_refs, t.n_pages, threadIdx.x * kPagesPerThread);
+  for (int b = threadIdx.x; b < t.B; b += kPlanThreads) {
+    const long long len = max(t.kv_lens[b], 0), want = len + max(n_new[b], 0);
+    const bool fits = want <= room;
+    length[b] = fits ? static_cast<int>(len) : -1;
+    // a sum of more than the pool has is never served
+    prefix[b] = fits ? min(pages_for(want, t.page_log2) - pages_for(len, t.page_log2), t.n_pages + 1) : 0;
+  }
+  scan_needs(prefix, t.B, warp_sums);
+  const int got = find_free(t.page_refs, t.n_pages, prefix[t.B], ready, warp_sums, [&](int rank, int page) {
     const int b = row_of_rank(prefix, t.B, rank);
-    t.page_table[b * t.table_stride + pages_for(len_of(b), t.page_log2) + rank - prefix[b]] = page;
+    t.page_table[b * t.table_stride + pages_for(length[b], t.page_log2) + rank - prefix[b]] = page;
     t.page_refs[page] = 1;
   });
   __syncthreads();
   for (int b = threadIdx.x; b < t.B; b += kPlanThreads) {
     const int n = prefix[b + 1] - prefix[b];
-    int st = fits(b) ? 0 : kStatusTooLong;
+    int st = length[b] >= 0 ? 0 : kStatusTooLong;
     if (n > 0 && prefix[b + 1] > got) {
       st = kStatusNoPages;
-      const int have = pages_for(len_of(b), t.page_log2);
+      const int have = pages_for(length[b], t.page_log2);
       for (int i = 0; i < got - prefix[b]; ++i) {
         int *e = &t.page_table[b * t.table_stride + have + i];
         t.page_refs[*e] = 0;
         *e = -1;
       }
     }
-    if (st == 0) t.kv_lens[b] = static_cast<int>(len_of(b) + more(b));
+    if (st == 0) t.kv_lens[b] = length[b] + max(n_new[b], 0);
     status[b] = st;
   }
 }
@@ -160,20 +171,28 @@ __global__ void __launch_bounds__(kPlanThreads)
     fork_plan_kernel(PageTables t, const __grid_constant__ PageList pairs, int *status) {
   __shared__ int prefix[kPageListMax + 1];
   __shared__ int warp_sums[33];
-  const int mask = (1 << t.page_log2) - 1;
-  const int room = static_cast<int>(min(static_cast<long long>(t.max_pages) << t.page_log2, 0x7fffffffll));
-  auto len_of = [&](int i) { return min(max(t.kv_lens[pairs.a[i]], 0), room); };
-  auto in_use = [&](int i) { return t.kv_lens[pairs.b[i]] != 0; };
-  auto need = [&](int i) -> int { return !in_use(i) && (len_of(i) & mask) != 0; };
-  scan_needs(prefix, pairs.n, warp_sums, need);
-  const int got = find_free(t.page_refs, t.n_pages, prefix[pairs.n], warp_sums, [&](int rank, int page) {
-    const int i = row_of_rank(prefix, pairs.n, rank);
-    t.page_table[pairs.b[i] * t.table_stride + (len_of(i) >> t.page_log2)] = page;
+  __shared__ int *entry[kPageListMax];  // where the target's own page goes
+  launch_dependents();
+  const unsigned ready = free_mask(t.page_refs, t.n_pages, threadIdx.x * kPagesPerThread);
+  const int i = threadIdx.x;  // kPageListMax pairs at most: one a thread
+  bool in_use = false;
+  if (i < pairs.n) {
+    const long long room = static_cast<long long>(t.max_pages) << t.page_log2;
+    const int dst = pairs.b[i];
+    in_use = t.kv_lens[dst] != 0;
+    const int len = static_cast<int>(min(static_cast<long long>(max(t.kv_lens[pairs.a[i]], 0)), room));
+    prefix[i] = !in_use && (len & ((1 << t.page_log2) - 1)) != 0;
+    entry[i] = t.page_table + dst * t.table_stride + (len >> t.page_log2);
+  }
+  scan_needs(prefix, pairs.n, warp_sums);
+  const int got = find_free(t.page_refs, t.n_pages, prefix[pairs.n], ready, warp_sums, [&](int rank, int page) {
+    *entry[row_of_rank(prefix, pairs.n, rank)] = page;
     t.page_refs[page] = 1;
   });
-  for (int i = threadIdx.x; i < pairs.n; i += kPlanThreads)
-    status[i] = in_use(i) ? kStatusInUse : (prefix[i + 1] > got && prefix[i + 1] > prefix[i] ? kStatusNoPages : 0);
+  if (i < pairs.n)
+    status[i] = in_use ? kStatusInUse : (prefix[i + 1] > got && prefix[i + 1] > prefix[i] ? kStatusNoPages : 0);
 }
+static_assert(kPageListMax <= kPlanThreads, "one pair a thread");
 
 // Copies `bytes` (a multiple of 16) with the CTA's threads, four 16-byte loads in flight each.
 __device__ __forceinline__ void copy_bytes(unsigned char *dst, const unsigned char *src, long long bytes) {
@@ -214,6 +233,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     fork_copy_kernel(PageTables t, const __grid_constant__ PoolList pools, const __grid_constant__ PageList pairs,
                      const int *status, int chunks) {
   const int i = blockIdx.y, src = pairs.a[i], dst = pairs.b[i];
+  wait_prerequisites();
   if (status[i] != 0) return;
   const int room = static_cast<int>(min(static_cast<long long>(t.max_pages) << t.page_log2, 0x7fffffffll));
   const int len = min(max(t.kv_lens[src], 0), room);
@@ -255,6 +275,7 @@ constexpr int kBlockPages = 4096;
 
 __global__ void __launch_bounds__(kPlanThreads) count_kernel(const int *refs, int n_pages, int *counts) {
   __shared__ int warp_sums[33];
+  launch_dependents();
   int live = 0;
 #pragma unroll
   for (int k = 0; k < kBlockPages / kPlanThreads; ++k) {
@@ -282,6 +303,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     rank_kernel(const int *refs, int n_pages, const int *counts, int n_blocks, int *n_live_out, int *n_moves, int *rank,
                 int *holes, int *movers, int *mover_refs) {
   __shared__ int warp_sums[33];
+  launch_dependents();
+  wait_prerequisites();
   int sum = 0;
   for (int i = threadIdx.x; i < n_blocks; i += kPlanThreads) sum += counts[i];
   int n_live;
@@ -327,6 +350,7 @@ __global__ void __launch_bounds__(kCopyThreads)
                 const int *page_refs, int *out_refs, int B, int max_pages, int n_pages, const int *n_live_in,
                 const int *n_moves_in, const int *rank, const int *holes, const int *movers, const int *mover_refs,
                 int chunks) {
+  wait_prerequisites();
   const int n_live = *n_live_in;
   const long long tid = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x;
   const long long threads = static_cast<long long>(gridDim.x) * kCopyThreads;
@@ -374,8 +398,8 @@ cudaError_t launch_fork(const PageTables &t, const PoolList &pools, const PageLi
   if (e != cudaSuccess) return e;
   const int chunks = chunks_of(pools);
   const dim3 grid(1 + static_cast<unsigned>(pools.total_layers) * chunks, pairs.n);
-  fork_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(t, pools, pairs, status, chunks > 0 ? chunks : 1);
-  return cudaGetLastError();
+  return launch_dependent(fork_copy_kernel, grid, dim3(kCopyThreads), stream, t, pools, pairs, status,
+                          chunks > 0 ? chunks : 1);
 }
 
 cudaError_t launch_copy(const PoolList &pools, const PageList &pairs, cudaStream_t stream) {
@@ -392,15 +416,15 @@ cudaError_t launch_compact(const PoolList &pools, const int *page_table, int *ou
   int *n_moves = workspace, *counts = n_moves + 1, *rank = counts + n_blocks, *holes = rank + n_pages,
       *movers = holes + n_pages, *mover_refs = movers + n_pages;  // compact_workspace_ints in all
   count_kernel<<<n_blocks, kPlanThreads, 0, stream>>>(page_refs, n_pages, counts);
-  rank_kernel<<<n_blocks, kPlanThreads, 0, stream>>>(page_refs, n_pages, counts, n_blocks, n_live, n_moves, rank, holes,
-                                                    movers, mover_refs);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  e = launch_dependent(rank_kernel, dim3(n_blocks), dim3(kPlanThreads), stream, page_refs, n_pages, counts, n_blocks,
+                       n_live, n_moves, rank, holes, movers, mover_refs);
+  if (e != cudaSuccess) return e;
   const int chunks = chunks_of(pools);
-  move_kernel<<<device_sm_count() * 8, kCopyThreads, 0, stream>>>(
-      pools, page_table, out_table, table_stride, page_refs, out_refs, B, max_pages, n_pages, n_live, n_moves, rank,
-      holes, movers, mover_refs, chunks > 0 ? chunks : 1);
-  return cudaGetLastError();
+  return launch_dependent(move_kernel, dim3(device_sm_count() * 8), dim3(kCopyThreads), stream, pools, page_table,
+                          out_table, table_stride, page_refs, out_refs, B, max_pages, n_pages, n_live, n_moves, rank,
+                          holes, movers, mover_refs, chunks > 0 ? chunks : 1);
 }
 
 size_t compact_workspace_ints(int n_pages) {
