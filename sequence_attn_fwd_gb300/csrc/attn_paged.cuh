@@ -542,10 +542,18 @@ struct WarpWalk {
   Walk walk;
   Segment seg;
   bool more;
+  int ring;  // ring position of the segment's first K tile
 };
 constexpr int kStageBytes = 2560;  // 32 rows of a warp's epilogue, 80 bytes apart
 constexpr int kWarpBytes = 2688;   // and its WarpWalk
 static_assert(kStageBytes + sizeof(WarpWalk) <= kWarpBytes, "a softmax warp's shared memory");
+
+// x, in a way that nothing computed from it moves ahead of this place: what the
+// ends of a segment need must not sit in registers through its main loop.
+__device__ __forceinline__ int hidden(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
 
 // Softmax warpgroup of query tile t: a thread has one row (TMEM lane = tile row),
 // the dense forward's scheme. own: this warp's kWarpBytes of shared memory.
@@ -563,35 +571,43 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
   WarpWalk &ww = *reinterpret_cast<WarpWalk *>(own + kStageBytes);
   if (lane == 0) {
     ww.walk = walk0;
+    ww.ring = 0;
     ww.more = ww.walk.next(p, ww.seg);
   }
   __syncwarp();
-  int steps = 0, ring = 0;  // key tiles of this query tile so far; ring position of the segment's first K tile
-  uint32_t u = 0;           // segments in which it had any
+  uint32_t steps = 0;  // key tiles of this query tile so far
+  uint32_t u = 0;      // segments in which it had any
   while (ww.more) {
     const int n = Walk::tiles(p, ww.seg, t);
-    const int first = (2 * ww.seg.rb + t) * p.tok;  // the tile's first token within the sequence
-    const bool row_valid = r < p.tok * p.G && first + r / p.G < ww.seg.s.q_len;
+    int first_key, row_rel, cut_from, tail_from;
+    bool row_valid, holes;
+    {
+      const int first = (2 * ww.seg.rb + t) * p.tok;  // the tile's first token within the sequence
+      const int tok = hidden(r) / p.G, kv_len = ww.seg.s.kv_len;
+      row_valid = r < p.tok * p.G && first + tok < ww.seg.s.q_len;
+      // last key of the tile's first token, and of this row (rows of no token --
+      // zeros, or other sequences' rows -- see every key: nothing of them is written)
+      const int tile_last = p.causal ? kv_len - ww.seg.s.q_len + first : kv_len - 1;
+      const int row_last = row_valid && p.causal ? min(tile_last + tok, kv_len - 1) : kv_len - 1;
+      first_key = ww.seg.j0 * kRowsPerTile;
+      row_rel = row_last - first_key;
+      cut_from = (tile_last + 1 - first_key) >> 7;   // the first tile of which some row does not see all keys
+      tail_from = (kv_len - first_key) >> 7;         // the tile that the sequence ends in
+      holes = n > 0 && pages_missing(p, ww.seg);     // pages have to be looked up tile by tile
+    }
     const bool warp_valid = __any_sync(0xffffffffu, row_valid);
-    const int kv_len = ww.seg.s.kv_len, j0 = ww.seg.j0;
-    // last key of the tile's first token, and of this row (rows of no token --
-    // zeros, or other sequences' rows -- see every key: nothing of them is written)
-    const int tile_last = p.causal ? kv_len - ww.seg.s.q_len + first : kv_len - 1;
-    const int row_last = row_valid && p.causal ? min(tile_last + r / p.G, kv_len - 1) : kv_len - 1;
     const float c2 = p.scale_log2;
-    const int *row = n > 0 && pages_missing(p, ww.seg) ? page_row(p, ww.seg) : nullptr;  // to be looked up tile by tile
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      const unsigned there = row ? pages_there(p, row, kv_len, j0 + j) : 0xffffffffu;
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait(bar_t + 8u * W::kSFull, static_cast<uint32_t>(steps + j) & 1u, abort_flag, err));
+      const unsigned there =
+          holes ? pages_there(p, page_row(p, ww.seg), ww.seg.s.kv_len, ww.seg.j0 + j) : 0xffffffffu;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_t + 8u * W::kSFull, (steps + j) & 1u, abort_flag, err));
       if (!ok) break;
       tc_fence_after();
-      const int kv0 = (j0 + j) * kRowsPerTile;
       if (warp_valid) {
-        const bool cut = kv0 + kRowsPerTile - 1 > tile_last;  // some row does not see all keys of the tile
-        const int last = row_last - kv0;
+        const bool cut = j >= cut_from;
+        const int last = row_rel - j * kRowsPerTile;  // the last key of the tile that this row sees
         auto mask_scores = [&](uint32_t *x, int c0, int cols) {
           if (cut) {
 #pragma unroll
@@ -646,10 +662,10 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
         tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
         tmem_st_wait();
       }
-      if (kv_len - kv0 < kRowsPerTile) {
-        const int cv = ring + 2 * j + 1, slot = cv % C::kStages;  // ring position of the V tile
-        ok = clear_tail<D>(kv_len - kv0, sRing + slot * C::kTileBytes, bar0 + 8u * (W::kFull + slot), (cv / C::kStages) & 1,
-                           abort_flag, err);
+      if (j >= tail_from) {
+        const int cv = ww.ring + 2 * j + 1, slot = cv % C::kStages;  // ring position of the V tile
+        ok = clear_tail<D>(ww.seg.s.kv_len - first_key - j * kRowsPerTile, sRing + slot * C::kTileBytes,
+                           bar0 + 8u * (W::kFull + slot), (cv / C::kStages) & 1, abort_flag, err);
         if (!ok) break;
       }
       tc_fence_before();
@@ -657,11 +673,13 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
       if (lane == 0) mbar_arrive(bar_t + 8u * W::kPFull);  // one arrival per warp
     }
     // what the epilogue needs of the segment; then the next one, while the last product runs
-    const int slot = ww.seg.slot, h = ww.seg.h, q0 = ww.seg.s.q0;
-    ring += 2 * max(Walk::tiles(p, ww.seg, 0), Walk::tiles(p, ww.seg, 1));
+    const int slot = ww.seg.slot, h = ww.seg.h, q0 = ww.seg.s.q0 + (2 * ww.seg.rb + t) * p.tok;
     steps += n;
     __syncwarp();
-    if (lane == 0) ww.more = ww.walk.next(p, ww.seg);
+    if (lane == 0) {
+      ww.ring += 2 * max(Walk::tiles(p, ww.seg, 0), Walk::tiles(p, ww.seg, 1));
+      ww.more = ww.walk.next(p, ww.seg);
+    }
     __syncwarp();
     bool have_o = false;
     if (ok && n > 0) {
@@ -678,11 +696,12 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
     // store instruction writes 64 bytes of eight rows (each lane its own row, 16
     // bytes at a time, cost twice the sectors: 10,000 clocks a segment, now
     // about half). `stage`: 32 rows of this warp, 80 bytes apart.
-    const uint32_t stage = smem_addr(own), mine = stage + lane * 80u;
-    const int sub = lane >> 2, quad = lane & 3;
+    const int ln = hidden(lane), rr = hidden(r);
+    const uint32_t stage = smem_addr(own), mine = stage + ln * 80u;
+    const int sub = ln >> 2, quad = ln & 3;
     long long off;  // this lane's row in the output, elements
     if (slot >= 0) {
-      const size_t at = static_cast<size_t>(slot) * p.part_rows + t * p.tok * p.G + r;
+      const size_t at = static_cast<size_t>(slot) * p.part_rows + t * p.tok * p.G + rr;
       if (row_valid) p.part_lse[at] = lse;
       if (!have_o) continue;  // no key seen: the merge does not read O
       off = static_cast<long long>(at) * D;
@@ -712,7 +731,7 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
       __syncwarp();
       continue;
     }
-    const int head = h * p.G + r % p.G, row_at = q0 + first + r / p.G;
+    const int head = h * p.G + rr % p.G, row_at = q0 + rr / p.G;
     if (row_valid && p.lse) p.lse[static_cast<size_t>(head) * p.total_q + row_at] = lse;
     off = head * p.o_h + row_at * p.o_s;
     uint32_t v[32];
