@@ -60,7 +60,7 @@ typedef struct {
  *             bytes; no other call may use it at the same time
  * Strides are in elements and multiples of 8. Rows that see no key: O = 0,
  * lse = -inf. Keys inside kv_lens must be finite. D 64 or 128, Hq / Hkv at
- * most 128, B at most 2048, max_pages * page_size at most 2^30, and at most
+ * most 128, B at most 4096, max_pages * page_size at most 2^30, and at most
  * 2^31 tiles of 128 keys over all row blocks of 256 rows (else
  * ATTN_ERR_UNSUPPORTED). Two kernels: the attention itself, its key tiles
  * dealt evenly over the SMs whatever the lengths, and the merge of the rows

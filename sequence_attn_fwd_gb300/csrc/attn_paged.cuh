@@ -45,13 +45,16 @@ struct Cfg {
   static constexpr int kNumBarriers = 2 + 2 * kStages + 7;
   // tiles of the wide form (Q, ring, epilogue) or of the narrow one (ring, P, Q), then
   // barriers, three words, warp sums, the first segment, the narrow form's
-  // reductions, prefix sums
-  static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 2 * 16 * D * 2;
+  // reductions. The prefix sums over the sequences are needed before the tiles
+  // arrive only: they lie where the ring of either form will be.
+  static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 64 * D * 2;
   static_assert(2 * kTileBytes + kStages * kTileBytes + 8 * 2688 <= kAreaBytes, "wide layout");
   static constexpr int kMaxBarriers = 2 * (196608 / kTileBytes) + 10;
   static constexpr int kRedFloats = 2 * 6 * 32;
-  static constexpr int kSmemBytes =
-      1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 24 + 48 + 4 * kRedFloats + 4 * (kPagedMaxSeqs + 1);
+  static constexpr int kPrefixAt = 65536;
+  static_assert(kPrefixAt >= 2 * kTileBytes && kPrefixAt + 4 * (kPagedMaxSeqs + 1) <= 2 * kTileBytes + kStages * kTileBytes,
+                "prefix sums inside either ring");
+  static constexpr int kSmemBytes = 1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 24 + 48 + 4 * kRedFloats;
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -208,14 +211,12 @@ __device__ __forceinline__ const int *page_row(const PagedAttnParams &p, const S
 // runs once per CTA costs its instruction fetches more than its work.
 struct Walk {
   int pos, end, per;
-  const int *prefix;
   const Segment *first;
   bool fresh;
-  __device__ __forceinline__ Walk(const int *prefix_, const Segment *first_, int B, int n_ctas)
-      : prefix(prefix_), first(first_), fresh(true) {
-    per = cost_per_cta(prefix[B], n_ctas);
-    pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(prefix[B])));
-    end = static_cast<int>(min(static_cast<long long>(pos) + per, static_cast<long long>(prefix[B])));
+  __device__ __forceinline__ Walk(int total, const Segment *first_, int n_ctas) : first(first_), fresh(true) {
+    per = cost_per_cta(total, n_ctas);
+    pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
+    end = static_cast<int>(min(static_cast<long long>(pos) + per, static_cast<long long>(total)));
   }
   // The segment of row block rb at cost `within` of it, which is position `pos`
   // (j0 == j1 if the range ends before its first tile).
@@ -245,10 +246,10 @@ struct Walk {
         rb = 0;
         if (++g.h >= p.cache.Hkv) {
           g.h = 0;
-          do ++g.b;
-          while (g.b < p.cache.B && prefix[g.b + 1] == prefix[g.b]);
-          if (g.b >= p.cache.B) return false;
-          g.s = sequence(p, g.b);
+          do {
+            if (++g.b >= p.cache.B) return false;
+            g.s = sequence(p, g.b);
+          } while (g.s.q_len == 0 || g.s.kv_len == 0);
           g.rbs = row_blocks(p, g.s);
         }
       }
@@ -805,20 +806,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   int *warp_sums = reinterpret_cast<int *>(tmem_slot + 4);
   Segment *first = reinterpret_cast<Segment *>(warp_sums + 24);
   float *red = reinterpret_cast<float *>(warp_sums + 36);
-  int *prefix = reinterpret_cast<int *>(red + C::kRedFloats);
+  int *prefix = reinterpret_cast<int *>(smem + C::kPrefixAt);
   const uint32_t bar0 = smem_addr(bars), base = smem_addr(smem);
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int *err = &g_device_error;
 
+  const int most = prefix_tiles(p, prefix, warp_sums);
   if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
-  const int most = prefix_tiles(p, prefix, warp_sums);
   const bool narrow = most * p.G <= 64;
   const L sh(most * p.G, p.G);
-  const Walk walk(prefix, first, p.cache.B, gridDim.x);
+  const Walk walk(prefix[p.cache.B], first, gridDim.x);
   int first_entry = -1;  // the producer's lanes: the first key tile's pages
   if (warp == kTmaWarp && walk.pos < walk.end) {
     Segment g;
@@ -869,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t at = base + (narrow ? sh.q_at() : 0);
     const int pieces = (narrow ? sh.q_bufs * sh.q_bytes() : 2 * C::kTileBytes) / 16;
     for (int i = threadIdx.x; i < pieces; i += kThreads) st_shared_v4(at + 16 * i, 0u, 0u, 0u, 0u);
-    fence_proxy_async_shared();
+    fence_proxy_async_shared();  // these and the prefix sums before the copies that follow
   }
   tc_fence_before();
   __syncthreads();

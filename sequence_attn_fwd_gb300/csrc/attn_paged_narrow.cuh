@@ -3,8 +3,8 @@
 //
 // The cost is reading K and V, and what bounds that is bytes in flight: with
 // 96, 128 KB of tiles per SM the 64-sequence batch of the benchmark (2.1 GB of
-// cache) took 490, 389 us. So shared memory goes to the ring (192 KB, 160 KB
-// beyond 32 rows), and the products are turned over, keys on the 128 rows of
+// cache) took 490, 389 us. So shared memory goes to the ring (192 KB), and the
+// products are turned over, keys on the 128 rows of
 // the tensor tile: S^T = K Q^T (128 keys x N rows, N = 16, 32 or 64) and
 // O^T += V^T P (D x N). Q and P are small then, no tensor row is wasted on
 // queries that do not exist, and a thread has one key: N exponentials instead
@@ -29,20 +29,19 @@ struct Narrow {
   static constexpr int kTileBytes = kRowsPerTile * D * 2;
   static constexpr int kPBytes = kRowsPerTile * 128;
   static constexpr int kMaxStages = 196608 / kTileBytes;
-  int N, tok, stages, q_bufs, groups;  // groups: softmax warpgroups
+  static constexpr int stages = kMaxStages;
+  int N, tok, q_bufs, groups;  // groups: softmax warpgroups
   __device__ __forceinline__ Narrow(int rows, int G) {
     N = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
     tok = max(1, N / G);
-    stages = (N == 64 ? 163840 : 196608) / kTileBytes;
-    q_bufs = N == 16 ? 2 : 1;
+    q_bufs = N == 64 ? 1 : 2;
     groups = N == 16 ? 1 : 2;
   }
   // shared memory behind the 1024-byte aligned start: ring, P, Q
   __device__ __forceinline__ int p_at() const { return stages * kTileBytes; }
   __device__ __forceinline__ int q_at() const { return p_at() + kPBytes; }
   __device__ __forceinline__ int q_bytes() const { return N * D * 2; }
-  static constexpr int kAreaBytes = 196608 + kPBytes + 2 * 16 * D * 2;  // N = 16 or 32; N = 64 needs less
-  static_assert(163840 + kPBytes + 64 * D * 2 <= kAreaBytes, "narrow layouts");
+  static constexpr int kAreaBytes = 196608 + kPBytes + 64 * D * 2;
   // barriers
   static constexpr int kFull = 0, kEmpty = kMaxStages, kQFull = 2 * kMaxStages, kQEmpty = kQFull + 2,
                        kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 1, kMmaDone = kPvDone + 1,
@@ -308,13 +307,16 @@ __device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const N
       };
       float x[C];
       float top = -INFINITY;
+      if (j > 0) {
 #pragma unroll
-      for (int h = 0; h < C; h += 16) {
-        load_scores(h, m + h, x + h);
+        for (int h = 0; h < C; h += 16) {
+          load_scores(h, m + h, x + h);
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) top = fmax3(top, x[h + c], x[h + c + 1]);
+          for (int c = 0; c < 16; c += 2) top = fmax3(top, x[h + c], x[h + c + 1]);
+        }
       }
-      if (!named_bar_and(id, 128, ok && !(top > 8.f))) {
+      // the first tile of a segment has no reference yet
+      if (j == 0 || !named_bar_and(id, 128, ok && !(top > 8.f))) {
         // maxima of the tile's 128 keys, then O and l onto the new reference
 #pragma unroll
         for (int h = 0; h < C; h += 16) {

@@ -139,7 +139,7 @@ struct PagedAttnParams {
   float scale_log2;
 };
 constexpr int kPagedMaxCtas = 160;   // CTAs of one launch (at most one per SM)
-constexpr int kPagedMaxSeqs = 2048;  // sequences of one launch (their prefix sums sit in shared memory)
+constexpr int kPagedMaxSeqs = 4096;  // sequences of one launch (their prefix sums sit in shared memory)
 constexpr int kPagedMaxRows = 4096;  // rows of a page table
 
 // Maps: q bf16 4-D [Hkv][total_q][G][D], box 64 x G x tok x 1, and the same with

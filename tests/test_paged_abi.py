@@ -59,8 +59,8 @@ def test_attn_paged_refusals(lib):
     assert run(D=96) == 2 and run(D=256) == 2
     assert run(page_size=8) == 2 and run(page_size=24) == 2 and run(page_size=0) == 1
     assert run(max_pages=1 << 27, table_stride=1 << 27) == 2  # more than 2^30 keys
-    assert run(total=1 << 29, wb=1 << 40, B=2048, max_pages=1 << 26, table_stride=1 << 26) == 2  # key tiles past 2^31
-    assert run(B=2049) == 2 and run(Hq=512) == 2  # too many sequences; more than 128 heads in a group
+    assert run(total=1 << 29, wb=1 << 40, B=4096, max_pages=1 << 26, table_stride=1 << 26) == 2  # key tiles past 2^31
+    assert run(B=4097) == 2 and run(Hq=512) == 2  # too many sequences; more than 128 heads in a group
     assert run(Hq=3) == 1 and run(causal=2) == 1 and run(scale=0.0) == 1 and run(scale=float("inf")) == 1
     assert run(page_stride=16 * 128) == 1 and run(page_stride=2 * 16 * 128 + 4) == 1 and run(table_stride=7) == 1
     assert run(q=0) == 1 and run(q=FAKE + 8) == 1 and run(o=FAKE + 2) == 1 and run(lse=FAKE + 2) == 1
@@ -119,7 +119,7 @@ def test_paged_append_refusals(lib):
         return lib.paged_append(None if q is None else ctypes.addressof(q), ctypes.addressof(k), ctypes.addressof(v),
                                 ctypes.addressof(c), pos, 64, 3, ctypes.addressof(f), ctypes.addressof(a), total, inter, None)
 
-    assert run(D=80) == 2 and run(page_size=12) == 2 and run(B=2049) == 2
+    assert run(D=80) == 2 and run(page_size=12) == 2 and run(B=4097) == 2
     assert run(k=rows(heads=3)) == 1 and run(v=rows(heads=1)) == 1 and run(total=-1) == 1 and run(inter=3) == 1
     assert run(q=rows(4), pos=0) == 1  # q without positions
     assert run(q=rows(4, out=FAKE + 4)) == 1 and run(k=rows(at=FAKE + 2)) == 1 and run(pos=FAKE + 1) == 1
