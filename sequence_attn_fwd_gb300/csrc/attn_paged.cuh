@@ -49,7 +49,7 @@ struct Cfg {
   // arrive only: they lie where the ring of either form will be.
   static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 64 * D * 2;
   static_assert(2 * kTileBytes + kStages * kTileBytes + 8 * 2688 <= kAreaBytes, "wide layout");
-  static constexpr int kMaxBarriers = 2 * (196608 / kTileBytes) + 10;
+  static constexpr int kMaxBarriers = 2 * (196608 / kTileBytes) + 11;
   static constexpr int kRedFloats = 2 * 6 * 32;
   static constexpr int kPrefixAt = 65536;
   static_assert(kPrefixAt >= 2 * kTileBytes && kPrefixAt + 4 * (kPagedMaxSeqs + 1) <= 2 * kTileBytes + kStages * kTileBytes,
@@ -841,9 +841,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(L::kQFull + i), 1);
         mbar_init(bar(L::kQEmpty + i), 1);
         mbar_init(bar(L::kSFull + i), 1);
+        mbar_init(bar(L::kPFull + i), 4 * sh.groups);
+        mbar_init(bar(L::kPvDone + i), 1);
       }
-      mbar_init(bar(L::kPFull), 4 * sh.groups);
-      mbar_init(bar(L::kPvDone), 1);
       mbar_init(bar(L::kMmaDone), 1);
     } else {
       mbar_init(bar(W::kQFull), 1);

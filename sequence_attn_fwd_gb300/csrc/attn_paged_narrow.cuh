@@ -3,8 +3,8 @@
 //
 // The cost is reading K and V, and what bounds that is bytes in flight: with
 // 96, 128 KB of tiles per SM the 64-sequence batch of the benchmark (2.1 GB of
-// cache) took 490, 389 us. So shared memory goes to the ring (192 KB), and the
-// products are turned over, keys on the 128 rows of
+// cache) took 490, 389 us. So shared memory goes to the ring (192 KB, 160 KB
+// beyond 32 rows), and the products are turned over, keys on the 128 rows of
 // the tensor tile: S^T = K Q^T (128 keys x N rows, N = 16, 32 or 64) and
 // O^T += V^T P (D x N). Q and P are small then, no tensor row is wasted on
 // queries that do not exist, and a thread has one key: N exponentials instead
@@ -16,7 +16,10 @@
 // Roles: warps 0-3 (and 4-7 for N > 16, with the upper half of the columns)
 // softmax, warp 8 MMA issuer, warp 9 producer. TMEM columns: S^T in two
 // buffers [0, N), [N, 2 N), O^T [2 N, 3 N). P goes through shared memory as
-// [key][row], 128 bytes a key, 128-byte swizzle.
+// [key][row], 128 bytes a key, 128-byte swizzle, in two buffers too (rows 0 and
+// N of the 64 that a key has room for, or two tiles when N = 64): with one, a
+// tile's P waited for the product of the tile before, 2,170 clocks a tile at
+// N = 16 (measured), above D = 64's share of the DRAM rate.
 #pragma once
 
 namespace seqattn {
@@ -29,22 +32,25 @@ struct Narrow {
   static constexpr int kTileBytes = kRowsPerTile * D * 2;
   static constexpr int kPBytes = kRowsPerTile * 128;
   static constexpr int kMaxStages = 196608 / kTileBytes;
-  static constexpr int stages = kMaxStages;
-  int N, tok, q_bufs, groups;  // groups: softmax warpgroups
+  int N, tok, stages, q_bufs, groups;  // groups: softmax warpgroups
   __device__ __forceinline__ Narrow(int rows, int G) {
     N = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
     tok = max(1, N / G);
+    stages = (N == 64 ? 163840 : 196608) / kTileBytes;
     q_bufs = N == 64 ? 1 : 2;
     groups = N == 16 ? 1 : 2;
   }
   // shared memory behind the 1024-byte aligned start: ring, P, Q
   __device__ __forceinline__ int p_at() const { return stages * kTileBytes; }
-  __device__ __forceinline__ int q_at() const { return p_at() + kPBytes; }
+  // P buffer b: its first key's first row
+  __device__ __forceinline__ int p_buf(uint32_t b) const { return p_at() + static_cast<int>(b) * (N == 64 ? kPBytes : 2 * N); }
+  __device__ __forceinline__ int q_at() const { return p_at() + (N == 64 ? 2 : 1) * kPBytes; }
   __device__ __forceinline__ int q_bytes() const { return N * D * 2; }
-  static constexpr int kAreaBytes = 196608 + kPBytes + 64 * D * 2;
+  static constexpr int kAreaBytes = 196608 + kPBytes + 2 * 32 * D * 2;
+  static_assert(163840 + 2 * kPBytes + 64 * D * 2 <= kAreaBytes, "narrow layouts");
   // barriers
   static constexpr int kFull = 0, kEmpty = kMaxStages, kQFull = 2 * kMaxStages, kQEmpty = kQFull + 2,
-                       kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 1, kMmaDone = kPvDone + 1,
+                       kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2, kMmaDone = kPvDone + 2,
                        kNumBarriers = kMmaDone + 1;
 };
 
@@ -148,7 +154,6 @@ __device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Na
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
   const uint32_t idesc_s = idesc_narrow(sh.N, false), idesc_o = idesc_narrow(sh.N, true);
   const uint32_t o_col = tmem + 2 * sh.N;
-  const uint64_t pd = sw128_desc(smem + sh.p_at(), kColBlockBytes, 1024);
   RingPos k{0, 0};
   uint32_t step = 0;  // key tiles so far
   int nq = 0;
@@ -181,7 +186,7 @@ __device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Na
       // buffer was read before P of the tile before this one was signalled
       const bool early = j + 1 < n && mbar_test(bar(C::kFull + k1.slot), k1.phase);
       if (early) scores(k1, step + 1, j + 2 == n);
-      if (!mbar_wait(bar(C::kPFull), step & 1u, abort_flag, err) ||
+      if (!mbar_wait(bar(C::kPFull + (step & 1u)), (step >> 1) & 1u, abort_flag, err) ||
           !mbar_wait(bar(C::kFull + v.slot), v.phase, abort_flag, err)) {
         ok = false;
         break;
@@ -191,12 +196,13 @@ __device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Na
       // upper 64 rows of the product read the bytes behind the tile and are
       // never looked at (rows of a product do not mix)
       const uint64_t vd = sw128_desc(smem + v.slot * C::kTileBytes, kColBlockBytes, 1024);
+      const uint64_t pd = sw128_desc(smem + sh.p_buf(step & 1u), kColBlockBytes, 1024);
 #pragma unroll 4
       for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
         mma_ss(o_col, vd + static_cast<uint64_t>(kk * 128), pd + static_cast<uint64_t>(kk * 128), idesc_o,
                (j > 0 || kk > 0) ? 1u : 0u);
       mma_commit(bar(C::kEmpty + v.slot));
-      mma_commit(bar(C::kPvDone));
+      mma_commit(bar(C::kPvDone + (step & 1u)));
       if (j + 1 < n && !early) {
         if (!mbar_wait(bar(C::kFull + k1.slot), k1.phase, abort_flag, err)) {
           ok = false;
@@ -246,7 +252,10 @@ __device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const N
   const int col0 = gi * C, id = 1 + gi;
   const uint32_t lane_off = static_cast<uint32_t>(32 * w) << 16;
   const uint32_t o_addr = tmem + lane_off + 2 * sh.N + col0;
-  const uint32_t p_row = smem + sh.p_at() + key * 128;
+  // until the product of key tile s (and so all before it) is done
+  auto product_done = [&](uint32_t s) {
+    return __all_sync(0xffffffffu, mbar_wait(bar(L::kPvDone + (s & 1u)), (s >> 1) & 1u, abort_flag, err));
+  };
   const float c2 = p.scale_log2;
   auto larger = [](float a, float b) { return fmaxf(a, b); };
   auto sum_of = [](float a, float b) { return a + b; };
@@ -334,7 +343,7 @@ __device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const N
         }
         ok = named_bar_and(id, 128, ok);
         if (ok && j > 0)
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kPvDone), (step - 1) & 1u, abort_flag, err));
+          ok = product_done(step - 1);
         tc_fence_after();
         const bool old = ok && j > 0;  // O holds the sum of the tiles before
 #pragma unroll
@@ -366,13 +375,15 @@ __device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const N
         __nv_bfloat162 pair = __floats2bfloat162_rn(a, b);
         pk[i / 2] = *reinterpret_cast<uint32_t *>(&pair);
       }
-      // the product of the tile before has read P
-      if (j > 0)
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::kPvDone), (step - 1) & 1u, abort_flag, err));
+      // the product of the tile before the last has read its P
+      if (step >= 2) ok = ok && product_done(step - 2);
       if (ok) {
+        // 16-byte pieces of this key's rows, at the swizzled places
+        const uint32_t p_key = smem + sh.p_at() + (sh.N == 64 ? (step & 1u) * L::kPBytes : 0u) + key * 128;
+        const int piece = (col0 + (sh.N == 64 ? 0 : static_cast<int>(step & 1u) * sh.N)) / 8;
 #pragma unroll
         for (int i = 0; i < C / 8; ++i)
-          st_shared_v4(p_row + (static_cast<uint32_t>((col0 / 8 + i) ^ (key & 7)) << 4), pk[4 * i], pk[4 * i + 1],
+          st_shared_v4(p_key + (static_cast<uint32_t>((piece + i) ^ (key & 7)) << 4), pk[4 * i], pk[4 * i + 1],
                        pk[4 * i + 2], pk[4 * i + 3]);
         const RingPos v = k.next(sh.stages);
         if (gi == 0 && g.s.kv_len - kv0 < kRowsPerTile)
@@ -381,11 +392,11 @@ __device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const N
         fence_proxy_async_shared();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kPFull));  // one arrival per warp
+        if (lane == 0) mbar_arrive(bar(L::kPFull + (step & 1u)));  // one arrival per warp
       }
       k = k.next(sh.stages).next(sh.stages);
     }
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::kPvDone), (step - 1) & 1u, abort_flag, err));
+    ok = ok && product_done(step - 1);
     tc_fence_after();
     // l over the keys, and from it each row's factor and lse
 #pragma unroll
