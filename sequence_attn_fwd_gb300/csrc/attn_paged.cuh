@@ -444,96 +444,119 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
   __syncwarp();
 }
 
-// MMA issuer of query tile t, one thread (the dense forward's scheme).
+// MMA issuer of query tile t (the dense forward's scheme): the whole warp, its
+// code uniform, one lane for the products. (As the code of a single thread it
+// took about 95 clocks an MMA to bring the operands into uniform registers,
+// longer than the MMA itself; both issuers take turns, so that was the time of a
+// key tile.)
 template <int D>
-__device__ __forceinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, int t, uint32_t bar0,
-                                         uint32_t sQ, uint32_t sRing, uint32_t tmem, volatile int *turn,
-                                         volatile int *abort_flag, int *err) {
+__device__ __forceinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, int t_in, uint32_t bar0, uint32_t sQ,
+                                            uint32_t sRing, uint32_t tmem_in, volatile int *turn,
+                                            volatile int *abort_flag, int *err) {
   using C = Cfg<D>;
   using W = WideBars<D>;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  auto wait = [&](int i, uint32_t phase) {
+    return __all_sync(0xffffffffu, mbar_wait(bar(i), phase, abort_flag, err));
+  };
+  const bool leader = elect_one();
+  const int t = uniform(t_in);
+  const uint32_t tmem = uniform(tmem_in);
   Segment g;
   constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, D, true);
-  constexpr int kKSteps = D / 16;
-  const uint32_t qt = sQ + t * C::kTileBytes, ring_base = sRing;
+  const uint64_t qd = sw128_desc(sQ + t * C::kTileBytes, 16, 1024);
   const uint32_t s_col = s_column(tmem, t), o_col = o_column(tmem, t);
-  int c = 0, nq = 0, steps = 0, base = 0;
+  uint32_t c = 0, nq = 0, steps = 0;
+  int base = 0;
   bool ok = true;
   while (ok && walk.next(p, g)) {
-    const int nt = Walk::tiles(p, g, t);
-    const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
+    const int nt = uniform(Walk::tiles(p, g, t));
+    const int n_max = uniform(max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1)));
     // tile 1 has nothing to do: its issuer only gives Q back, and tile 0's
     // goes on without taking turns and releases each slot for both
-    const bool single = Walk::tiles(p, g, 1) == 0;
-    if (!mbar_wait(bar(W::kQFull), nq & 1, abort_flag, err)) break;
+    const bool single = uniform(Walk::tiles(p, g, 1)) == 0;
+    if (!wait(W::kQFull, nq & 1)) break;
     ++nq;
-    if (nt == 0) mma_commit(bar(W::kQEmpty));
+    if (nt == 0 && leader) mma_commit(bar(W::kQEmpty));
+    __syncwarp();
     if (single && t == 1) {
       c += 2 * n_max;
       continue;
     }
     for (int j = 0; ok && j <= n_max; ++j) {
-      const int cK = c + 2 * j, cV = c + 2 * j - 1;
-      const int sK = cK % C::kStages, sV = (cV + C::kStages) % C::kStages;
-      const int cV2 = cK + 1, sV2 = cV2 % C::kStages;
-      const uint32_t k_base = ring_base + sK * C::kTileBytes, v_base = ring_base + sV * C::kTileBytes;
+      const uint32_t cK = c + 2 * j, cV = c + 2 * j - 1;  // ring positions of K_j and V_{j-1}
+      const uint32_t sK = cK % C::kStages, sV = cV % C::kStages;
+      const uint32_t cV2 = cK + 1, sV2 = cV2 % C::kStages;
+      const uint64_t kd = sw128_desc(sRing + sK * C::kTileBytes, 16, 1024);
+      const uint64_t vd = sw128_desc(sRing + sV * C::kTileBytes, kColBlockBytes, 1024);
       const bool has_pv = j >= 1 && j - 1 < nt, has_s = j < nt, unused = !has_s && j < n_max;
-      if ((has_s || unused) && !mbar_wait(bar(W::kFull + sK), (cK / C::kStages) & 1, abort_flag, err)) {
+      if ((has_s || unused) && !wait(W::kFull + sK, (cK / C::kStages) & 1)) {
         ok = false;
         break;
       }
-      if (unused && !mbar_wait(bar(W::kFull + sV2), (cV2 / C::kStages) & 1, abort_flag, err)) {
+      if (unused && !wait(W::kFull + sV2, (cV2 / C::kStages) & 1)) {
         ok = false;
         break;
       }
-      if (has_pv && (!mbar_wait(bar(W::kFull + sV), (cV / C::kStages) & 1, abort_flag, err) ||
-                     !mbar_wait(bar(W::kPFull + t), (steps + j - 1) & 1, abort_flag, err))) {
+      if (has_pv && (!wait(W::kFull + sV, (cV / C::kStages) & 1) || !wait(W::kPFull + t, (steps + j - 1) & 1))) {
         ok = false;
         break;
       }
       const int turn_at = base + 2 * j + t;
-      if (!single && !wait_turn(turn, turn_at, abort_flag, err)) {
+      if (!single && !__all_sync(0xffffffffu, wait_turn(turn, turn_at, abort_flag, err))) {
         ok = false;
         break;
       }
       if (has_pv) {
         tc_fence_after();
-        const uint64_t vd = sw128_desc(v_base, kColBlockBytes, 1024);
+        const uint32_t add = j > 1 ? 1u : 0u;
+        if (leader) {
+          mma_ts(o_col, s_col, vd, idesc_o, add);
 #pragma unroll
-        for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
-          mma_ts(o_col, s_col + kk * 8, vd + static_cast<uint64_t>(kk * 128), idesc_o, (j > 1 || kk > 0) ? 1u : 0u);
+          for (int kk = 1; kk < kRowsPerTile / 16; ++kk)
+            mma_ts(o_col, s_col + kk * 8, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
+        }
+        __syncwarp();
       }
       if (has_s) {
-        const uint64_t qd = sw128_desc(qt, 16, 1024), kd = sw128_desc(k_base, 16, 1024);
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < kKSteps; ++kk) {
-          const uint64_t off = static_cast<uint64_t>(((kk / 4) * kColBlockBytes + (kk % 4) * 32) >> 4);
-          mma_ss(s_col, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk / 4) * kColBlockBytes + (kk % 4) * 32) >> 4);
+            mma_ss(s_col, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+          }
+        }
+        __syncwarp();
+      }
+      if (leader) {
+        if (!single) *turn = turn_at + 1;
+        if (has_s) mma_commit(bar(W::kSFull + t));
+        if (has_pv) {
+          if (j - 1 == nt - 1) mma_commit(bar(W::kOFull + t));
+          mma_commit(bar(W::kEmpty + sV));
+          if (single) mma_commit(bar(W::kEmpty + sV));
+        }
+        if (has_s) {
+          mma_commit(bar(W::kEmpty + sK));
+          if (single) mma_commit(bar(W::kEmpty + sK));
+          if (j == nt - 1) mma_commit(bar(W::kQEmpty));
+        }
+        if (unused) {
+          mma_commit(bar(W::kEmpty + sK));
+          mma_commit(bar(W::kEmpty + sV2));
         }
       }
-      if (!single) *turn = turn_at + 1;
-      if (has_s) mma_commit(bar(W::kSFull + t));
-      if (has_pv) {
-        if (j - 1 == nt - 1) mma_commit(bar(W::kOFull + t));
-        mma_commit(bar(W::kEmpty + sV));
-        if (single) mma_commit(bar(W::kEmpty + sV));
-      }
-      if (has_s) {
-        mma_commit(bar(W::kEmpty + sK));
-        if (single) mma_commit(bar(W::kEmpty + sK));
-        if (j == nt - 1) mma_commit(bar(W::kQEmpty));
-      }
-      if (unused) {
-        mma_commit(bar(W::kEmpty + sK));
-        mma_commit(bar(W::kEmpty + sV2));
-      }
+      __syncwarp();
     }
     c += 2 * n_max;
     steps += nt;
     if (!single) base += 2 * (n_max + 1);
   }
-  mma_commit(bar(W::kMmaDone));
-  mbar_drain(bar(W::kMmaDone), 0, err);
+  if (leader) {
+    mma_commit(bar(W::kMmaDone));
+    mbar_drain(bar(W::kMmaDone), 0, err);
+  }
+  __syncwarp();
 }
 
 // What a softmax warp knows of its walk, in shared memory: it has no registers to
@@ -888,8 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       narrow_producer<D>(p, sh, walk, &tm_q.narrow[sh.N == 16 ? 0 : (sh.N == 32 ? 1 : 2)], &tm_k, &tm_v, bar0, base,
                          first_entry, abort_flag, err);
     } else if (warp == kMmaWarp) {
-      if (lane == 0) narrow_issuer<D>(p, sh, walk, bar0, base, tmem, abort_flag, err);
-      __syncwarp();
+      narrow_issuer<D>(p, sh, walk, bar0, base, tmem, abort_flag, err);
     } else if (warp < 4 * sh.groups) {
       if (sh.N == 64)
         narrow_softmax<D, 32>(p, sh, walk, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 6 * 32, abort_flag, err);
@@ -901,8 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kTmaWarp) {
       wide_producer<D>(p, walk, &tm_q.wide, &tm_k, &tm_v, bar0, sQ, sRing, first_entry, abort_flag, err);
     } else if (warp == kMmaWarp || warp == kMmaWarp1) {
-      if (lane == 0) wide_issuer<D>(p, walk, warp == kMmaWarp ? 0 : 1, bar0, sQ, sRing, tmem, turn, abort_flag, err);
-      __syncwarp();
+      wide_issuer<D>(p, walk, warp == kMmaWarp ? 0 : 1, bar0, sQ, sRing, tmem, turn, abort_flag, err);
     } else {
       wide_softmax<D>(p, walk, warp >> 2, bar0, sRing, tmem, smem + 2 * C::kTileBytes + C::kStages * C::kTileBytes + warp * kWarpBytes,
                       abort_flag, err);

@@ -145,49 +145,59 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
   __syncwarp();
 }
 
-// MMA issuer: one thread.
+// MMA issuer: the whole warp, its code uniform, one lane for the products. (As the
+// code of a single thread it took about 95 clocks an MMA to bring the operands
+// into uniform registers, 1,520 to 1,800 a tile: more than the MMAs.)
 template <int D>
-__device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
-                                           uint32_t bar0, uint32_t smem, uint32_t tmem, volatile int *abort_flag,
-                                           int *err) {
+__device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk, uint32_t bar0,
+                                              uint32_t smem, uint32_t tmem_in, volatile int *abort_flag, int *err) {
   using C = Narrow<D>;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
-  const uint32_t idesc_s = idesc_narrow(sh.N, false), idesc_o = idesc_narrow(sh.N, true);
-  const uint32_t o_col = tmem + 2 * sh.N;
+  auto wait = [&](int i, uint32_t phase) {
+    return __all_sync(0xffffffffu, mbar_wait(bar(i), phase, abort_flag, err));
+  };
+  const bool leader = elect_one();
+  const uint32_t tmem = uniform(tmem_in), N = uniform(static_cast<uint32_t>(sh.N));
+  const int stages = uniform(sh.stages), q_bufs = N == 64 ? 1 : 2;
+  const uint32_t p_at = smem + stages * C::kTileBytes, p_step = N == 64 ? static_cast<uint32_t>(C::kPBytes) : 2 * N;
+  const uint32_t q_at = p_at + (N == 64 ? 2 : 1) * C::kPBytes, q_bytes = N * D * 2;
+  const uint32_t idesc_s = idesc_narrow(N, false), idesc_o = idesc_narrow(N, true);
+  const uint32_t o_col = tmem + 2 * N;
   RingPos k{0, 0};
   uint32_t step = 0;  // key tiles so far
   int nq = 0;
   bool ok = true;
   Segment g;
   while (ok && walk.next(p, g)) {
-    const int n = g.j1 - g.j0;
-    const int qb = nq % sh.q_bufs;
-    if (!mbar_wait(bar(C::kQFull + qb), (nq / sh.q_bufs) & 1, abort_flag, err)) break;
+    const int n = uniform(g.j1 - g.j0);
+    const int qb = nq & (q_bufs - 1);
+    if (!wait(C::kQFull + qb, (q_bufs == 2 ? nq >> 1 : nq) & 1)) break;
     ++nq;
-    const uint64_t qd = sw128_desc(smem + sh.q_at() + qb * sh.q_bytes(), 16, 1024);
-    const uint64_t q_block = static_cast<uint64_t>((sh.N * 128) >> 4);  // from one 64-column block to the next
+    const uint64_t qd = sw128_desc(q_at + qb * q_bytes, 16, 1024);
+    const uint64_t q_block = static_cast<uint64_t>((N * 128) >> 4);  // from one 64-column block to the next
     auto scores = [&](const RingPos &at, uint32_t to, bool last) {
       const uint64_t kd = sw128_desc(smem + at.slot * C::kTileBytes, 16, 1024);
-#pragma unroll 1
-      for (int cb = 0; cb < C::kColBlocks; ++cb)
+      const uint32_t s_col = tmem + (to & 1u) * N;
+      if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss(tmem + (to & 1u) * sh.N, kd + static_cast<uint64_t>((cb * kColBlockBytes + kk * 32) >> 4),
-                 qd + cb * q_block + static_cast<uint64_t>(kk * 2), idesc_s, cb + kk > 0 ? 1u : 0u);
-      mma_commit(bar(C::kSFull + (to & 1u)));
-      mma_commit(bar(C::kEmpty + at.slot));
-      if (last) mma_commit(bar(C::kQEmpty + qb));
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(s_col, kd + static_cast<uint64_t>(((kk / 4) * kColBlockBytes + (kk % 4) * 32) >> 4),
+                 qd + (kk / 4) * q_block + static_cast<uint64_t>((kk % 4) * 2), idesc_s, kk > 0 ? 1u : 0u);
+        mma_commit(bar(C::kSFull + (to & 1u)));
+        mma_commit(bar(C::kEmpty + at.slot));
+        if (last) mma_commit(bar(C::kQEmpty + qb));
+      }
+      __syncwarp();
     };
-    if (!mbar_wait(bar(C::kFull + k.slot), k.phase, abort_flag, err)) break;
+    if (!wait(C::kFull + k.slot, k.phase)) break;
     scores(k, step, n == 1);
     for (int j = 0; j < n; ++j, ++step) {
-      const RingPos v = k.next(sh.stages), k1 = v.next(sh.stages);
+      const RingPos v = k.next(stages), k1 = v.next(stages);
       // the next scores ahead of this product if their keys are there; their
       // buffer was read before P of the tile before this one was signalled
-      const bool early = j + 1 < n && mbar_test(bar(C::kFull + k1.slot), k1.phase);
+      const bool early = j + 1 < n && __all_sync(0xffffffffu, mbar_test(bar(C::kFull + k1.slot), k1.phase));
       if (early) scores(k1, step + 1, j + 2 == n);
-      if (!mbar_wait(bar(C::kPFull + (step & 1u)), (step >> 1) & 1u, abort_flag, err) ||
-          !mbar_wait(bar(C::kFull + v.slot), v.phase, abort_flag, err)) {
+      if (!wait(C::kPFull + (step & 1u), (step >> 1) & 1u) || !wait(C::kFull + v.slot, v.phase)) {
         ok = false;
         break;
       }
@@ -196,15 +206,19 @@ __device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Na
       // upper 64 rows of the product read the bytes behind the tile and are
       // never looked at (rows of a product do not mix)
       const uint64_t vd = sw128_desc(smem + v.slot * C::kTileBytes, kColBlockBytes, 1024);
-      const uint64_t pd = sw128_desc(smem + sh.p_buf(step & 1u), kColBlockBytes, 1024);
-#pragma unroll 4
-      for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
-        mma_ss(o_col, vd + static_cast<uint64_t>(kk * 128), pd + static_cast<uint64_t>(kk * 128), idesc_o,
-               (j > 0 || kk > 0) ? 1u : 0u);
-      mma_commit(bar(C::kEmpty + v.slot));
-      mma_commit(bar(C::kPvDone + (step & 1u)));
+      const uint64_t pd = sw128_desc(p_at + (step & 1u) * p_step, kColBlockBytes, 1024);
+      const uint32_t add = j > 0 ? 1u : 0u;
+      if (leader) {
+        mma_ss(o_col, vd, pd, idesc_o, add);
+#pragma unroll
+        for (int kk = 1; kk < kRowsPerTile / 16; ++kk)
+          mma_ss(o_col, vd + static_cast<uint64_t>(kk * 128), pd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
+        mma_commit(bar(C::kEmpty + v.slot));
+        mma_commit(bar(C::kPvDone + (step & 1u)));
+      }
+      __syncwarp();
       if (j + 1 < n && !early) {
-        if (!mbar_wait(bar(C::kFull + k1.slot), k1.phase, abort_flag, err)) {
+        if (!wait(C::kFull + k1.slot, k1.phase)) {
           ok = false;
           break;
         }
@@ -213,8 +227,11 @@ __device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Na
       k = k1;
     }
   }
-  mma_commit(bar(C::kMmaDone));
-  mbar_drain(bar(C::kMmaDone), 0, err);
+  if (leader) {
+    mma_commit(bar(C::kMmaDone));
+    mbar_drain(bar(C::kMmaDone), 0, err);
+  }
+  __syncwarp();
 }
 
 // Reduces 16 values over the 32 lanes of a warp at once, halving the values with
