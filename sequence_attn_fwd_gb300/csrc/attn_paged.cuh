@@ -275,14 +275,44 @@ struct Walk {
   }
 };
 
-// The table entry of lane `lane` for key tile j of a sequence with kv_len keys:
-// one entry per page of the tile, -1 past them and past the sequence.
-__device__ __forceinline__ int page_entry(const PagedAttnParams &p, const int *row, int kv_len, int j, int lane) {
-  const bool small = p.page_log2 < 7;
-  if (lane >= (small ? kRowsPerTile >> p.page_log2 : 1)) return -1;
-  const int i = small ? j * (kRowsPerTile >> p.page_log2) + lane : (j * kRowsPerTile) >> p.page_log2;
-  return (i << p.page_log2) < kv_len ? row[i] : -1;
+// Pages of a key tile: 128 / page_size, or one larger page.
+__device__ __forceinline__ int pages_of_tile(const PagedAttnParams &p) {
+  return p.page_log2 < 7 ? kRowsPerTile >> p.page_log2 : 1;
 }
+// Index in the table row of the first page of key tile j.
+__device__ __forceinline__ int first_page(const PagedAttnParams &p, int j) { return (j * kRowsPerTile) >> p.page_log2; }
+// A lane's entry of the 32 from index `from` on, -1 past the sequence's pages.
+__device__ __forceinline__ int window_entry(const PagedAttnParams &p, const int *row, int kv_len, int from) {
+  const int i = from + static_cast<int>(threadIdx.x & 31);
+  return i <= (kv_len - 1) >> p.page_log2 ? row[i] : -1;
+}
+
+// The producer's view of a segment's pages: 32 entries of the table, one a lane,
+// and the 32 after them on their way, so that no load's latency is between two
+// tiles (it was: 1,300 clocks a tile with pages of 32 keys).
+struct PageWindow {
+  const int *row;
+  int kv_len, from, now, ahead;
+  __device__ __forceinline__ PageWindow(const PagedAttnParams &p, const Segment &g, bool have_first, int first)
+      : row(page_row(p, g)), kv_len(g.s.kv_len), from(first_page(p, g.j0)) {
+    now = have_first ? first : window_entry(p, row, kv_len, from);
+    ahead = window_entry(p, row, kv_len, from + 32);
+  }
+  // This lane's page of key tile j (lanes below pages_of_tile): n_pages, which
+  // reads as zeros, where there is none. Tiles in ascending order.
+  __device__ __forceinline__ int page(const PagedAttnParams &p, int j) {
+    const int boxes = pages_of_tile(p), lane = threadIdx.x & 31;
+    int off = first_page(p, j) - from;
+    if (off >= 32) {  // (a tile's pages are never in two windows)
+      from += 32;
+      off -= 32;
+      now = ahead;
+      ahead = window_entry(p, row, kv_len, from + 32);
+    }
+    const int e = __shfl_sync(0xffffffffu, now, off + (lane < boxes ? lane : 0));
+    return e >= 0 && e < p.cache.n_pages ? e : p.cache.n_pages;
+  }
+};
 
 // Whether a page of a segment's key tiles is missing, found by a warp at the
 // segment's start, so that the tiles of a whole sequence look nothing up.
@@ -383,7 +413,7 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
   const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
   const int page_size = 1 << p.page_log2;
   const bool small = page_size < kRowsPerTile;
-  const int boxes = small ? kRowsPerTile >> p.page_log2 : 1;  // pages of a key tile
+  const int boxes = pages_of_tile(p);
   const uint32_t box_bytes = (small ? page_size : kRowsPerTile) * 128u;
   int c = 0, nq = 0;
   bool ok = true;
@@ -394,10 +424,7 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
       cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, walk.last_cta(p, g));
     const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
     const bool two = Walk::tiles(p, g, 1) > 0;
-    const int *row = page_row(p, g);
-    // the page of this lane for key tile j: n_pages (read as zeros) where there is none
-    auto page_of = [&](int entry) -> int { return entry >= 0 && entry < p.cache.n_pages ? entry : p.cache.n_pages; };
-    int page = page_of(nq == 0 ? first_entry : page_entry(p, row, g.s.kv_len, g.j0, lane));
+    PageWindow pages(p, g, nq == 0, first_entry);
     if (lane == 0) {
       ok = nq == 0 || mbar_wait(bar(W::kQEmpty), (nq - 1) & 1, abort_flag, err);
       if (ok) {
@@ -413,8 +440,7 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
     if (!ok) break;
     ++nq;
     for (int j = 0; j < n_max && ok; ++j) {
-      const int now = page;
-      if (j + 1 < n_max) page = page_of(page_entry(p, row, g.s.kv_len, g.j0 + j + 1, lane));
+      const int page = pages.page(p, g.j0 + j);
       const int in_page = small ? 0 : ((g.j0 + j) * kRowsPerTile) & (page_size - 1);
       for (int which = 0; which < 2; ++which, ++c) {
         const int slot = c % C::kStages;
@@ -429,7 +455,7 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
 #pragma unroll
           for (int cb = 0; cb < C::kColBlocks; ++cb)
             tma_load_4d_hint(sRing + (slot * C::kColBlocks + cb) * kColBlockBytes + lane * box_bytes, map,
-                             bar(W::kFull + slot), cb * 64, in_page, g.h, now, pol_kv);
+                             bar(W::kFull + slot), cb * 64, in_page, g.h, page, pol_kv);
         }
         __syncwarp();
       }
@@ -843,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool narrow = most * p.G <= 64;
   const L sh(most * p.G, p.G);
   const Walk walk(prefix[p.cache.B], first, gridDim.x);
-  int first_entry = -1;  // the producer's lanes: the first key tile's pages
+  int first_entry = -1;  // the producer's lanes: the first pages
   if (warp == kTmaWarp && walk.pos < walk.end) {
     Segment g;
     const Place at = place_of(p, prefix, walk.pos, g.s);
@@ -851,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     g.h = at.h;
     g.rbs = row_blocks(p, g.s);
     walk.make(p, at.rb, at.r, g);
-    first_entry = page_entry(p, page_row(p, g), g.s.kv_len, g.j0, lane);
+    first_entry = window_entry(p, page_row(p, g), g.s.kv_len, first_page(p, g.j0));
     if (lane == 0) *first = g;
   }
   if (threadIdx.x == 0) {

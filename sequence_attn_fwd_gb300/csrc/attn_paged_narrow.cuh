@@ -80,7 +80,7 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
   const uint64_t pol_q = l2_policy_evict_last(), pol_kv = l2_policy_evict_first();
   const int page_size = 1 << p.page_log2;
   const bool small = page_size < kRowsPerTile;
-  const int boxes = small ? kRowsPerTile >> p.page_log2 : 1;
+  const int boxes = pages_of_tile(p);
   const uint32_t box_bytes = (small ? page_size : kRowsPerTile) * 128u;
   const uint32_t q_bytes = static_cast<uint32_t>(sh.tok * p.G) * 128u * C::kColBlocks;
   RingPos at{0, 0};
@@ -92,12 +92,10 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
   while (ok && walk.next(p, g)) {
     if (g.j0 == 0 && g.slot >= 0) cut = make_int4(g.s.q0, g.s.q_len * p.G, g.h, walk.last_cta(p, g));
     const int n = g.j1 - g.j0;
-    const int *row = page_row(p, g);
-    // n_pages (read as zeros) where there is none
-    auto page_of = [&](int entry) -> int { return entry >= 0 && entry < p.cache.n_pages ? entry : p.cache.n_pages; };
+    PageWindow pages(p, g, nq == 0, first_entry);
     const int qb = nq % sh.q_bufs, use = nq / sh.q_bufs;
     bool q_due = true;  // this segment's Q is still to be loaded
-    int page = page_of(nq == 0 ? first_entry : page_entry(p, row, g.s.kv_len, g.j0, lane));
+    int page = 0;
     for (int f = 0; f < 2 * n && ok; ++f, ++fills) {
       // Q as soon as its buffer is free, but K and V go ahead of it meanwhile:
       // the slots of the first fills are given back by earlier segments
@@ -114,7 +112,7 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
         q_due = false;
       }
       const int j = g.j0 + (f >> 1), which = f & 1;
-      const int now = page;
+      if (!which) page = pages.page(p, j);
       if (lane == 0 && ok) {
         ok = fills < sh.stages || mbar_wait(bar(C::kEmpty + at.slot), at.phase ^ 1u, abort_flag, err);
         if (ok) mbar_arrive_expect_tx(bar(C::kFull + at.slot), C::kTileBytes);
@@ -127,9 +125,8 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
 #pragma unroll
         for (int cb = 0; cb < C::kColBlocks; ++cb)
           tma_load_4d_hint(smem + at.slot * C::kTileBytes + cb * kColBlockBytes + lane * box_bytes, map,
-                           bar(C::kFull + at.slot), cb * 64, in_page, g.h, now, pol_kv);
+                           bar(C::kFull + at.slot), cb * 64, in_page, g.h, page, pol_kv);
       }
-      if (which && f + 1 < 2 * n) page = page_of(page_entry(p, row, g.s.kv_len, j + 1, lane));
       at = at.next(sh.stages);
     }
     ++nq;
