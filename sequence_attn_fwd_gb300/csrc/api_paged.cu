@@ -36,7 +36,7 @@ int check_cache(const paged_cache *c) {
   if (c->table_stride < c->max_pages) return ATTN_ERR_INVALID_ARG;
   if (c->B == 0) return ATTN_OK;
   if (!c->k_pages || !c->v_pages || !aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return ATTN_ERR_INVALID_ARG;
-  if (!c->page_table || !c->kv_lens || !c->cu_seqlens || !aligned(c->page_table, 4) || !aligned(c->kv_lens, 4) ||
+  if ((!c->page_table && c->max_pages > 0) || !c->kv_lens || !c->cu_seqlens || !aligned(c->page_table, 4) || !aligned(c->kv_lens, 4) ||
       !aligned(c->cu_seqlens, 4))
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;

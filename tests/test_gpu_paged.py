@@ -181,6 +181,120 @@ def test_captured_call_follows_lengths_and_tables(sa):
         ref.check_attention((out, lse), ref.attention(q, kp, vp, table, lens, cu, True, 1 / math.sqrt(128)))
 
 
+def test_rows_behind_the_sequences_may_hold_anything(sa):
+    """NaN and inf in query rows of no sequence reach no other row, in either form of the kernel."""
+    for new, kv in (([1, 2], [300, 40]), ([70, 1], [300, 140])):
+        kp, vp, table, lens, cu = make_cache(new, kv, 2, 128, 16, 15)
+        q = torch.randn((8, sum(new) + 9, 128)).to(BF).cuda()
+        q[:, sum(new):sum(new) + 4], q[:, sum(new) + 4:] = math.nan, math.inf
+        out = torch.full_like(q, 7.0)
+        got = sa.attn_paged(q, kp, vp, table, lens, cu, out=out)
+        ref.check_attention(got, ref.attention(q, kp, vp, table, lens, cu, True, 1 / math.sqrt(128)))
+        assert (out[:, sum(new):] == 7).all()
+
+
+def test_no_pages_no_lse_and_a_table_without_columns(sa):
+    kp, vp, table, lens, cu = make_cache([3, 1], [50, 20], 2, 64, 16, 16)
+    q = torch.randn((4, 4, 64)).to(BF).cuda()
+    none = torch.zeros((2, 0), dtype=I32, device="cuda")
+    o, lse = sa.attn_paged(q, kp, vp, none, lens, cu)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    o, lse = sa.attn_paged(q, kp, vp, torch.full_like(table, -1), lens, cu)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    # the C call without lse gives the same O
+    import ctypes
+
+    from sequence_attn_fwd_gb300 import paged
+
+    want = sa.attn_paged(q, kp, vp, table, lens, cu)[0]
+    out, ws = torch.empty_like(q), torch.empty(sa.attn_paged_workspace_bytes(4, 2, 4, 64), dtype=torch.uint8, device="cuda")
+    view = paged._cache_view(kp, vp, table, lens, cu)[0]
+    assert sa.lib.attn_paged(q.data_ptr(), q.stride(0), q.stride(1), view, out.data_ptr(), q.stride(0), q.stride(1), None,
+                             ws.data_ptr(), ws.numel(), 4, 4, 1, ctypes.c_float(1 / 8),
+                             torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(out, want)
+
+
+def test_most_sequences_of_a_call(sa):
+    B = 4096
+    new = [1 if b % 3 else 0 for b in range(B)]
+    kv = [n + b % 23 for b, n in enumerate(new)]
+    run_case(sa, new, kv, 2, 2, 64, 16, True, seed=17)
+    with pytest.raises(sa.AttnError):
+        run_case(sa, new + [1], kv + [1], 2, 2, 64, 16, True, seed=17)
+
+
+@pytest.mark.parametrize("new,kv", [([4] * 40, [257] * 40), ([8, 1, 8], [5000, 4000, 640]), ([64] * 3, [64, 200, 900]),
+                                    ([2, 65], [700, 1300]), ([129, 128, 127], [140, 128, 1000])])
+@pytest.mark.parametrize("G", [1, 7, 8])
+def test_row_counts_around_the_tiles(sa, new, kv, G):
+    """Rows per KV head below, at and above 16, 32, 64 and the tiles of 128; items that ranges cut anywhere."""
+    run_case(sa, new, kv, 2 * G, 2, 128, 32, True, seed=G)
+    run_case(sa, new, kv, 2 * G, 2, 64, 16, False, seed=G)
+
+
+def test_offsets_past_32_bits(sa):
+    """Pools of more than 2^32 elements: append, attend, fork and copy at their far end."""
+    Hkv, ps, D, n_pages = 8, 128, 128, 33100
+    assert n_pages * Hkv * ps * D > 2 ** 32
+    kp = torch.empty((n_pages, Hkv, ps, D), dtype=BF, device="cuda")
+    vp = torch.empty_like(kp)
+    pages = [n_pages - 1, 5, n_pages - 3]
+    table = i32([pages + [-1], [-1] * 4])
+    refs = torch.ones(n_pages, dtype=I32, device="cuda")
+    refs[[n_pages - 2, 17]] = 0
+    n = 300
+    lens, cu = i32([n, 0]), i32([0, n, n])
+    g = torch.Generator().manual_seed(3)
+    k, v, q = (torch.randn((n, H, D), generator=g).to(BF).cuda().transpose(0, 1) for H in (Hkv, Hkv, 8))
+    sa.paged_append(k, v, kp, vp, table, lens, cu)
+    for i, p in enumerate(pages):
+        rows = min(ps, n - i * ps)
+        assert torch.equal(kp[p, :, :rows], k[:, i * ps:i * ps + rows]) and torch.equal(vp[p, :, :rows], v[:, i * ps:i * ps + rows])
+    dense_k, dense_v = k.contiguous()[None], v.contiguous()[None]
+    got = sa.attn_paged(q, kp, vp, table, lens, cu)
+    want = ref.attention(q, dense_k, dense_v, torch.zeros((1, 1), dtype=I32), torch.tensor([n]), torch.tensor([0, n]), True,
+                         1 / math.sqrt(D))
+    ref.check_attention(got, want)
+    assert sa.paged_fork((kp, vp), table, lens, refs, [0], [1]).tolist() == [0]
+    assert table[1].tolist() == [n_pages - 1, 5, 17, -1] and torch.equal(kp[17, :, :n - 256], kp[n_pages - 3, :, :n - 256])
+    sa.paged_copy((kp, vp), [n_pages - 1], [n_pages - 2])
+    assert torch.equal(vp[n_pages - 2], vp[n_pages - 1])
+
+
+def test_after_a_timeout_the_rows_come_out_empty_until_it_is_reported(sa):
+    kp, vp, table, lens, cu = make_cache([1, 3], [900, 77], 2, 128, 16, 18)
+    q = torch.randn((4, 4, 128)).to(BF).cuda()
+    want = sa.attn_paged(q, kp, vp, table, lens, cu)
+    assert sa.lib.attn_debug_expire_wait(1000, torch.cuda.current_stream().cuda_stream) == 0
+    o, lse = sa.attn_paged(q, kp, vp, table, lens, cu)
+    with pytest.raises(sa.AttnError):
+        sa.query_device_error()
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    again = sa.attn_paged(q, kp, vp, table, lens, cu)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def test_two_captured_calls_that_share_a_workspace_in_order(sa):
+    """Two graphs with one workspace, replayed one after the other on one stream."""
+    kp, vp, table, lens, cu = make_cache([1, 1], [2000, 900], 2, 128, 16, 19, garbage=False)
+    qs = [torch.randn((8, 2, 128)).to(BF).cuda() for _ in range(2)]
+    ws = torch.empty(sa.attn_paged_workspace_bytes(8, 2, 2, 128), dtype=torch.uint8, device="cuda")
+    want = [sa.attn_paged(q, kp, vp, table, lens, cu) for q in qs]
+    graphs, outs = [], []
+    for q in qs:
+        outs.append((torch.empty_like(q), torch.empty((8, 2), device="cuda")))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            sa.attn_paged(q, kp, vp, table, lens, cu, out=outs[-1][0], lse=outs[-1][1], workspace=ws)
+    for _ in range(5):
+        for gr in graphs:
+            gr.replay()
+    torch.cuda.synchronize()
+    for (o, lse), (wo, wl) in zip(outs, want):
+        assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
 # ---------------------------------------------------------------------------- rotary positions
 ROPE = [(1, 1, 0, 1, 64), (2, 3, 1, 17, 64), (1, 4, 2, 131, 128), (3, 28, 4, 5, 128), (1, 2, 1, 3001, 64)]
 
@@ -258,6 +372,33 @@ def test_rope_captured_backward_while_eager_results_live(sa):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, eager)
+
+
+def test_rope_of_more_than_32_bits_of_elements(sa):
+    D, H, S = 128, 34, 500_000
+    assert H * S * D > 2 ** 31
+    plan = sa.RopePlan(D, (64,))
+    x = torch.empty((1, H, S, D), dtype=BF, device="cuda").normal_()
+    pos = torch.arange(S, dtype=I32, device="cuda").view(1, 1, S)
+    y, _ = sa.rope_axes(x, None, pos, *plan)
+    for rows in (slice(0, 3), slice(S - 40, S)):
+        for h in (0, H - 1):
+            ref.within(y[:, h:h + 1, rows], *ref.rotate(x[:, h:h + 1, rows], pos[:, :, rows], *plan, False))
+
+
+def test_rope_rows_with_strides(sa):
+    """A slice of a fused projection in, a slice of another tensor out; the rest of it untouched."""
+    B, S, H, D = 2, 37, 3, 64
+    fused = torch.randn((B, S, 5 * H, D)).to(BF).cuda()
+    x = fused[:, :, H:2 * H].transpose(1, 2)
+    out = torch.full((B, H + 2, S + 3, D), 7.0, dtype=BF, device="cuda")
+    pos = torch.arange(S, dtype=I32, device="cuda").view(1, 1, S).expand(2, B, S)
+    plan = sa.RopePlan(D, (16, 16), shared=False)
+    y, _ = sa.rope_axes(x, None, pos, *plan, interleaved=True, out_q=out[:, 1:1 + H, 2:2 + S])
+    ref.within(y, *ref.rotate(x, pos, *plan, True))
+    assert (out[:, 0] == 7).all() and (out[:, H + 1] == 7).all() and (out[:, :, :2] == 7).all() and (out[:, :, S + 2] == 7).all()
+    with pytest.raises(ValueError, match="expanded"):
+        sa.rope_axes(x, None, pos, *plan, out_q=out[:, :1, 2:2 + S].expand(B, H, S, D))
 
 
 # ---------------------------------------------------------------------------- appends
