@@ -36,8 +36,8 @@ int check_cache(const paged_cache *c) {
   if (c->table_stride < c->max_pages) return ATTN_ERR_INVALID_ARG;
   if (c->B == 0) return ATTN_OK;
   if (!c->k_pages || !c->v_pages || !aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return ATTN_ERR_INVALID_ARG;
-  if ((!c->page_table && c->max_pages > 0) || !c->kv_lens || !c->cu_seqlens || !aligned(c->page_table, 4) || !aligned(c->kv_lens, 4) ||
-      !aligned(c->cu_seqlens, 4))
+  if ((!c->page_table && c->max_pages > 0) || !c->kv_lens || !c->cu_seqlens || !aligned(c->page_table, 4) ||
+      !aligned(c->kv_lens, 4) || !aligned(c->cu_seqlens, 4))
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -173,10 +173,9 @@ int attn_paged(const void *q, long long q_head_stride, long long q_row_stride, c
   if (cache->B == 0 || total_q == 0) return ATTN_OK;
   if (!q || !o || !workspace || !aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 16) || !aligned(lse, 4))
     return ATTN_ERR_INVALID_ARG;
-  if (q_head_stride % 8 || q_row_stride % 8 || o_head_stride % 8 || o_row_stride % 8) return ATTN_ERR_INVALID_ARG;
-  // no stride of a dimension longer than one may make rows overlap
-  if ((Hq > 1 && (q_head_stride < D || o_head_stride < D)) || (total_q > 1 && (q_row_stride < D || o_row_stride < D)))
-    return ATTN_ERR_INVALID_ARG;
+  // strides of dimensions of one are not looked at; no other may make rows overlap
+  if (Hq > 1 && (q_head_stride % 8 || o_head_stride % 8 || q_head_stride < D || o_head_stride < D)) return ATTN_ERR_INVALID_ARG;
+  if (total_q > 1 && (q_row_stride % 8 || o_row_stride % 8 || q_row_stride < D || o_row_stride < D)) return ATTN_ERR_INVALID_ARG;
   const Workspace ws = workspace_of(G, total_q, D);
   if (workspace_bytes < ws.total) return ATTN_ERR_INVALID_ARG;
 

@@ -182,7 +182,8 @@ __device__ __forceinline__ Place place_of(const PagedAttnParams &p, const int *p
   const int b = seq_of(prefix, p.cache.B, pos);
   s = sequence(p, b);
   const int per_head = max(1, (prefix[b + 1] - prefix[b]) / p.cache.Hkv);
-  const int off = pos - prefix[b], h = off / per_head;
+  // (the bounds matter only if cu_seqlens decreases, when costs need not fit 32 bits)
+  const int off = max(0, pos - prefix[b]), h = min(off / per_head, p.cache.Hkv - 1);
   int rest = off - h * per_head, rb = 0;
   const int rbs = row_blocks(p, s);
   for (; rb < rbs; ++rb) {
@@ -265,7 +266,7 @@ struct Walk {
   }
   // The last CTA of an item that this one begins with segment g.
   __device__ __forceinline__ int last_cta(const PagedAttnParams &p, const Segment &g) const {
-    return (g.next - (g.j1 + kItemCost) + item_tiles(p, g.s, g.rb) + kItemCost - 1) / per;
+    return min((g.next - (g.j1 + kItemCost) + item_tiles(p, g.s, g.rb) + kItemCost - 1) / per, static_cast<int>(gridDim.x) - 1);
   }
   // Key tiles of segment g that query tile t goes through, counted from g.j0.
   static __device__ __forceinline__ int tiles(const PagedAttnParams &p, const Segment &g, int t) {
@@ -739,8 +740,9 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
     }
     if (!ok || (n > 0 && !have_o)) return;  // (a warp that gives up makes the others give up too)
     if (!warp_valid) continue;
-    const float inv_l = l > 0.f ? 1.f / l : 0.f;
-    const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    // (not l > 0: the NaN of a row with a NaN score must not look like a row without keys)
+    const float inv_l = l != 0.f ? 1.f / l : 0.f;
+    const float lse = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     const unsigned valid = __ballot_sync(0xffffffffu, row_valid);
     // Rows leave through shared memory, 64 bytes of each at a time, so that a
     // store instruction writes 64 bytes of eight rows (each lane its own row, 16
@@ -988,14 +990,14 @@ __device__ __forceinline__ void merged_row(const PagedAttnParams &p, const int4 
                                            float m, float sum) {
   constexpr int kCols = D / 32;
   const int lane = threadIdx.x & 31;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   const int head = cut.z * p.G + r % p.G, row = cut.x + r / p.G;
   __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + head * p.o_h + row * p.o_s +
                                                            lane * kCols);
 #pragma unroll
   for (int i = 0; i < kCols / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
   if (lane == 0 && p.lse)
-    p.lse[static_cast<size_t>(head) * p.total_q + row] = sum > 0.f ? m + logf(sum) : -INFINITY;
+    p.lse[static_cast<size_t>(head) * p.total_q + row] = sum != 0.f ? m + logf(sum) : -INFINITY;
 }
 
 // Rows of a cut item with at most kParts partials: a warp takes kRows of them and

@@ -248,9 +248,9 @@ __device__ __forceinline__ float reduce16(float (&v)[16], Op op) {
   return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-// The reference of a column that has seen no key: any score passes it, and
-// 2^(-inf - it) is still 0.
-constexpr float kNoReference = -1e30f;
+// The reference of a column that has seen no key, the lowest finite number: any
+// score passes it, and 2^(-inf - it) is still 0.
+constexpr float kNoReference = -3.402823466e38f;
 
 // Softmax and epilogue of columns [col0, col0 + C) of S^T: one thread per key
 // (and, in the epilogue, per column of O). `red` is this warpgroup's 6 x C
@@ -425,9 +425,9 @@ __device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const N
     const size_t part = static_cast<size_t>(max(g.slot, 0)) * p.part_rows + col0;
     if (key < C) {
       const float sum = (red[key] + red[C + key]) + (red[2 * C + key] + red[3 * C + key]);
-      factor[key] = sum > 0.f ? 1.f / sum : 0.f;
+      factor[key] = sum != 0.f ? 1.f / sum : 0.f;
       if (col0 + key < rows) {
-        const float lse = sum > 0.f ? (ref[key] + log2f(sum)) * kLn2 : -INFINITY;
+        const float lse = sum != 0.f ? (ref[key] + log2f(sum)) * kLn2 : -INFINITY;
         const int tok = (col0 + key) / p.G, head = g.h * p.G + (col0 + key) - tok * p.G;
         if (g.slot >= 0) p.part_lse[part + key] = lse;
         else if (p.lse) p.lse[static_cast<size_t>(head) * p.total_q + g.s.q0 + tok] = lse;

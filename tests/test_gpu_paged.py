@@ -193,6 +193,30 @@ def test_rows_behind_the_sequences_may_hold_anything(sa):
         assert (out[:, sum(new):] == 7).all()
 
 
+@pytest.mark.parametrize("new", [[1, 3, 1], [80, 3, 1]])
+def test_a_nan_query_stays_nan(sa, new):
+    """A row with a NaN score is NaN with a NaN lse, also when its keys were split; no other row is."""
+    kp, vp, table, lens, cu = make_cache(new, [5000, 40, 20], 2, 128, 16, 20)
+    q = torch.randn((2, sum(new), 128)).to(BF).cuda()
+    bad = q.clone()
+    bad[1, 0, 5] = math.nan
+    want = sa.attn_paged(q, kp, vp, table, lens, cu)
+    o, lse = sa.attn_paged(bad, kp, vp, table, lens, cu)
+    assert o[1, 0].isnan().all() and lse[1, 0].isnan()
+    want[0][1, 0], want[1][1, 0] = o[1, 0], lse[1, 0]
+    assert torch.equal(o.nan_to_num(), want[0].nan_to_num()) and torch.equal(lse.nan_to_num(), want[1].nan_to_num())
+
+
+def test_strides_of_dimensions_of_one_are_free(sa):
+    kp, vp, table, lens, cu = make_cache([1], [77], 2, 64, 16, 22)
+    q = torch.randn((4, 1, 64)).to(BF).cuda()
+    want = sa.attn_paged(q, kp, vp, table, lens, cu)
+    odd = q.as_strided((4, 1, 64), (64, 3, 1))
+    out = torch.empty_like(q).as_strided((4, 1, 64), (64, 5, 1))
+    got = sa.attn_paged(odd, kp, vp, table, lens, cu, out=out)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_no_pages_no_lse_and_a_table_without_columns(sa):
     kp, vp, table, lens, cu = make_cache([3, 1], [50, 20], 2, 64, 16, 16)
     q = torch.randn((4, 4, 64)).to(BF).cuda()
