@@ -315,6 +315,34 @@ struct PageWindow {
   }
 };
 
+// The boxes of a key tile, lane i's page the i-th: issued by one lane, in code that
+// is uniform for the warp. (One lane a page took about 110 clocks a box: the
+// lanes follow each other, each with its operands on the way to uniform
+// registers.)
+template <int D, int kBoxes>
+__device__ __forceinline__ void load_boxes(uint32_t dst, const CUtensorMap *map, uint32_t bar, int in_page, int head,
+                                           int page, uint32_t box_bytes, bool leader, uint64_t pol) {
+  int pg[kBoxes];
+#pragma unroll
+  for (int i = 0; i < kBoxes; ++i) pg[i] = uniform(__shfl_sync(0xffffffffu, page, i));
+  if (leader) {
+#pragma unroll
+    for (int i = 0; i < kBoxes; ++i)
+#pragma unroll
+      for (int cb = 0; cb < D / 64; ++cb)
+        tma_load_4d_hint(dst + cb * kColBlockBytes + i * box_bytes, map, bar, cb * 64, in_page, head, pg[i], pol);
+  }
+  __syncwarp();
+}
+template <int D>
+__device__ __forceinline__ void load_pages(uint32_t dst, const CUtensorMap *map, uint32_t bar, int in_page, int head,
+                                           int page, int boxes, uint32_t box_bytes, bool leader, uint64_t pol) {
+  if (boxes == 1) load_boxes<D, 1>(dst, map, bar, in_page, head, page, box_bytes, leader, pol);
+  else if (boxes == 2) load_boxes<D, 2>(dst, map, bar, in_page, head, page, box_bytes, leader, pol);
+  else if (boxes == 4) load_boxes<D, 4>(dst, map, bar, in_page, head, page, box_bytes, leader, pol);
+  else load_boxes<D, 8>(dst, map, bar, in_page, head, page, box_bytes, leader, pol);
+}
+
 // Whether a page of a segment's key tiles is missing, found by a warp at the
 // segment's start, so that the tiles of a whole sequence look nothing up.
 __device__ __forceinline__ bool pages_missing(const PagedAttnParams &p, const Segment &g) {
@@ -414,8 +442,12 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
   const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
   const int page_size = 1 << p.page_log2;
   const bool small = page_size < kRowsPerTile;
-  const int boxes = pages_of_tile(p);
-  const uint32_t box_bytes = (small ? page_size : kRowsPerTile) * 128u;
+  const int boxes = uniform(pages_of_tile(p));
+  const uint32_t box_bytes = uniform((small ? page_size : kRowsPerTile) * 128u);
+  const bool leader = elect_one();
+  auto wait = [&](int i, uint32_t phase) {
+    return __all_sync(0xffffffffu, mbar_wait(bar(i), phase, abort_flag, err));
+  };
   int c = 0, nq = 0;
   bool ok = true;
   // the item that this CTA begins and another one ends, for the merge
@@ -423,42 +455,32 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
   while (ok && walk.next(p, g)) {
     if (g.j0 == 0 && g.slot >= 0)
       cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, walk.last_cta(p, g));
-    const int n_max = max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1));
+    const int n_max = uniform(max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1)));
+    const int j0 = uniform(g.j0), head = uniform(g.h);
     const bool two = Walk::tiles(p, g, 1) > 0;
     PageWindow pages(p, g, nq == 0, first_entry);
-    if (lane == 0) {
-      ok = nq == 0 || mbar_wait(bar(W::kQEmpty), (nq - 1) & 1, abort_flag, err);
-      if (ok) {
-        const uint32_t q_bytes = static_cast<uint32_t>(p.tok * p.G) * 128u * C::kColBlocks;
-        mbar_arrive_expect_tx(bar(W::kQFull), two ? 2 * q_bytes : q_bytes);
-        for (int t = 0; t < (two ? 2 : 1); ++t)
-          for (int cb = 0; cb < C::kColBlocks; ++cb)
-            tma_load_4d_hint(sQ + (t * C::kColBlocks + cb) * kColBlockBytes, tm_q, bar(W::kQFull), cb * 64, 0,
-                             g.s.q0 + (2 * g.rb + t) * p.tok, g.h, pol_q);
-      }
-    }
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    ok = nq == 0 || wait(W::kQEmpty, (nq - 1) & 1);
     if (!ok) break;
+    if (leader) {
+      const uint32_t q_bytes = static_cast<uint32_t>(p.tok * p.G) * 128u * C::kColBlocks;
+      mbar_arrive_expect_tx(bar(W::kQFull), two ? 2 * q_bytes : q_bytes);
+      for (int t = 0; t < (two ? 2 : 1); ++t)
+        for (int cb = 0; cb < C::kColBlocks; ++cb)
+          tma_load_4d_hint(sQ + (t * C::kColBlocks + cb) * kColBlockBytes, tm_q, bar(W::kQFull), cb * 64, 0,
+                           g.s.q0 + (2 * g.rb + t) * p.tok, head, pol_q);
+    }
+    __syncwarp();
     ++nq;
     for (int j = 0; j < n_max && ok; ++j) {
-      const int page = pages.page(p, g.j0 + j);
-      const int in_page = small ? 0 : ((g.j0 + j) * kRowsPerTile) & (page_size - 1);
+      const int page = pages.page(p, j0 + j);
+      const int in_page = small ? 0 : ((j0 + j) * kRowsPerTile) & (page_size - 1);
       for (int which = 0; which < 2; ++which, ++c) {
         const int slot = c % C::kStages;
-        if (lane == 0) {
-          ok = c < C::kStages || mbar_wait(bar(W::kEmpty + slot), ((c / C::kStages) - 1) & 1, abort_flag, err);
-          if (ok) mbar_arrive_expect_tx(bar(W::kFull + slot), C::kTileBytes);
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        ok = c < C::kStages || wait(W::kEmpty + slot, ((c / C::kStages) - 1) & 1);
         if (!ok) break;
-        if (lane < boxes) {
-          const CUtensorMap *map = which ? tm_v : tm_k;
-#pragma unroll
-          for (int cb = 0; cb < C::kColBlocks; ++cb)
-            tma_load_4d_hint(sRing + (slot * C::kColBlocks + cb) * kColBlockBytes + lane * box_bytes, map,
-                             bar(W::kFull + slot), cb * 64, in_page, g.h, page, pol_kv);
-        }
-        __syncwarp();
+        if (leader) mbar_arrive_expect_tx(bar(W::kFull + slot), C::kTileBytes);
+        load_pages<D>(sRing + slot * C::kTileBytes, which ? tm_v : tm_k, bar(W::kFull + slot), in_page, head, page, boxes,
+                      box_bytes, leader, pol_kv);
       }
     }
   }

@@ -80,9 +80,13 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
   const uint64_t pol_q = l2_policy_evict_last(), pol_kv = l2_policy_evict_first();
   const int page_size = 1 << p.page_log2;
   const bool small = page_size < kRowsPerTile;
-  const int boxes = pages_of_tile(p);
-  const uint32_t box_bytes = (small ? page_size : kRowsPerTile) * 128u;
+  const int boxes = uniform(pages_of_tile(p)), stages = uniform(sh.stages);
+  const uint32_t box_bytes = uniform((small ? page_size : kRowsPerTile) * 128u);
   const uint32_t q_bytes = static_cast<uint32_t>(sh.tok * p.G) * 128u * C::kColBlocks;
+  const bool leader = elect_one();
+  auto wait = [&](int i, uint32_t phase) {
+    return __all_sync(0xffffffffu, mbar_wait(bar(i), phase, abort_flag, err));
+  };
   RingPos at{0, 0};
   long long fills = 0;
   int nq = 0, q_loads = 0;
@@ -91,7 +95,7 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
   int4 cut = make_int4(0, 0, 0, 0);
   while (ok && walk.next(p, g)) {
     if (g.j0 == 0 && g.slot >= 0) cut = make_int4(g.s.q0, g.s.q_len * p.G, g.h, walk.last_cta(p, g));
-    const int n = g.j1 - g.j0;
+    const int j0 = uniform(g.j0), n = uniform(g.j1) - j0, head = uniform(g.h);
     PageWindow pages(p, g, nq == 0, first_entry);
     const int qb = nq % sh.q_bufs, use = nq / sh.q_bufs;
     bool q_due = true;  // this segment's Q is still to be loaded
@@ -99,35 +103,30 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
     for (int f = 0; f < 2 * n && ok; ++f, ++fills) {
       // Q as soon as its buffer is free, but K and V go ahead of it meanwhile:
       // the slots of the first fills are given back by earlier segments
-      if (lane == 0 && q_due &&
-          (use == 0 || f >= sh.stages / 2 || f == 2 * n - 1 || mbar_test(bar(C::kQEmpty + qb), (use - 1) & 1))) {
-        ok = use == 0 || mbar_wait(bar(C::kQEmpty + qb), (use - 1) & 1, abort_flag, err);
-        if (ok) {
-          ++q_loads;
+      if (q_due && (use == 0 || f >= stages / 2 || f == 2 * n - 1 ||
+                    __all_sync(0xffffffffu, mbar_test(bar(C::kQEmpty + qb), (use - 1) & 1)))) {
+        ok = use == 0 || wait(C::kQEmpty + qb, (use - 1) & 1);
+        if (!ok) break;
+        ++q_loads;
+        q_due = false;
+        if (leader) {
           mbar_arrive_expect_tx(bar(C::kQFull + qb), q_bytes);
           for (int cb = 0; cb < C::kColBlocks; ++cb)
             tma_load_4d_hint(smem + sh.q_at() + qb * sh.q_bytes() + cb * sh.N * 128, tm_q, bar(C::kQFull + qb), cb * 64, 0,
-                             g.s.q0, g.h, pol_q);
+                             g.s.q0, head, pol_q);
         }
-        q_due = false;
+        __syncwarp();
       }
-      const int j = g.j0 + (f >> 1), which = f & 1;
+      const int j = j0 + (f >> 1), which = f & 1;
       if (!which) page = pages.page(p, j);
-      if (lane == 0 && ok) {
-        ok = fills < sh.stages || mbar_wait(bar(C::kEmpty + at.slot), at.phase ^ 1u, abort_flag, err);
-        if (ok) mbar_arrive_expect_tx(bar(C::kFull + at.slot), C::kTileBytes);
-      }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      ok = fills < stages || wait(C::kEmpty + at.slot, at.phase ^ 1u);
       if (!ok) break;
-      if (lane < boxes) {
-        const CUtensorMap *map = which ? tm_v : tm_k;
-        const int in_page = small ? 0 : (j * kRowsPerTile) & (page_size - 1);
-#pragma unroll
-        for (int cb = 0; cb < C::kColBlocks; ++cb)
-          tma_load_4d_hint(smem + at.slot * C::kTileBytes + cb * kColBlockBytes + lane * box_bytes, map,
-                           bar(C::kFull + at.slot), cb * 64, in_page, g.h, page, pol_kv);
-      }
-      at = at.next(sh.stages);
+      if (leader) mbar_arrive_expect_tx(bar(C::kFull + at.slot), C::kTileBytes);
+      const CUtensorMap *map = which ? tm_v : tm_k;
+      const int in_page = small ? 0 : (j * kRowsPerTile) & (page_size - 1);
+      load_pages<D>(smem + at.slot * C::kTileBytes, map, bar(C::kFull + at.slot), in_page, head, page, boxes, box_bytes,
+                    leader, pol_kv);
+      at = at.next(stages);
     }
     ++nq;
   }
@@ -136,8 +135,8 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
     // every copy must have landed before the CTA may exit
     for (int i = max(0, q_loads - sh.q_bufs); i < q_loads; ++i)
       mbar_drain(bar(C::kQFull + i % sh.q_bufs), (i / sh.q_bufs) & 1, err);
-    for (long long i = max(0ll, fills - sh.stages); i < fills; ++i)
-      mbar_drain(bar(C::kFull + static_cast<int>(i % sh.stages)), static_cast<uint32_t>(i / sh.stages) & 1u, err);
+    for (long long i = max(0ll, fills - stages); i < fills; ++i)
+      mbar_drain(bar(C::kFull + static_cast<int>(i % stages)), static_cast<uint32_t>(i / stages) & 1u, err);
   }
   __syncwarp();
 }
