@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(PageTables t, con
   __shared__ int prefix[kPagedMaxRows + 1];
   __shared__ int length[kPagedMaxRows];  // -1: the row's table has no room
   __shared__ int warp_sums[33];
+  launch_dependents();
+  wait_prerequisites();
   const long long room = static_cast<long long>(t.max_pages) << t.page_log2;
   const unsigned ready = free_mask(t.page_refs, t.n_pages, threadIdx.x * kPagesPerThread);
   for (int b = threadIdx.x; b < t.B; b += kPlanThreads) {
@@ -155,6 +157,8 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(PageTables t, con
 
 // blockIdx.x: row of the list.
 __global__ void free_kernel(PageTables t, const __grid_constant__ PageList rows) {
+  launch_dependents();
+  wait_prerequisites();
   const int b = rows.a[blockIdx.x];
   int *row = t.page_table + b * t.table_stride;
   for (int i = threadIdx.x; i < t.max_pages; i += blockDim.x) {
@@ -173,6 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int warp_sums[33];
   __shared__ int *entry[kPageListMax];  // where the target's own page goes
   launch_dependents();
+  wait_prerequisites();
   const unsigned ready = free_mask(t.page_refs, t.n_pages, threadIdx.x * kPagesPerThread);
   const int i = threadIdx.x;  // kPageListMax pairs at most: one a thread
   bool in_use = false;
@@ -233,6 +238,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     fork_copy_kernel(PageTables t, const __grid_constant__ PoolList pools, const __grid_constant__ PageList pairs,
                      const int *status, int chunks) {
   const int i = blockIdx.y, src = pairs.a[i], dst = pairs.b[i];
+  launch_dependents();
   wait_prerequisites();
   if (status[i] != 0) return;
   const int room = static_cast<int>(min(static_cast<long long>(t.max_pages) << t.page_log2, 0x7fffffffll));
@@ -263,6 +269,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 // blockIdx.y: pair; blockIdx.x: (layer, chunk).
 __global__ void __launch_bounds__(kCopyThreads)
     copy_kernel(const __grid_constant__ PoolList pools, const __grid_constant__ PageList pairs, int chunks) {
+  launch_dependents();
+  wait_prerequisites();
   copy_page(pools, blockIdx.x / chunks, pairs.a[blockIdx.y], pairs.b[blockIdx.y], blockIdx.x % chunks);
 }
 
@@ -276,6 +284,7 @@ constexpr int kBlockPages = 4096;
 __global__ void __launch_bounds__(kPlanThreads) count_kernel(const int *refs, int n_pages, int *counts) {
   __shared__ int warp_sums[33];
   launch_dependents();
+  wait_prerequisites();
   int live = 0;
 #pragma unroll
   for (int k = 0; k < kBlockPages / kPlanThreads; ++k) {
@@ -350,6 +359,7 @@ __global__ void __launch_bounds__(kCopyThreads)
                 const int *page_refs, int *out_refs, int B, int max_pages, int n_pages, const int *n_live_in,
                 const int *n_moves_in, const int *rank, const int *holes, const int *movers, const int *mover_refs,
                 int chunks) {
+  launch_dependents();
   wait_prerequisites();
   const int n_live = *n_live_in;
   const long long tid = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x;
@@ -382,31 +392,27 @@ int chunks_of(const PoolList &pools) {
 }  // namespace
 
 cudaError_t launch_reserve(const PageTables &t, const int *n_new, int *status, cudaStream_t stream) {
-  reserve_kernel<<<1, kPlanThreads, 0, stream>>>(t, n_new, status);
-  return cudaGetLastError();
+  return launch_dependent(reserve_kernel, dim3(1), dim3(kPlanThreads), 0, stream, t, n_new, status);
 }
 
 cudaError_t launch_free(const PageTables &t, const PageList &rows, cudaStream_t stream) {
-  free_kernel<<<rows.n, 256, 0, stream>>>(t, rows);
-  return cudaGetLastError();
+  return launch_dependent(free_kernel, dim3(rows.n), dim3(256), 0, stream, t, rows);
 }
 
 cudaError_t launch_fork(const PageTables &t, const PoolList &pools, const PageList &pairs, int *status,
                         cudaStream_t stream) {
-  fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(t, pairs, status);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, t, pairs, status);
   if (e != cudaSuccess) return e;
   const int chunks = chunks_of(pools);
   const dim3 grid(1 + static_cast<unsigned>(pools.total_layers) * chunks, pairs.n);
-  return launch_dependent(fork_copy_kernel, grid, dim3(kCopyThreads), stream, t, pools, pairs, status,
+  return launch_dependent(fork_copy_kernel, grid, dim3(kCopyThreads), 0, stream, t, pools, pairs, status,
                           chunks > 0 ? chunks : 1);
 }
 
 cudaError_t launch_copy(const PoolList &pools, const PageList &pairs, cudaStream_t stream) {
   const int chunks = chunks_of(pools);
   const dim3 grid(static_cast<unsigned>(pools.total_layers) * chunks, pairs.n);
-  copy_kernel<<<grid, kCopyThreads, 0, stream>>>(pools, pairs, chunks);
-  return cudaGetLastError();
+  return launch_dependent(copy_kernel, grid, dim3(kCopyThreads), 0, stream, pools, pairs, chunks);
 }
 
 cudaError_t launch_compact(const PoolList &pools, const int *page_table, int *out_table, long long table_stride,
@@ -415,14 +421,13 @@ cudaError_t launch_compact(const PoolList &pools, const int *page_table, int *ou
   const int n_blocks = (n_pages + kBlockPages - 1) / kBlockPages;
   int *n_moves = workspace, *counts = n_moves + 1, *rank = counts + n_blocks, *holes = rank + n_pages,
       *movers = holes + n_pages, *mover_refs = movers + n_pages;  // compact_workspace_ints in all
-  count_kernel<<<n_blocks, kPlanThreads, 0, stream>>>(page_refs, n_pages, counts);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(count_kernel, dim3(n_blocks), dim3(kPlanThreads), 0, stream, page_refs, n_pages, counts);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(rank_kernel, dim3(n_blocks), dim3(kPlanThreads), stream, page_refs, n_pages, counts, n_blocks,
+  e = launch_dependent(rank_kernel, dim3(n_blocks), dim3(kPlanThreads), 0, stream, page_refs, n_pages, counts, n_blocks,
                        n_live, n_moves, rank, holes, movers, mover_refs);
   if (e != cudaSuccess) return e;
   const int chunks = chunks_of(pools);
-  return launch_dependent(move_kernel, dim3(device_sm_count() * 8), dim3(kCopyThreads), stream, pools, page_table,
+  return launch_dependent(move_kernel, dim3(device_sm_count() * 8), dim3(kCopyThreads), 0, stream, pools, page_table,
                           out_table, table_stride, page_refs, out_refs, B, max_pages, n_pages, n_live, n_moves, rank,
                           holes, movers, mover_refs, chunks > 0 ? chunks : 1);
 }

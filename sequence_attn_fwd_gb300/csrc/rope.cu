@@ -22,6 +22,7 @@
 #include <stdint.h>
 
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace seqattn {
 namespace {
@@ -121,6 +122,8 @@ __global__ void __launch_bounds__(kRopeThreads)
   constexpr int kSlices = D / 16;                               // threads per row
   constexpr int kHeads = kRopeThreads / (kSlices * kTok);       // heads of a CTA at a time
   constexpr int kPieces = Vec16<T>::kPieces;
+  launch_dependents();
+  wait_prerequisites();
   const int sl = threadIdx.x % kSlices;
   const long long t = static_cast<long long>(blockIdx.x) * kTok + threadIdx.x / kSlices % kTok;
   const long long n_tok = static_cast<long long>(p.B) * p.S;
@@ -195,9 +198,9 @@ cudaError_t launch_tile(const RopeParams &p, const RopeTable &tbl, cudaStream_t 
   const long long most = (heads + kHeads - 1) / kHeads;
   want = want < 1 ? 1 : (want > most ? most : want);
   if (tiles > 0x7fffffffll || want > 65535) return cudaErrorInvalidValue;
-  rope_kernel<T, D, kInterleaved, kAppend, kTok>
-      <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(want)), kRopeThreads, 0, stream>>>(p, tbl);
-  return cudaGetLastError();
+  return launch_dependent(rope_kernel<T, D, kInterleaved, kAppend, kTok>,
+                          dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(want)), dim3(kRopeThreads), 0, stream, p,
+                          tbl);
 }
 
 template <typename T, int D, bool kAppend>
