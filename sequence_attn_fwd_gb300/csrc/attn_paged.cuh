@@ -82,19 +82,22 @@ __device__ __forceinline__ int item_tiles(const PagedAttnParams &p, const Seq &s
   return tiles_seen(p, s, (rb + 1) * 2 * p.tok);
 }
 
-// sum_{i=0}^{n-1} floor((a i + b) / m), a, b >= 0 (the lattice points under a
-// line, by the Euclidean algorithm on a and m).
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum_{i=0}^{n-1} floor((a i + b) / m), a and m at most 256 (the lattice points
+// under a line, by the Euclidean algorithm on a and m). Divisions of 32 bits
+// wherever the numbers have no more: with 64 throughout, the sums over a batch of
+// prompt pieces took 3,800 clocks of every CTA's start.
+__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   long long sum = 0;
   while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long top = a * n + b;
+    const unsigned whole_a = a / m, whole_b = b / m;
+    sum += static_cast<long long>(n) * (n - 1) / 2 * whole_a + static_cast<long long>(n) * whole_b;
+    a -= whole_a * m;
+    b -= whole_b * m;
+    const unsigned long long top = static_cast<unsigned long long>(a) * n + b;
     if (top < m) break;
-    n = top / m;
-    b = top % m;
-    const long long t = m;
+    n = top >> 32 ? static_cast<unsigned>(top / m) : static_cast<unsigned>(top) / m;
+    b = static_cast<unsigned>(top - static_cast<unsigned long long>(n) * m);
+    const unsigned t = m;
     m = a;
     a = t;
   }
@@ -117,10 +120,11 @@ __device__ __forceinline__ long long cost_before(const PagedAttnParams &p, const
   if (!p.causal) return static_cast<long long>(rb) * item_cost(tiles_seen(p, s, s.q_len));
   // row block i < rbs - 1 sees ceil((c + i w) / 128) tiles, w = 2 tok rows, where c + i w > 0
   const int w = 2 * p.tok, n = min(rb, rbs - 1);
-  const long long c = static_cast<long long>(s.kv_len) - s.q_len + w;
+  const int c = s.kv_len - s.q_len + w;
   long long sum = 0;
-  const long long first = c > 0 ? 0 : (-c) / w + 1;  // first block that sees a key
-  if (first < n) sum = floor_sum(n - first, kRowsPerTile, w, c + first * w + kRowsPerTile - 1) + (n - first) * kItemCost;
+  const int first = c > 0 ? 0 : (-c) / w + 1;  // first block that sees a key
+  if (first < n)
+    sum = floor_sum(n - first, kRowsPerTile, w, c + first * w + kRowsPerTile - 1) + static_cast<long long>(n - first) * kItemCost;
   if (rb == rbs) sum += item_cost(tiles_seen(p, s, s.q_len));
   return sum;
 }
@@ -130,7 +134,7 @@ __device__ __forceinline__ long long cost_before(const PagedAttnParams &p, const
 // has 24 entries.
 __device__ __forceinline__ int prefix_tiles(const PagedAttnParams &p, int *prefix, int *warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int B = p.cache.B, per = (B + blockDim.x - 1) / blockDim.x;
+  const int B = p.cache.B, per = (B + kThreads - 1) / kThreads;
   const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
   int sum = 0, most = 0;
   for (int b = b0; b < b1; ++b) {
@@ -151,11 +155,11 @@ __device__ __forceinline__ int prefix_tiles(const PagedAttnParams &p, int *prefi
     warp_sums[12 + warp] = most;
   }
   __syncthreads();
-  int base = incl - sum;
-  for (int i = 0; i < warp; ++i) base += warp_sums[i];
-  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) most = max(most, warp_sums[12 + i]);
+  const bool one = lane < kThreads / 32;
+  const int base = incl - sum + __reduce_add_sync(0xffffffffu, one && lane < warp ? warp_sums[lane] : 0);
+  most = __reduce_max_sync(0xffffffffu, one ? warp_sums[12 + lane] : 0);
   for (int b = b0; b < b1; ++b) prefix[b] += base;
-  if (threadIdx.x == blockDim.x - 1) prefix[B] = base + sum;
+  if (threadIdx.x == kThreads - 1) prefix[B] = base + sum;
   __syncthreads();
   return most;
 }
@@ -174,7 +178,7 @@ __device__ __forceinline__ int seq_of(const int *prefix, int B, int pos) {
 // Cost per CTA of a launch of n_ctas.
 __device__ __forceinline__ int cost_per_cta(int total, int n_ctas) { return total / n_ctas + (total % n_ctas != 0); }
 
-// An item and the cost before a position within it.
+// An item and the cost before a position within it, found by a warp.
 struct Place {
   int b, h, rb, r;
 };
@@ -184,14 +188,26 @@ __device__ __forceinline__ Place place_of(const PagedAttnParams &p, const int *p
   const int per_head = max(1, (prefix[b + 1] - prefix[b]) / p.cache.Hkv);
   // (the bounds matter only if cu_seqlens decreases, when costs need not fit 32 bits)
   const int off = max(0, pos - prefix[b]), h = min(off / per_head, p.cache.Hkv - 1);
-  int rest = off - h * per_head, rb = 0;
+  int rest = off - h * per_head;
   const int rbs = row_blocks(p, s);
-  for (; rb < rbs; ++rb) {
-    const int n = item_cost(item_tiles(p, s, rb));
-    if (rest < n) break;
-    rest -= n;
+  if (rbs == 1) return {b, h, 0, rest};
+  const int lane = threadIdx.x & 31;
+  for (int rb = 0; rb < rbs; rb += 32) {
+    const int n = rb + lane < rbs ? item_cost(item_tiles(p, s, rb + lane)) : 0;
+    int incl = n;
+#pragma unroll
+    for (int step = 1; step < 32; step <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, step);
+      if (lane >= step) incl += y;
+    }
+    const unsigned behind = __ballot_sync(0xffffffffu, rest < incl);
+    if (behind != 0) {
+      const int at = __ffs(behind) - 1;
+      return {b, h, rb + at, rest - __shfl_sync(0xffffffffu, incl - n, at)};
+    }
+    rest -= __shfl_sync(0xffffffffu, incl, 31);
   }
-  return {b, h, rb, rest};
+  return {b, h, rbs, rest};
 }
 
 // A CTA's part of one work item: key tiles [j0, j1) of row block rb. The first
@@ -290,21 +306,24 @@ __device__ __forceinline__ int window_entry(const PagedAttnParams &p, const int 
 
 // The producer's view of a segment's pages: 32 entries of the table, one a lane,
 // and the 32 after them on their way, so that no load's latency is between two
-// tiles (it was: 1,300 clocks a tile with pages of 32 keys).
+// tiles (it was: 1,300 clocks a tile with pages of 32 keys). The first 32 of
+// those are asked for behind the first tile, which does not wait for them.
 struct PageWindow {
   const int *row;
   int kv_len, from, now, ahead;
   __device__ __forceinline__ PageWindow(const PagedAttnParams &p, const Segment &g, bool have_first, int first)
       : row(page_row(p, g)), kv_len(g.s.kv_len), from(first_page(p, g.j0)) {
     now = have_first ? first : window_entry(p, row, kv_len, from);
-    ahead = window_entry(p, row, kv_len, from + 32);
+    ahead = -1;
   }
+  __device__ __forceinline__ void prefetch(const PagedAttnParams &p) { ahead = window_entry(p, row, kv_len, from + 32); }
   // This lane's page of key tile j (lanes below pages_of_tile): n_pages, which
   // reads as zeros, where there is none. Tiles in ascending order.
   __device__ __forceinline__ int page(const PagedAttnParams &p, int j) {
     const int boxes = pages_of_tile(p), lane = threadIdx.x & 31;
     int off = first_page(p, j) - from;
     if (off >= 32) {  // (a tile's pages are never in two windows)
+      __syncwarp();   // a branch, not a choice between `now` and `ahead`: that one would wait for both
       from += 32;
       off -= 32;
       now = ahead;
@@ -321,10 +340,11 @@ struct PageWindow {
 // registers.)
 template <int D, int kBoxes>
 __device__ __forceinline__ void load_boxes(uint32_t dst, const CUtensorMap *map, uint32_t bar, int in_page, int head,
-                                           int page, uint32_t box_bytes, bool leader, uint64_t pol) {
+                                           int first, int page, uint32_t box_bytes, bool leader, uint64_t pol) {
   int pg[kBoxes];
+  dst += first * box_bytes;
 #pragma unroll
-  for (int i = 0; i < kBoxes; ++i) pg[i] = uniform(__shfl_sync(0xffffffffu, page, i));
+  for (int i = 0; i < kBoxes; ++i) pg[i] = uniform(__shfl_sync(0xffffffffu, page, first + i));
   if (leader) {
 #pragma unroll
     for (int i = 0; i < kBoxes; ++i)
@@ -337,10 +357,14 @@ __device__ __forceinline__ void load_boxes(uint32_t dst, const CUtensorMap *map,
 template <int D>
 __device__ __forceinline__ void load_pages(uint32_t dst, const CUtensorMap *map, uint32_t bar, int in_page, int head,
                                            int page, int boxes, uint32_t box_bytes, bool leader, uint64_t pol) {
-  if (boxes == 1) load_boxes<D, 1>(dst, map, bar, in_page, head, page, box_bytes, leader, pol);
-  else if (boxes == 2) load_boxes<D, 2>(dst, map, bar, in_page, head, page, box_bytes, leader, pol);
-  else if (boxes == 4) load_boxes<D, 4>(dst, map, bar, in_page, head, page, box_bytes, leader, pol);
-  else load_boxes<D, 8>(dst, map, bar, in_page, head, page, box_bytes, leader, pol);
+  if (boxes == 1) {
+    load_boxes<D, 1>(dst, map, bar, in_page, head, 0, page, box_bytes, leader, pol);
+  } else if (boxes == 2) {
+    load_boxes<D, 2>(dst, map, bar, in_page, head, 0, page, box_bytes, leader, pol);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < boxes; i += 4) load_boxes<D, 4>(dst, map, bar, in_page, head, i, page, box_bytes, leader, pol);
+  }
 }
 
 // Whether a page of a segment's key tiles is missing, found by a warp at the
@@ -481,6 +505,7 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
         if (leader) mbar_arrive_expect_tx(bar(W::kFull + slot), C::kTileBytes);
         load_pages<D>(sRing + slot * C::kTileBytes, which ? tm_v : tm_k, bar(W::kFull + slot), in_page, head, page, boxes,
                       box_bytes, leader, pol_kv);
+        if (j == 0 && which == 1) pages.prefetch(p);
       }
     }
   }
@@ -889,7 +914,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
+  if (threadIdx.x == kTmaWarp * 32) {
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
+  }
   wait_prerequisites();  // nothing of the tensors or the workspace is touched before
+  // an earlier timeout, not yet cleared by the host: this CTA skips its work
+  // and its rows come out as O = 0, lse = -inf
+  const bool failed = warp == kMmaWarp1 && *reinterpret_cast<volatile int *>(err) != kErrNone;
   const int most = prefix_tiles(p, prefix, warp_sums);
   const bool narrow = most * p.G <= 64;
   const L sh(most * p.G, p.G);
@@ -905,47 +937,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     first_entry = window_entry(p, page_row(p, g), g.s.kv_len, first_page(p, g.j0));
     if (lane == 0) *first = g;
   }
-  if (threadIdx.x == 0) {
-    if (narrow) {
-      for (int s = 0; s < sh.stages; ++s) {
-        mbar_init(bar(L::kFull + s), 1);
-        mbar_init(bar(L::kEmpty + s), 1);
+  if (warp == kMmaWarp1) {
+    // a barrier a lane (one thread for all of them: 1,400 clocks)
+    for (int i = lane; i < (narrow ? L::kNumBarriers : C::kNumBarriers); i += 32) {
+      int arrivals = 1;
+      if (narrow) {
+        if (i == L::kPFull || i == L::kPFull + 1) arrivals = 4 * sh.groups;
+      } else {
+        if (i == W::kQEmpty || i == W::kMmaDone || (i >= W::kEmpty && i < W::kEmpty + C::kStages)) arrivals = 2;
+        if (i == W::kPFull || i == W::kPFull + 1) arrivals = 4;
       }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(bar(L::kQFull + i), 1);
-        mbar_init(bar(L::kQEmpty + i), 1);
-        mbar_init(bar(L::kSFull + i), 1);
-        mbar_init(bar(L::kPFull + i), 4 * sh.groups);
-        mbar_init(bar(L::kPvDone + i), 1);
-      }
-      mbar_init(bar(L::kMmaDone), 1);
-    } else {
-      mbar_init(bar(W::kQFull), 1);
-      mbar_init(bar(W::kQEmpty), 2);
-      for (int s = 0; s < C::kStages; ++s) {
-        mbar_init(bar(W::kFull + s), 1);
-        mbar_init(bar(W::kEmpty + s), 2);
-      }
-      for (int t = 0; t < 2; ++t) {
-        mbar_init(bar(W::kSFull + t), 1);
-        mbar_init(bar(W::kPFull + t), 4);
-        mbar_init(bar(W::kOFull + t), 1);
-      }
-      mbar_init(bar(W::kMmaDone), 2);
+      mbar_init(bar(i), arrivals);
     }
-    // an earlier timeout, not yet cleared by the host: this CTA skips its work
-    // and its rows come out as O = 0, lse = -inf
-    *abort_flag = *reinterpret_cast<volatile int *>(err) != kErrNone;
-    *turn = 0;
+    if (lane == 0) {
+      *abort_flag = failed;
+      *turn = 0;
+    }
     fence_barrier_init();
   }
-  {
+  if (warp != kTmaWarp) {
     // rows of Q that no token fills: zeros, not whatever was there
     const uint32_t at = base + (narrow ? sh.q_at() : 0);
     const int pieces = (narrow ? sh.q_bufs * sh.q_bytes() : 2 * C::kTileBytes) / 16;
-    for (int i = threadIdx.x; i < pieces; i += kThreads) st_shared_v4(at + 16 * i, 0u, 0u, 0u, 0u);
-    fence_proxy_async_shared();  // these and the prefix sums before the copies that follow
+    for (int i = warp < kTmaWarp ? threadIdx.x : threadIdx.x - 32; i < pieces; i += kThreads - 32)
+      st_shared_v4(at + 16 * i, 0u, 0u, 0u, 0u);
   }
+  fence_proxy_async_shared();  // these and the prefix sums before the copies that follow
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -126,6 +126,7 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
       const int in_page = small ? 0 : (j * kRowsPerTile) & (page_size - 1);
       load_pages<D>(smem + at.slot * C::kTileBytes, map, bar(C::kFull + at.slot), in_page, head, page, boxes, box_bytes,
                     leader, pol_kv);
+      if (f == 1) pages.prefetch(p);
       at = at.next(stages);
     }
     ++nq;
