@@ -24,6 +24,8 @@
  *              belong to no sequence and are left as they are. Entries outside
  *              [0, total] are clamped; if they decrease, results are unspecified
  *              but every access stays inside the tensors.
+ * The kernels are launched as programmatic dependents of what is before them on
+ * the stream and wait for it before they touch memory.
  * Everything that changes from step to step is read on the device, so a call
  * can be captured into a graph and replayed on new lengths and tables.
  */
@@ -59,7 +61,8 @@ typedef struct {
  *   workspace 16-byte aligned device memory of attn_paged_workspace_bytes(...)
  *             bytes; no other call may use it at the same time
  * Strides are in elements and multiples of 8. Rows that see no key: O = 0,
- * lse = -inf. Keys inside kv_lens must be finite. D 64 or 128, Hq / Hkv at
+ * lse = -inf. Keys and values
+ * inside kv_lens must be finite (a row with a NaN score comes out as NaN). D 64 or 128, Hq / Hkv at
  * most 128, B at most 4096, max_pages * page_size at most 2^30, and at most
  * 2^31 tiles of 128 keys over all row blocks of 256 rows (else
  * ATTN_ERR_UNSUPPORTED). Two kernels: the attention itself, its key tiles
@@ -122,6 +125,9 @@ int paged_append(const rope_rows *q, const rope_rows *k, const rope_rows *v, con
  * Page management. page_refs, int32 [n_pages] on the device, counts the table
  * entries that hold each page; a page with 0 is free. New pages are always the
  * lowest free ones, handed out in the order of the rows that need them.
+ * kv_lens and the entries of the table change through these calls only: a
+ * row's entries behind its length are -1. Entries in front may be set to -1
+ * (evicted) by the caller, who then counts their references down.
  * status (int32 per row or pair, device, output): 0 done, PAGED_NO_PAGES, or
  * the reason given below; a row or pair that is not done is left unchanged.
  * All rows of one call belong to one table; calls that change the same table

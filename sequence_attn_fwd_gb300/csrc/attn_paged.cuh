@@ -21,8 +21,16 @@
 //
 // Inside a CTA the roles are those of the dense forward: a TMA producer warp,
 // an MMA issuer per query tile taking turns, a softmax warpgroup per query
-// tile. The producer reads the page table, one lane per page of a key tile
-// (128 / page_size boxes, or one box inside a larger page).
+// tile. The producer reads the page table, a window of 32 entries ahead, and
+// issues a key tile as 128 / page_size boxes, or one box inside a larger page; 16
+// keys a page cost no more than 128 (319 us against 318 for the batch below).
+//
+// Measured (GB300): 1,024 new tokens behind 65,536 keys, 32 heads over 8 KV heads
+// of 128, 0.78 ms = 1,420 TFLOP/s, 3,000 clocks a pair of tiles (the dense
+// forward's share; the tensor pipe's own time is 2,048); six sequences of up to
+// 600 new tokens behind up to 12,400 keys 162 us, and 11 more for the merge: the
+// tiles at that rate, 12,000 clocks until the first scores of a CTA and about as
+// many from an item to the next, most of it the epilogue of the softmax warps.
 //
 // This is the wide form. When no sequence of the call has more than 64 rows per
 // KV head, the launch takes the narrow form (attn_paged_narrow.cuh) on the same
@@ -106,8 +114,9 @@ __device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned 
 
 // The cost of an item is its key tiles and kItemCost more, for what comes once
 // per item: Q, the first scores' and the last product's way through the empty
-// pipeline, the epilogue (14,000 to 18,000 clocks measured on items of 4 tiles,
-// of 3,600 to 4,500 each). An item that sees no key costs nothing.
+// pipeline, the epilogue (about 12,000 clocks, of 3,000 a tile; with 2, 4, 6, 8 a
+// batch of prompt pieces took 190, 174, 173, 177 us and a small cross attention
+// 37.0, 36.4, 37.5, 39.3). An item that sees no key costs nothing.
 constexpr int kItemCost = 4;
 __device__ __forceinline__ int item_cost(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
 
@@ -793,8 +802,8 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
     const unsigned valid = __ballot_sync(0xffffffffu, row_valid);
     // Rows leave through shared memory, 64 bytes of each at a time, so that a
     // store instruction writes 64 bytes of eight rows (each lane its own row, 16
-    // bytes at a time, cost twice the sectors: 10,000 clocks a segment, now
-    // about half). `stage`: 32 rows of this warp, 80 bytes apart.
+    // bytes at a time, cost twice the sectors and 10,000 clocks a segment; this
+    // 4,500 to 7,500). `stage`: 32 rows of this warp, 80 bytes apart.
     const int ln = hidden(lane), rr = hidden(r);
     const uint32_t stage = smem_addr(own), mine = stage + ln * 80u;
     const int sub = ln >> 2, quad = ln & 3;
@@ -1084,7 +1093,8 @@ __device__ __forceinline__ void merge_few(const PagedAttnParams &p, const int4 &
 // the keys. Bound by latency, so the loads are made to overlap: with two (four)
 // partials a warp takes four (two) rows at once; with more, one row, eight
 // partials at a time. (Loads that wait for the weights, two partials at a time:
-// 17 us behind the attention of a batch of drafts, this: 8.)
+// 17 us behind the attention of a batch of drafts, this: 8. Half the CTAs with
+// twice the rows: 2.7 us more behind a small cross attention.)
 constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_constant__ PagedAttnParams p) {
