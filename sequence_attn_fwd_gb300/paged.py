@@ -19,6 +19,7 @@ sequences (or CPU int32 tensors), checked before anything is launched.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import struct
 
@@ -114,11 +115,17 @@ def _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens):
                        D), dev, B, Hkv, D
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(Hq: int, Hkv: int, total_q: int, D: int) -> int:
+    """The library's answer for these sizes (a call of its own otherwise)."""
+    return int(lib.attn_paged_workspace_bytes(Hq, Hkv, total_q, D))
+
+
 def attn_paged_workspace_bytes(Hq: int, Hkv: int, total_q: int, D: int) -> int:
     """Device workspace bytes attn_paged needs."""
-    n = lib.attn_paged_workspace_bytes(Hq, Hkv, total_q, D)
+    n = _workspace_bytes(Hq, Hkv, total_q, D)
     _require(n > 0, "invalid sizes")
-    return int(n)
+    return n
 
 
 def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
@@ -160,7 +167,7 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, pa
         used.append(lse)
     if total == 0 or B == 0:
         return out, lse
-    need = lib.attn_paged_workspace_bytes(Hq, Hkv, total, D)
+    need = _workspace_bytes(Hq, Hkv, total, D)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=where)
     else:

@@ -690,3 +690,61 @@ def test_captured_serving_step(sa):
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert caches[0].kv_lens.tolist() == [20] * 3
     assert torch.equal(caches[0].page_table, caches[1].page_table)
+
+
+def serving_chain(sa, seed, pause=lambda: None):
+    """Steps of a cache whose kernels depend on one another in every way: outputs and the final state."""
+    Hq, Hkv, D, ps, rows = 14, 2, 128, 16, 8
+    plan = sa.RopePlan(D, (64,))
+    cache = sa.PagedCache(300, Hkv, D, rows=rows, max_pages=40, page_size=ps, plan=plan)
+    cache.k_pages.zero_(), cache.v_pages.zero_()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    outs = []
+    for it in range(24):
+        if it % 6 == 3:
+            cache.free([4, 5, 6, 7])
+            pause()
+            cache.fork([0, 1, 0, 2], [4, 5, 6, 7])
+            pause()
+        new = [1] * rows if it % 4 else [40, 3, 70, 1] + [0] * 4
+        if it % 6 < 3:
+            new[4:] = [0] * 4
+        n_new, cu = i32(new), torch.nn.functional.pad(i32(new).cumsum(0), (1, 0)).to(I32)
+        total = sum(new)
+        q, k, v = (torch.randn((H, total, D), generator=g, device="cuda").to(BF) for H in (Hq, Hkv, Hkv))
+        pos = torch.randint(0, 5000, (1, total), generator=g, device="cuda", dtype=I32)
+        pause()
+        cache.reserve(n_new)
+        pause()
+        for _ in range(2):  # the second call reads what the first one read, into tensors that may be its neighbours
+            outs.append(cache.step(0, q, k, v, cu, pos))
+            pause()
+        if it % 8 == 7:
+            cache.compact()
+            pause()
+    return outs, (cache.page_table, cache.kv_lens, cache.page_refs)
+
+
+def test_a_chain_without_waits_equals_one_with_waits(sa):
+    """Every kernel may start before the one ahead of it has ended; none may read or write too early."""
+    want, state = serving_chain(sa, 3, torch.cuda.synchronize)
+    for _ in range(3):
+        got, after = serving_chain(sa, 3)
+        for (o, lse), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
+        for a, b in zip(after, state):
+            assert torch.equal(a, b)
+
+
+def test_chains_on_two_streams_at_once(sa):
+    want = [serving_chain(sa, s, torch.cuda.synchronize)[0] for s in (5, 6)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for s, stream in zip((5, 6), streams):
+        with torch.cuda.stream(stream):
+            got.append(serving_chain(sa, s)[0])
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for (o, lse), (wo, wl) in zip(a, b):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
