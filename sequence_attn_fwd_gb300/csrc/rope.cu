@@ -12,8 +12,8 @@
 // -- of one token, forms its eight sines and cosines once, in registers, and
 // goes over heads with them, four rows in flight; D / 16 threads cover a row
 // with whole 32-byte sectors in either pairing. (Sines in shared memory, shared
-// by the CTA, cost more in reads than they save: 109 us instead of 91 for
-// 32,768 tokens of 32 heads of 128 in bf16, 5.9 TB/s of the 6.8 that a copy
+// by the CTA, cost more in reads than they save: 109 us instead of 89 for
+// 32,768 tokens of 32 heads of 128 in bf16, 6.0 TB/s of the 6.8 that a copy
 // reaches.) The heads of a token are dealt over the CTA and, with few tokens, over
 // the grid.
 #include <cuda_bf16.h>
@@ -171,8 +171,11 @@ __global__ void __launch_bounds__(kRopeThreads)
         pack(y, w);
       }
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-        *reinterpret_cast<uint4 *>(to + piece_at<T, D, kInterleaved>(sl, i)) = w[i];
+      for (int i = 0; i < kPieces; ++i) {
+        uint4 *at = reinterpret_cast<uint4 *>(to + piece_at<T, D, kInterleaved>(sl, i));
+        if (kAppend) *at = w[i];  // the attention of the same step reads it
+        else __stcs(at, w[i]);    // (2 % of a long sequence's time)
+      }
     }
   };
   auto in = [&](const RopeView &x) { return static_cast<const T *>(x.in) + (kAppend ? 0 : b * x.in_b) + s * x.in_s; };
@@ -206,7 +209,7 @@ cudaError_t launch_tile(const RopeParams &p, const RopeTable &tbl, cudaStream_t 
 template <typename T, int D, bool kAppend>
 cudaError_t launch_typed_rope(const RopeParams &p, const RopeTable &tbl, bool interleaved, cudaStream_t stream) {
   // Tiles of 32 tokens give a thread the most heads to its sines (32,768 tokens
-  // of 32 heads in bf16: 91 us; tiles of 16 and 8: 95 us); with fewer tokens than
+  // of 32 heads in bf16: 89 us; tiles of 16 and 8: 4 us more); with fewer tokens than
   // one such tile an SM, tiles of 4 give more CTAs.
   const bool small = static_cast<long long>(p.B) * p.S < 32ll * device_sm_count();
   if (interleaved)
