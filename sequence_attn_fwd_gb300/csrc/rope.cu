@@ -171,11 +171,8 @@ __global__ void __launch_bounds__(kRopeThreads)
         pack(y, w);
       }
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        uint4 *at = reinterpret_cast<uint4 *>(to + piece_at<T, D, kInterleaved>(sl, i));
-        if (kAppend) *at = w[i];  // the attention of the same step reads it
-        else __stcs(at, w[i]);    // (2 % of a long sequence's time)
-      }
+      for (int i = 0; i < kPieces; ++i)  // (streaming stores: 2 % of a long sequence's time)
+        __stcs(reinterpret_cast<uint4 *>(to + piece_at<T, D, kInterleaved>(sl, i)), w[i]);
     }
   };
   auto in = [&](const RopeView &x) { return static_cast<const T *>(x.in) + (kAppend ? 0 : b * x.in_b) + s * x.in_s; };
