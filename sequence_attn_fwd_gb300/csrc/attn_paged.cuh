@@ -32,9 +32,11 @@
 // tiles at that rate, 12,000 clocks until the first scores of a CTA and about as
 // many from an item to the next, most of it the epilogue of the softmax warps.
 //
-// This is the wide form. When no sequence of the call has more than 64 rows per
-// KV head, the launch takes the narrow form (attn_paged_narrow.cuh) on the same
-// ranges: every CTA finds that out for itself, along with its range.
+// This is the wide form. Sequences of at most 64 rows per KV head are the narrow
+// form's (attn_paged_narrow.cuh): their items make a line of their own, and the
+// CTAs are dealt to the two lines by their costs. Every CTA finds that out for
+// itself, along with its range. (63 single tokens and a prompt piece of 512, 2.1 GB
+// of cache: 356 us, with every item in the wide form 496.)
 #pragma once
 
 namespace seqattn {
@@ -62,7 +64,7 @@ struct Cfg {
   static constexpr int kPrefixAt = 65536;
   static_assert(kPrefixAt >= 2 * kTileBytes && kPrefixAt + 4 * (kPagedMaxSeqs + 1) <= 2 * kTileBytes + kStages * kTileBytes,
                 "prefix sums inside either ring");
-  static constexpr int kSmemBytes = 1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 24 + 48 + 4 * kRedFloats;
+  static constexpr int kSmemBytes = 1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 36 + 48 + 4 * kRedFloats;
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -118,6 +120,11 @@ __device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned 
 // batch of prompt pieces took 190, 174, 173, 177 us and a small cross attention
 // 37.0, 36.4, 37.5, 39.3). An item that sees no key costs nothing.
 constexpr int kItemCost = 4;
+// Cost of a narrow tile in wide ones, as the two share the machine. Five mixes of
+// 31 to 200 single tokens with prompt pieces took in all, at 0.5, 0.6, 0.65, 0.7,
+// 0.75, 1: 1,138, 1,085, 1,074, 1,080, 1,127, 1,345 us with heads of 128; at 0.4,
+// 0.55, 0.65, 0.75, 1: 933, 855, 833, 878, 1,027 us with heads of 64.
+constexpr float kNarrowUnit = 0.65f;
 __device__ __forceinline__ int item_cost(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
 
 // Cost of the items before row block `rb` of one KV head of a sequence.
@@ -138,39 +145,80 @@ __device__ __forceinline__ long long cost_before(const PagedAttnParams &p, const
   return sum;
 }
 
-// prefix[0 .. B]: cost of all KV heads of the sequences before each, by
-// every thread of the CTA; returns the most new tokens of a sequence. warp_sums
-// has 24 entries.
-__device__ __forceinline__ int prefix_tiles(const PagedAttnParams &p, int *prefix, int *warp_sums) {
+// The line of costs that a CTA works on: the narrow form's or the wide one's.
+struct Line {
+  bool narrow;
+  int total, n_ctas, first_cta;  // its cost, and its CTAs
+  int rows;                      // most rows of a narrow sequence
+};
+
+// Rows per KV head up to which a sequence is the narrow form's.
+constexpr int kNarrowRows = 64;
+__device__ __forceinline__ bool is_narrow(const PagedAttnParams &p, const Seq &s) {
+  return s.q_len <= kNarrowRows && s.q_len * p.G <= kNarrowRows && gridDim.x > 1;
+}
+
+// Deals the grid's CTAs, the first ones to the narrow form, so that the later of
+// the two ends as early as it can.
+__device__ __forceinline__ Line line_of(int narrow_total, int wide_total, int rows) {
+  const int n = gridDim.x;
+  if (wide_total <= 0 || narrow_total <= 0) return {wide_total <= 0, max(wide_total, narrow_total), n, 0, rows};
+  const float a = static_cast<float>(narrow_total) * kNarrowUnit, b = static_cast<float>(wide_total);
+  int wide = max(1, min(n - 1, static_cast<int>(n * (b / (a + b)))));
+  if (wide < n - 1 && fmaxf(a / (n - wide), b / wide) > fmaxf(a / (n - wide - 1), b / (wide + 1))) ++wide;
+  const bool narrow = static_cast<int>(blockIdx.x) < n - wide;
+  return {narrow, narrow ? narrow_total : wide_total, narrow ? n - wide : wide, narrow ? 0 : n - wide, rows};
+}
+
+// The CTA's line, and prefix[0 .. B]: cost in it of all KV heads of the sequences
+// before each; by every thread of the CTA. sums has 36 entries.
+__device__ __forceinline__ Line prefix_costs(const PagedAttnParams &p, int *prefix, int *sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int B = p.cache.B, per = (B + kThreads - 1) / kThreads;
   const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
-  int sum = 0, most = 0;
+  int narrow = 0, wide = 0, rows = 0;
   for (int b = b0; b < b1; ++b) {
     const Seq s = sequence(p, b);
-    most = max(most, s.q_len);
-    prefix[b] = sum;
-    if (s.q_len > 0) sum += static_cast<int>(cost_before(p, s, row_blocks(p, s))) * p.cache.Hkv;
+    const int cost = s.q_len > 0 ? static_cast<int>(cost_before(p, s, row_blocks(p, s))) * p.cache.Hkv : 0;
+    if (is_narrow(p, s)) {
+      rows = max(rows, s.q_len * p.G);
+      narrow += cost;
+      prefix[b] = cost;
+    } else {
+      wide += cost;
+      prefix[b] = -cost;
+    }
   }
-  int incl = sum;
+  int narrow_incl = narrow, wide_incl = wide;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += y;
+    const int x = __shfl_up_sync(0xffffffffu, narrow_incl, off), y = __shfl_up_sync(0xffffffffu, wide_incl, off);
+    if (lane >= off) {
+      narrow_incl += x;
+      wide_incl += y;
+    }
   }
-  most = __reduce_max_sync(0xffffffffu, most);
+  rows = __reduce_max_sync(0xffffffffu, rows);
   if (lane == 31) {
-    warp_sums[warp] = incl;
-    warp_sums[12 + warp] = most;
+    sums[warp] = narrow_incl;
+    sums[12 + warp] = wide_incl;
+    sums[24 + warp] = rows;
   }
   __syncthreads();
   const bool one = lane < kThreads / 32;
-  const int base = incl - sum + __reduce_add_sync(0xffffffffu, one && lane < warp ? warp_sums[lane] : 0);
-  most = __reduce_max_sync(0xffffffffu, one ? warp_sums[12 + lane] : 0);
-  for (int b = b0; b < b1; ++b) prefix[b] += base;
-  if (threadIdx.x == kThreads - 1) prefix[B] = base + sum;
+  const int of_narrow = one ? sums[lane] : 0, of_wide = one ? sums[12 + lane] : 0;
+  const Line line = line_of(__reduce_add_sync(0xffffffffu, of_narrow), __reduce_add_sync(0xffffffffu, of_wide),
+                               __reduce_max_sync(0xffffffffu, one ? sums[24 + lane] : 0));
+  int at = __reduce_add_sync(0xffffffffu, lane < warp ? (line.narrow ? of_narrow : of_wide) : 0) +
+           (line.narrow ? narrow_incl - narrow : wide_incl - wide);
+  for (int b = b0; b < b1; ++b) {
+    const int cost = line.narrow ? prefix[b] : -prefix[b];
+    prefix[b] = at;
+    at += max(cost, 0);
+  }
+  if (threadIdx.x == kThreads - 1) prefix[B] = at;
   __syncthreads();
-  return most;
+  return line;
 }
 
 // The sequence whose range of the line of all costs has `pos`.
@@ -237,12 +285,16 @@ __device__ __forceinline__ const int *page_row(const PagedAttnParams &p, const S
 // runs once per CTA costs its instruction fetches more than its work.
 struct Walk {
   int pos, end, per;
+  int first_cta, last_cta;  // of the line
   const Segment *first;
-  bool fresh;
-  __device__ __forceinline__ Walk(int total, const Segment *first_, int n_ctas) : first(first_), fresh(true) {
-    per = cost_per_cta(total, n_ctas);
-    pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
-    end = static_cast<int>(min(static_cast<long long>(pos) + per, static_cast<long long>(total)));
+  bool fresh, narrow;
+  __device__ __forceinline__ Walk(const Line &line, const Segment *first_) : first(first_), fresh(true), narrow(line.narrow) {
+    per = cost_per_cta(line.total, line.n_ctas);
+    first_cta = line.first_cta;
+    last_cta = line.first_cta + line.n_ctas - 1;
+    const long long total = line.total;
+    pos = static_cast<int>(min(static_cast<long long>(per) * (static_cast<int>(blockIdx.x) - first_cta), total));
+    end = static_cast<int>(min(static_cast<long long>(pos) + per, total));
   }
   // The segment of row block rb at cost `within` of it, which is position `pos`
   // (j0 == j1 if the range ends before its first tile).
@@ -275,7 +327,7 @@ struct Walk {
           do {
             if (++g.b >= p.cache.B) return false;
             g.s = sequence(p, g.b);
-          } while (g.s.q_len == 0 || g.s.kv_len == 0);
+          } while (g.s.q_len == 0 || g.s.kv_len == 0 || is_narrow(p, g.s) != narrow);
           g.rbs = row_blocks(p, g.s);
         }
       }
@@ -290,8 +342,8 @@ struct Walk {
     return false;
   }
   // The last CTA of an item that this one begins with segment g.
-  __device__ __forceinline__ int last_cta(const PagedAttnParams &p, const Segment &g) const {
-    return min((g.next - (g.j1 + kItemCost) + item_tiles(p, g.s, g.rb) + kItemCost - 1) / per, static_cast<int>(gridDim.x) - 1);
+  __device__ __forceinline__ int ends_in(const PagedAttnParams &p, const Segment &g) const {
+    return min(first_cta + (g.next - (g.j1 + kItemCost) + item_tiles(p, g.s, g.rb) + kItemCost - 1) / per, last_cta);
   }
   // Key tiles of segment g that query tile t goes through, counted from g.j0.
   static __device__ __forceinline__ int tiles(const PagedAttnParams &p, const Segment &g, int t) {
@@ -487,7 +539,7 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
   int4 cut = make_int4(0, 0, 0, 0);
   while (ok && walk.next(p, g)) {
     if (g.j0 == 0 && g.slot >= 0)
-      cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, walk.last_cta(p, g));
+      cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, walk.ends_in(p, g));
     const int n_max = uniform(max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1)));
     const int j0 = uniform(g.j0), head = uniform(g.h);
     const bool two = Walk::tiles(p, g, 1) > 0;
@@ -653,6 +705,7 @@ struct WarpWalk {
 };
 constexpr int kStageBytes = 2560;  // 32 rows of a warp's epilogue, 80 bytes apart
 constexpr int kWarpBytes = 2688;   // and its WarpWalk
+static_assert(sizeof(Segment) <= 48, "the first segment's place");
 static_assert(kStageBytes + sizeof(WarpWalk) <= kWarpBytes, "a softmax warp's shared memory");
 
 // x, in a way that nothing computed from it moves ahead of this place: what the
@@ -911,8 +964,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *turn = reinterpret_cast<volatile int *>(tmem_slot + 2);  // next MMA burst slot (wide)
   int *warp_sums = reinterpret_cast<int *>(tmem_slot + 4);
-  Segment *first = reinterpret_cast<Segment *>(warp_sums + 24);
-  float *red = reinterpret_cast<float *>(warp_sums + 36);
+  Segment *first = reinterpret_cast<Segment *>(warp_sums + 36);
+  float *red = reinterpret_cast<float *>(warp_sums + 48);
   int *prefix = reinterpret_cast<int *>(smem + C::kPrefixAt);
   const uint32_t bar0 = smem_addr(bars), base = smem_addr(smem);
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -931,10 +984,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // an earlier timeout, not yet cleared by the host: this CTA skips its work
   // and its rows come out as O = 0, lse = -inf
   const bool failed = warp == kMmaWarp1 && *reinterpret_cast<volatile int *>(err) != kErrNone;
-  const int most = prefix_tiles(p, prefix, warp_sums);
-  const bool narrow = most * p.G <= 64;
-  const L sh(most * p.G, p.G);
-  const Walk walk(prefix[p.cache.B], first, gridDim.x);
+  const Line line = prefix_costs(p, prefix, warp_sums);
+  const bool narrow = line.narrow;
+  const L sh(line.rows, p.G);
+  const Walk walk(line, first);
   int first_entry = -1;  // the producer's lanes: the first pages
   if (warp == kTmaWarp && walk.pos < walk.end) {
     Segment g;

@@ -257,6 +257,15 @@ def test_row_counts_around_the_tiles(sa, new, kv, G):
     run_case(sa, new, kv, 2 * G, 2, 64, 16, False, seed=G)
 
 
+@pytest.mark.parametrize("new,kv", [([1] * 30 + [200], [500 + 37 * b for b in range(30)] + [900]), ([300, 1], [300, 3000]),
+                                    ([1, 0, 70, 2, 0, 1], [4000, 50, 130, 2, 0, 1]), ([65, 64, 1], [65, 64, 1])])
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 1), (128, 16)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_single_tokens_among_prompt_pieces(sa, new, kv, D, G, causal):
+    """Sequences of few rows and of many in one call: the two forms on their own shares of the machine."""
+    run_case(sa, new, kv, 2 * G, 2, D, 16, causal, seed=len(new), behind=3, holes=[(0, 1, -1)])
+
+
 def test_offsets_past_32_bits(sa):
     """Pools of more than 2^32 elements: append, attend, fork and copy at their far end."""
     Hkv, ps, D, n_pages = 8, 128, 128, 33100
