@@ -54,17 +54,18 @@ struct Cfg {
   static constexpr int kStages = 131072 / kTileBytes;
   static constexpr int kNumBarriers = 2 + 2 * kStages + 7;
   // tiles of the wide form (Q, ring, epilogue) or of the narrow one (ring, P, Q), then
-  // barriers, three words, warp sums, the first segment, the narrow form's
-  // reductions. The prefix sums over the sequences are needed before the tiles
+  // barriers, three words, four segments, the narrow form's reductions (before
+  // them, in the same place, the sums over warps). The prefix sums over the sequences are needed before the tiles
   // arrive only: they lie where the ring of either form will be.
   static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 64 * D * 2;
-  static_assert(2 * kTileBytes + kStages * kTileBytes + 8 * 2688 <= kAreaBytes, "wide layout");
-  static constexpr int kMaxBarriers = 2 * (196608 / kTileBytes) + 11;
+  static_assert(2 * kTileBytes + kStages * kTileBytes + 8 * 2560 <= kAreaBytes, "wide layout");
+  static constexpr int kItemBarrier = 2 * (196608 / kTileBytes) + 11;  // behind those of either form
+  static constexpr int kMaxBarriers = kItemBarrier + 8;
   static constexpr int kRedFloats = 2 * 6 * 32;
   static constexpr int kPrefixAt = 65536;
   static_assert(kPrefixAt >= 2 * kTileBytes && kPrefixAt + 4 * (kPagedMaxSeqs + 1) <= 2 * kTileBytes + kStages * kTileBytes,
                 "prefix sums inside either ring");
-  static constexpr int kSmemBytes = 1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 36 + 48 + 4 * kRedFloats;
+  static constexpr int kSmemBytes = 1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 48 + 4 * kRedFloats;
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -274,21 +275,20 @@ struct Segment {
   int b, rbs, h, rb, j0, j1;  // rbs: row blocks of the sequence
   int slot;  // partial written, -1: the whole item, written directly
   int next;  // position of the line behind the segment
+  int ring;  // the first K tile's place in the order of all tiles of the CTA
 };
+static_assert(sizeof(Segment) == 48, "its place in shared memory");
 __device__ __forceinline__ const int *page_row(const PagedAttnParams &p, const Segment &g) {
   return p.cache.page_table + g.b * p.cache.table_stride;
 }
 
-// Walks the segments of a CTA's range of the line in order; every role walks its
-// own. The first one is found once, by the producer warp, and read by every role
-// from shared memory; the code for the others is one copy for all roles: what
-// runs once per CTA costs its instruction fetches more than its work.
+// Walks the segments of a CTA's range of the line in order: the producer does,
+// from the first one on (g, when next is called first), and hands them on.
 struct Walk {
   int pos, end, per;
   int first_cta, last_cta;  // of the line
-  const Segment *first;
   bool fresh, narrow;
-  __device__ __forceinline__ Walk(const Line &line, const Segment *first_) : first(first_), fresh(true), narrow(line.narrow) {
+  __device__ __forceinline__ explicit Walk(const Line &line) : fresh(true), narrow(line.narrow) {
     per = cost_per_cta(line.total, line.n_ctas);
     first_cta = line.first_cta;
     last_cta = line.first_cta + line.n_ctas - 1;
@@ -309,7 +309,6 @@ struct Walk {
   __device__ __forceinline__ bool next(const PagedAttnParams &p, Segment &g) {
     if (pos >= end) return false;
     if (fresh) {
-      g = *first;
       fresh = false;
       pos = g.next;
       if (g.j1 > g.j0) return true;
@@ -345,11 +344,47 @@ struct Walk {
   __device__ __forceinline__ int ends_in(const PagedAttnParams &p, const Segment &g) const {
     return min(first_cta + (g.next - (g.j1 + kItemCost) + item_tiles(p, g.s, g.rb) + kItemCost - 1) / per, last_cta);
   }
-  // Key tiles of segment g that query tile t goes through, counted from g.j0.
+  // Key tiles of segment g that query tile t (of the wide form) goes through, counted from g.j0.
   static __device__ __forceinline__ int tiles(const PagedAttnParams &p, const Segment &g, int t) {
     const int first = (2 * g.rb + t) * p.tok;
     if (first >= g.s.q_len) return 0;
     return max(0, min(g.j1, tiles_seen(p, g.s, first + p.tok)) - g.j0);
+  }
+};
+
+// The segments on their way from the producer to the other roles, in four places
+// of shared memory, each with a barrier for "there" and one for "read by every
+// warp". (When every role walked by itself that was 1,300 to 3,500 clocks of each
+// item in each role.) A segment without tiles ends the CTA's range.
+struct Items {
+  Segment *places;
+  uint32_t bar;  // four for "there", four for "read"
+  int i;
+  __device__ __forceinline__ Items(Segment *places_, uint32_t bar_) : places(places_), bar(bar_), i(0) {}
+  __device__ __forceinline__ uint32_t there() const { return bar + 8u * static_cast<uint32_t>(i & 3); }
+  // The next segment, by a whole warp of a role; false at the end and after a timeout.
+  __device__ __forceinline__ bool wait(volatile int *abort_flag, int *err) const {
+    return __all_sync(0xffffffffu, mbar_wait(there(), static_cast<uint32_t>(i >> 2) & 1u, abort_flag, err)) &&
+           places[i & 3].j1 > places[i & 3].j0;
+  }
+  __device__ __forceinline__ const Segment &get() const { return places[i & 3]; }
+  // This warp has read it.
+  __device__ __forceinline__ void release() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(there() + 32u);
+    ++i;
+  }
+  // The producer warp hands on g.
+  __device__ __forceinline__ bool put(const Segment &g, volatile int *abort_flag, int *err) {
+    if (i >= 4 && !__all_sync(0xffffffffu, mbar_wait(there() + 32u, static_cast<uint32_t>((i >> 2) - 1) & 1u, abort_flag, err)))
+      return false;
+    if ((threadIdx.x & 31) == 0) {
+      places[i & 3] = g;
+      mbar_arrive(there());
+    }
+    __syncwarp();
+    ++i;
+    return true;
   }
 };
 
@@ -515,14 +550,14 @@ __device__ __forceinline__ uint32_t o_column(uint32_t tmem, int t) { return tmem
 // Producer: the whole warp. sQ [tile][col block][128 rows][128 B], sRing
 // [slot][col block][128 rows][128 B].
 template <int D>
-__device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk walk, const CUtensorMap *tm_q,
+__device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk walk, Segment g, Items items,
+                                           const CUtensorMap *tm_q,
                                            const CUtensorMap *tm_k, const CUtensorMap *tm_v, uint32_t bar0, uint32_t sQ,
                                            uint32_t sRing, int first_entry, volatile int *abort_flag, int *err) {
   using C = Cfg<D>;
   using W = WideBars<D>;
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
-  Segment g;
   // K and V are read again by the other row blocks of their sequence, Q is not
   const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
   const int page_size = 1 << p.page_log2;
@@ -538,6 +573,8 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
   // the item that this CTA begins and another one ends, for the merge
   int4 cut = make_int4(0, 0, 0, 0);
   while (ok && walk.next(p, g)) {
+    g.ring = c;
+    if (!items.put(g, abort_flag, err)) break;
     if (g.j0 == 0 && g.slot >= 0)
       cut = make_int4(g.s.q0 + g.rb * 2 * p.tok, min(2 * p.tok, g.s.q_len - g.rb * 2 * p.tok) * p.G, g.h, walk.ends_in(p, g));
     const int n_max = uniform(max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1)));
@@ -570,6 +607,8 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
       }
     }
   }
+  g.j0 = g.j1 = 0;
+  items.put(g, abort_flag, err);
   if (lane == 0) p.cuts[blockIdx.x] = cut;
   if (lane == 0) {  // every copy must have landed before the CTA may exit
     if (nq > 0) mbar_drain(bar(W::kQFull), (nq - 1) & 1, err);
@@ -585,7 +624,7 @@ __device__ __forceinline__ void wide_producer(const PagedAttnParams &p, Walk wal
 // longer than the MMA itself; both issuers take turns, so that was the time of a
 // key tile.)
 template <int D>
-__device__ __forceinline__ void wide_issuer(const PagedAttnParams &p, Walk walk, int t_in, uint32_t bar0, uint32_t sQ,
+__device__ __forceinline__ void wide_issuer(const PagedAttnParams &p, Items items, int t_in, uint32_t bar0, uint32_t sQ,
                                             uint32_t sRing, uint32_t tmem_in, volatile int *turn,
                                             volatile int *abort_flag, int *err) {
   using C = Cfg<D>;
@@ -597,27 +636,25 @@ __device__ __forceinline__ void wide_issuer(const PagedAttnParams &p, Walk walk,
   const bool leader = elect_one();
   const int t = uniform(t_in);
   const uint32_t tmem = uniform(tmem_in);
-  Segment g;
   constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, D, true);
   const uint64_t qd = sw128_desc(sQ + t * C::kTileBytes, 16, 1024);
   const uint32_t s_col = s_column(tmem, t), o_col = o_column(tmem, t);
-  uint32_t c = 0, nq = 0, steps = 0;
+  uint32_t nq = 0, steps = 0;
   int base = 0;
   bool ok = true;
-  while (ok && walk.next(p, g)) {
-    const int nt = uniform(Walk::tiles(p, g, t));
-    const int n_max = uniform(max(Walk::tiles(p, g, 0), Walk::tiles(p, g, 1)));
+  while (ok && items.wait(abort_flag, err)) {
+    const int n0 = uniform(Walk::tiles(p, items.get(), 0)), n1 = uniform(Walk::tiles(p, items.get(), 1));
+    const uint32_t c = uniform(items.get().ring);
+    items.release();
+    const int nt = t == 0 ? n0 : n1, n_max = max(n0, n1);
     // tile 1 has nothing to do: its issuer only gives Q back, and tile 0's
     // goes on without taking turns and releases each slot for both
-    const bool single = uniform(Walk::tiles(p, g, 1)) == 0;
+    const bool single = n1 == 0;
     if (!wait(W::kQFull, nq & 1)) break;
     ++nq;
     if (nt == 0 && leader) mma_commit(bar(W::kQEmpty));
     __syncwarp();
-    if (single && t == 1) {
-      c += 2 * n_max;
-      continue;
-    }
+    if (single && t == 1) continue;
     for (int j = 0; ok && j <= n_max; ++j) {
       const uint32_t cK = c + 2 * j, cV = c + 2 * j - 1;  // ring positions of K_j and V_{j-1}
       const uint32_t sK = cK % C::kStages, sV = cV % C::kStages;
@@ -683,7 +720,6 @@ __device__ __forceinline__ void wide_issuer(const PagedAttnParams &p, Walk walk,
       }
       __syncwarp();
     }
-    c += 2 * n_max;
     steps += nt;
     if (!single) base += 2 * (n_max + 1);
   }
@@ -694,19 +730,7 @@ __device__ __forceinline__ void wide_issuer(const PagedAttnParams &p, Walk walk,
   __syncwarp();
 }
 
-// What a softmax warp knows of its walk, in shared memory: it has no registers to
-// spare for it while it goes over a tile's scores (with the walk in registers the
-// main loop spilled, 15 % of the time of a long causal prompt).
-struct WarpWalk {
-  Walk walk;
-  Segment seg;
-  bool more;
-  int ring;  // ring position of the segment's first K tile
-};
-constexpr int kStageBytes = 2560;  // 32 rows of a warp's epilogue, 80 bytes apart
-constexpr int kWarpBytes = 2688;   // and its WarpWalk
-static_assert(sizeof(Segment) <= 48, "the first segment's place");
-static_assert(kStageBytes + sizeof(WarpWalk) <= kWarpBytes, "a softmax warp's shared memory");
+constexpr int kStageBytes = 2560;  // of a softmax warp's epilogue: 32 rows, 80 bytes apart
 
 // x, in a way that nothing computed from it moves ahead of this place: what the
 // ends of a segment need must not sit in registers through its main loop.
@@ -716,10 +740,12 @@ __device__ __forceinline__ int hidden(int x) {
 }
 
 // Softmax warpgroup of query tile t: a thread has one row (TMEM lane = tile row),
-// the dense forward's scheme. own: this warp's kWarpBytes of shared memory.
+// the dense forward's scheme. It reads its segment where the producer put it (with
+// it in registers the main loop spilled, 15 % of the time of a long causal
+// prompt). stage_in: this warp's kStageBytes of shared memory.
 template <int D>
-__device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Walk &walk0, int t, uint32_t bar0,
-                                             uint32_t sRing, uint32_t tmem, uint8_t *own, volatile int *abort_flag,
+__device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, Items items, int t, uint32_t bar0,
+                                             uint32_t sRing, uint32_t tmem, uint32_t stage_in, volatile int *abort_flag,
                                              int *err) {
   using C = Cfg<D>;
   using W = WideBars<D>;
@@ -728,32 +754,26 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
   const uint32_t bar_t = bar0 + 8u * t;
   const uint32_t lane_off = static_cast<uint32_t>(r & ~31) << 16;
   const uint32_t s_addr = s_column(tmem, t) + lane_off, o_addr = o_column(tmem, t) + lane_off;
-  WarpWalk &ww = *reinterpret_cast<WarpWalk *>(own + kStageBytes);
-  if (lane == 0) {
-    ww.walk = walk0;
-    ww.ring = 0;
-    ww.more = ww.walk.next(p, ww.seg);
-  }
-  __syncwarp();
   uint32_t steps = 0;  // key tiles of this query tile so far
   uint32_t u = 0;      // segments in which it had any
-  while (ww.more) {
-    const int n = Walk::tiles(p, ww.seg, t);
+  while (items.wait(abort_flag, err)) {
+    const Segment &seg = items.get();
+    const int n = Walk::tiles(p, seg, t);
     int first_key, row_rel, cut_from, tail_from;
     bool row_valid, holes;
     {
-      const int first = (2 * ww.seg.rb + t) * p.tok;  // the tile's first token within the sequence
-      const int tok = hidden(r) / p.G, kv_len = ww.seg.s.kv_len;
-      row_valid = r < p.tok * p.G && first + tok < ww.seg.s.q_len;
+      const int first = (2 * seg.rb + t) * p.tok;  // the tile's first token within the sequence
+      const int tok = hidden(r) / p.G, kv_len = seg.s.kv_len;
+      row_valid = r < p.tok * p.G && first + tok < seg.s.q_len;
       // last key of the tile's first token, and of this row (rows of no token --
       // zeros, or other sequences' rows -- see every key: nothing of them is written)
-      const int tile_last = p.causal ? kv_len - ww.seg.s.q_len + first : kv_len - 1;
+      const int tile_last = p.causal ? kv_len - seg.s.q_len + first : kv_len - 1;
       const int row_last = row_valid && p.causal ? min(tile_last + tok, kv_len - 1) : kv_len - 1;
-      first_key = ww.seg.j0 * kRowsPerTile;
+      first_key = seg.j0 * kRowsPerTile;
       row_rel = row_last - first_key;
       cut_from = (tile_last + 1 - first_key) >> 7;   // the first tile of which some row does not see all keys
       tail_from = (kv_len - first_key) >> 7;         // the tile that the sequence ends in
-      holes = n > 0 && pages_missing(p, ww.seg);     // pages have to be looked up tile by tile
+      holes = n > 0 && pages_missing(p, seg);     // pages have to be looked up tile by tile
     }
     const bool warp_valid = __any_sync(0xffffffffu, row_valid);
     const float c2 = p.scale_log2;
@@ -761,7 +781,7 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const unsigned there =
-          holes ? pages_there(p, page_row(p, ww.seg), ww.seg.s.kv_len, ww.seg.j0 + j) : 0xffffffffu;
+          holes ? pages_there(p, page_row(p, seg), seg.s.kv_len, seg.j0 + j) : 0xffffffffu;
       ok = __all_sync(0xffffffffu, mbar_wait(bar_t + 8u * W::kSFull, (steps + j) & 1u, abort_flag, err));
       if (!ok) break;
       tc_fence_after();
@@ -823,8 +843,8 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
         tmem_st_wait();
       }
       if (j >= tail_from) {
-        const int cv = ww.ring + 2 * j + 1, slot = cv % C::kStages;  // ring position of the V tile
-        ok = clear_tail<D>(ww.seg.s.kv_len - first_key - j * kRowsPerTile, sRing + slot * C::kTileBytes,
+        const int cv = seg.ring + 2 * j + 1, slot = cv % C::kStages;  // ring position of the V tile
+        ok = clear_tail<D>(seg.s.kv_len - first_key - j * kRowsPerTile, sRing + slot * C::kTileBytes,
                            bar0 + 8u * (W::kFull + slot), (cv / C::kStages) & 1, abort_flag, err);
         if (!ok) break;
       }
@@ -832,15 +852,10 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_t + 8u * W::kPFull);  // one arrival per warp
     }
-    // what the epilogue needs of the segment; then the next one, while the last product runs
-    const int slot = ww.seg.slot, h = ww.seg.h, q0 = ww.seg.s.q0 + (2 * ww.seg.rb + t) * p.tok;
+    // what the epilogue needs of the segment
+    const int slot = seg.slot, h = seg.h, q0 = seg.s.q0 + (2 * seg.rb + t) * p.tok;
     steps += n;
-    __syncwarp();
-    if (lane == 0) {
-      ww.ring += 2 * max(Walk::tiles(p, ww.seg, 0), Walk::tiles(p, ww.seg, 1));
-      ww.more = ww.walk.next(p, ww.seg);
-    }
-    __syncwarp();
+    items.release();
     bool have_o = false;
     if (ok && n > 0) {
       have_o = __all_sync(0xffffffffu, mbar_wait(bar_t + 8u * W::kOFull, u & 1u, abort_flag, err));
@@ -858,7 +873,7 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, const Wal
     // bytes at a time, cost twice the sectors and 10,000 clocks a segment; this
     // 4,500 to 7,500). `stage`: 32 rows of this warp, 80 bytes apart.
     const int ln = hidden(lane), rr = hidden(r);
-    const uint32_t stage = smem_addr(own), mine = stage + ln * 80u;
+    const uint32_t stage = stage_in, mine = stage + ln * 80u;
     const int sub = ln >> 2, quad = ln & 3;
     long long off;  // this lane's row in the output, elements
     if (slot >= 0) {
@@ -954,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   using L = Narrow<D>;
   using W = WideBars<D>;
-  static_assert(L::kAreaBytes <= C::kAreaBytes && L::kNumBarriers <= C::kMaxBarriers && W::kMmaDone < C::kMaxBarriers,
+  static_assert(L::kAreaBytes <= C::kAreaBytes && L::kNumBarriers <= C::kItemBarrier && W::kMmaDone < C::kItemBarrier,
                 "shared memory layout");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem =
@@ -963,9 +978,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kMaxBarriers);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *turn = reinterpret_cast<volatile int *>(tmem_slot + 2);  // next MMA burst slot (wide)
-  int *warp_sums = reinterpret_cast<int *>(tmem_slot + 4);
-  Segment *first = reinterpret_cast<Segment *>(warp_sums + 36);
-  float *red = reinterpret_cast<float *>(warp_sums + 48);
+  Segment *places = reinterpret_cast<Segment *>(tmem_slot + 4);
+  float *red = reinterpret_cast<float *>(places + 4);
+  int *warp_sums = reinterpret_cast<int *>(red);
   int *prefix = reinterpret_cast<int *>(smem + C::kPrefixAt);
   const uint32_t bar0 = smem_addr(bars), base = smem_addr(smem);
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -987,17 +1002,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Line line = prefix_costs(p, prefix, warp_sums);
   const bool narrow = line.narrow;
   const L sh(line.rows, p.G);
-  const Walk walk(line, first);
+  const Walk walk(line);
+  const Items items(places, bar(C::kItemBarrier));
+  Segment first = {};    // the producer's
   int first_entry = -1;  // the producer's lanes: the first pages
   if (warp == kTmaWarp && walk.pos < walk.end) {
-    Segment g;
-    const Place at = place_of(p, prefix, walk.pos, g.s);
-    g.b = at.b;
-    g.h = at.h;
-    g.rbs = row_blocks(p, g.s);
-    walk.make(p, at.rb, at.r, g);
-    first_entry = window_entry(p, page_row(p, g), g.s.kv_len, first_page(p, g.j0));
-    if (lane == 0) *first = g;
+    const Place at = place_of(p, prefix, walk.pos, first.s);
+    first.b = at.b;
+    first.h = at.h;
+    first.rbs = row_blocks(p, first.s);
+    walk.make(p, at.rb, at.r, first);
+    first_entry = window_entry(p, page_row(p, first), first.s.kv_len, first_page(p, first.j0));
   }
   if (warp == kMmaWarp1) {
     // a barrier a lane (one thread for all of them: 1,400 clocks)
@@ -1011,6 +1026,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_init(bar(i), arrivals);
     }
+    // read by the issuer(s) and the softmax warps
+    if (lane < 8) mbar_init(bar(C::kItemBarrier + lane), lane < 4 ? 1 : (narrow ? 1 + 4 * sh.groups : 10));
     if (lane == 0) {
       *abort_flag = failed;
       *turn = 0;
@@ -1038,25 +1055,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // nothing
   } else if (narrow) {
     if (warp == kTmaWarp) {
-      narrow_producer<D>(p, sh, walk, &tm_q.narrow[sh.N == 16 ? 0 : (sh.N == 32 ? 1 : 2)], &tm_k, &tm_v, bar0, base,
+      narrow_producer<D>(p, sh, walk, first, items, &tm_q.narrow[sh.N == 16 ? 0 : (sh.N == 32 ? 1 : 2)], &tm_k, &tm_v, bar0, base,
                          first_entry, abort_flag, err);
     } else if (warp == kMmaWarp) {
-      narrow_issuer<D>(p, sh, walk, bar0, base, tmem, abort_flag, err);
+      narrow_issuer<D>(p, sh, items, bar0, base, tmem, abort_flag, err);
     } else if (warp < 4 * sh.groups) {
       if (sh.N == 64)
-        narrow_softmax<D, 32>(p, sh, walk, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 6 * 32, abort_flag, err);
+        narrow_softmax<D, 32>(p, sh, items, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 6 * 32, abort_flag, err);
       else
-        narrow_softmax<D, 16>(p, sh, walk, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 6 * 32, abort_flag, err);
+        narrow_softmax<D, 16>(p, sh, items, warp >> 2, bar0, base, tmem, red + (warp >> 2) * 6 * 32, abort_flag, err);
     }
   } else {
     const uint32_t sQ = base, sRing = base + 2 * C::kTileBytes;
     if (warp == kTmaWarp) {
-      wide_producer<D>(p, walk, &tm_q.wide, &tm_k, &tm_v, bar0, sQ, sRing, first_entry, abort_flag, err);
+      wide_producer<D>(p, walk, first, items, &tm_q.wide, &tm_k, &tm_v, bar0, sQ, sRing, first_entry, abort_flag, err);
     } else if (warp == kMmaWarp || warp == kMmaWarp1) {
-      wide_issuer<D>(p, walk, warp == kMmaWarp ? 0 : 1, bar0, sQ, sRing, tmem, turn, abort_flag, err);
+      wide_issuer<D>(p, items, warp == kMmaWarp ? 0 : 1, bar0, sQ, sRing, tmem, turn, abort_flag, err);
     } else {
-      wide_softmax<D>(p, walk, warp >> 2, bar0, sRing, tmem, smem + 2 * C::kTileBytes + C::kStages * C::kTileBytes + warp * kWarpBytes,
-                      abort_flag, err);
+      wide_softmax<D>(p, items, warp >> 2, bar0, sRing, tmem, sRing + C::kStages * C::kTileBytes + warp * kStageBytes, abort_flag,
+                      err);
     }
   }
 

@@ -71,7 +71,7 @@ __device__ __forceinline__ uint32_t idesc_narrow(int N, bool pv) {
 
 // Producer: the whole warp.
 template <int D>
-__device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
+__device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk, Segment g, Items items,
                                              const CUtensorMap *tm_q, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
                                              uint32_t bar0, uint32_t smem, int first_entry, volatile int *abort_flag,
                                              int *err) {
@@ -92,9 +92,10 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
   long long fills = 0;
   int nq = 0, q_loads = 0;
   bool ok = true;
-  Segment g;
   int4 cut = make_int4(0, 0, 0, 0);
   while (ok && walk.next(p, g)) {
+    g.ring = static_cast<int>(fills);
+    if (!items.put(g, abort_flag, err)) break;
     if (g.j0 == 0 && g.slot >= 0) cut = make_int4(g.s.q0, g.s.q_len * p.G, g.h, walk.ends_in(p, g));
     const int j0 = uniform(g.j0), n = uniform(g.j1) - j0, head = uniform(g.h);
     PageWindow pages(p, g, nq == 0, first_entry);
@@ -132,6 +133,8 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
     }
     ++nq;
   }
+  g.j0 = g.j1 = 0;
+  items.put(g, abort_flag, err);
   if (lane == 0) {
     p.cuts[blockIdx.x] = cut;
     // every copy must have landed before the CTA may exit
@@ -147,7 +150,7 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
 // code of a single thread it took about 95 clocks an MMA to bring the operands
 // into uniform registers, 1,520 to 1,800 a tile: more than the MMAs.)
 template <int D>
-__device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk, uint32_t bar0,
+__device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Narrow<D> &sh, Items items, uint32_t bar0,
                                               uint32_t smem, uint32_t tmem_in, volatile int *abort_flag, int *err) {
   using C = Narrow<D>;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -165,9 +168,9 @@ __device__ __forceinline__ void narrow_issuer(const PagedAttnParams &p, const Na
   uint32_t step = 0;  // key tiles so far
   int nq = 0;
   bool ok = true;
-  Segment g;
-  while (ok && walk.next(p, g)) {
-    const int n = uniform(g.j1 - g.j0);
+  while (ok && items.wait(abort_flag, err)) {
+    const int n = uniform(items.get().j1 - items.get().j0);
+    items.release();
     const int qb = nq & (q_bufs - 1);
     if (!wait(C::kQFull + qb, (q_bufs == 2 ? nq >> 1 : nq) & 1)) break;
     ++nq;
@@ -258,7 +261,7 @@ constexpr float kNoReference = -3.402823466e38f;
 // floats of shared memory, `gi` its number. Every warp goes through the same
 // barriers whatever fails: a wait that runs out is carried to the next vote.
 template <int D, int C>
-__device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const Narrow<D> &sh, Walk walk,
+__device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const Narrow<D> &sh, Items items,
                                             int gi, uint32_t bar0, uint32_t smem, uint32_t tmem, float *red,
                                             volatile int *abort_flag, int *err) {
   using L = Narrow<D>;
@@ -277,8 +280,9 @@ __device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const N
   float *ref = red + 4 * C, *factor = red + 5 * C;  // references of the columns; a factor for each
   RingPos k{0, 0};
   uint32_t step = 0;
-  Segment g;
-  while (walk.next(p, g)) {
+  while (items.wait(abort_flag, err)) {
+    const Segment g = items.get();
+    items.release();
     const int n = g.j1 - g.j0, rows = g.s.q_len * p.G;
     const int first_last = p.causal ? g.s.kv_len - g.s.q_len : g.s.kv_len - 1;  // last key of the first token
     const int *table = page_row(p, g);
