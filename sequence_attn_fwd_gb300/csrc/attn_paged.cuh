@@ -26,7 +26,7 @@
 // keys a page cost no more than 128 (319 us against 318 for the batch below).
 //
 // Measured (GB300): 1,024 new tokens behind 65,536 keys, 32 heads over 8 KV heads
-// of 128, 0.78 ms = 1,420 TFLOP/s, 3,000 clocks a pair of tiles (the dense
+// of 128, 0.76 ms = 1,450 TFLOP/s, 3,000 clocks a pair of tiles (the dense
 // forward's share; the tensor pipe's own time is 2,048); six sequences of up to
 // 600 new tokens behind up to 12,400 keys 162 us, and 11 more for the merge: the
 // tiles at that rate, 12,000 clocks until the first scores of a CTA and about as
@@ -55,8 +55,9 @@ struct Cfg {
   static constexpr int kNumBarriers = 2 + 2 * kStages + 7;
   // tiles of the wide form (Q, ring, epilogue) or of the narrow one (ring, P, Q), then
   // barriers, three words, four segments, the narrow form's reductions (before
-  // them, in the same place, the sums over warps). The prefix sums over the sequences are needed before the tiles
-  // arrive only: they lie where the ring of either form will be.
+  // them, in the same place, the sums over warps). The prefix sums over the
+  // sequences are needed before the tiles arrive only: they lie where the ring of
+  // either form will be.
   static constexpr int kAreaBytes = 196608 + kRowsPerTile * 128 + 64 * D * 2;
   static_assert(2 * kTileBytes + kStages * kTileBytes + 8 * 2560 <= kAreaBytes, "wide layout");
   static constexpr int kItemBarrier = 2 * (196608 / kTileBytes) + 11;  // behind those of either form
