@@ -96,7 +96,7 @@ __device__ __forceinline__ void narrow_producer(const PagedAttnParams &p, const 
   while (ok && walk.next(p, g)) {
     g.ring = static_cast<int>(fills);
     if (!items.put(g, abort_flag, err)) break;
-    if (g.j0 == 0 && g.slot >= 0) cut = make_int4(g.s.q0, g.s.q_len * p.G, g.h, walk.ends_in(p, g));
+    if (g.j0 == 0 && g.slot >= 0) cut = make_int4(g.s.q0, min(g.s.q_len * p.G, kNarrowRows), g.h, walk.ends_in(p, g));
     const int j0 = uniform(g.j0), n = uniform(g.j1) - j0, head = uniform(g.h);
     PageWindow pages(p, g, nq == 0, first_entry);
     const int qb = nq % sh.q_bufs, use = nq / sh.q_bufs;
