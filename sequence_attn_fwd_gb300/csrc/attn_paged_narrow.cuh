@@ -1,5 +1,5 @@
-// The narrow form of the paged attention (included by attn_paged.cuh): every
-// sequence of the call has at most 64 rows per KV head (single tokens, drafts).
+// The narrow form of the paged attention (included by attn_paged.cuh): sequences
+// of at most 64 rows per KV head (single tokens, drafts).
 //
 // The cost is reading K and V, and what bounds that is bytes in flight: with
 // 96, 128 KB of tiles per SM a batch of 64 sequences (8 KV heads of 128, 2.1 GB
@@ -43,8 +43,6 @@ struct Narrow {
   }
   // shared memory behind the 1024-byte aligned start: ring, P, Q
   __device__ __forceinline__ int p_at() const { return stages * kTileBytes; }
-  // P buffer b: its first key's first row
-  __device__ __forceinline__ int p_buf(uint32_t b) const { return p_at() + static_cast<int>(b) * (N == 64 ? kPBytes : 2 * N); }
   __device__ __forceinline__ int q_at() const { return p_at() + (N == 64 ? 2 : 1) * kPBytes; }
   __device__ __forceinline__ int q_bytes() const { return N * D * 2; }
   static constexpr int kAreaBytes = 196608 + kPBytes + 2 * 32 * D * 2;
