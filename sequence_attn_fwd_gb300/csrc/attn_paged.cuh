@@ -812,12 +812,16 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, Items ite
         uint32_t sr[128];
         load_scores(sr);
         float rowsum;
-        if (j == 0) m = row_max(reinterpret_cast<const float *>(sr)) * c2;
+        // A row that has seen no key yet takes this tile's maximum as its reference:
+        // in the first tile, and behind tiles whose pages are all missing. (2^s of
+        // scores left without a reference is 0 below -126 and would lose their
+        // keys.) O is 0 or not yet written then, and needs no factor.
+        if (m == -INFINITY) m = row_max(reinterpret_cast<const float *>(sr)) * c2;
         rowsum = exp_row<false, 0>(reinterpret_cast<const float *>(sr), c2, (m == -INFINITY) ? 0.f : m, pk);
         if (j > 0) {
           // as in the dense forward: the reference moves, and O with it, only
-          // when the tile's P would sum to more than 2^8 or there is none yet
-          const bool big = row_valid && (!(rowsum <= kRescaleSum) || (m == -INFINITY && rowsum > 0.f));
+          // when the tile's P would sum to more than 2^8
+          const bool big = row_valid && !(rowsum <= kRescaleSum);
           if (__any_sync(0xffffffffu, big)) {
             float mx = -INFINITY;  // 32 columns at a time: few live registers
 #pragma unroll 1
