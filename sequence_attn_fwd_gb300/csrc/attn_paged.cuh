@@ -368,6 +368,12 @@ struct Items {
     return __all_sync(0xffffffffu, mbar_wait(there(), static_cast<uint32_t>(i >> 2) & 1u, abort_flag, err)) &&
            places[i & 3].j1 > places[i & 3].j0;
   }
+  // The same for the four warps of a role that meet at named barrier `id`: all go on
+  // or none does. (One alone may give up after an error elsewhere just before the
+  // producer hands the segment on; the others must not take it and wait for that one.)
+  __device__ __forceinline__ bool wait_together(int id, volatile int *abort_flag, int *err) const {
+    return named_bar_and(id, 128, wait(abort_flag, err));
+  }
   __device__ __forceinline__ const Segment &get() const { return places[i & 3]; }
   // This warp has read it.
   __device__ __forceinline__ void release() {

@@ -257,7 +257,8 @@ constexpr float kNoReference = -3.402823466e38f;
 // Softmax and epilogue of columns [col0, col0 + C) of S^T: one thread per key
 // (and, in the epilogue, per column of O). `red` is this warpgroup's 6 x C
 // floats of shared memory, `gi` its number. Every warp goes through the same
-// barriers whatever fails: a wait that runs out is carried to the next vote.
+// barriers whatever fails: a wait that runs out is carried to the next vote, the
+// wait for an item included.
 template <int D, int C>
 __device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const Narrow<D> &sh, Items items,
                                             int gi, uint32_t bar0, uint32_t smem, uint32_t tmem, float *red,
@@ -278,7 +279,7 @@ __device__ __forceinline__ void narrow_softmax(const PagedAttnParams &p, const N
   float *ref = red + 4 * C, *factor = red + 5 * C;  // references of the columns; a factor for each
   RingPos k{0, 0};
   uint32_t step = 0;
-  while (items.wait(abort_flag, err)) {
+  while (items.wait_together(id, abort_flag, err)) {
     const Segment g = items.get();
     items.release();
     const int n = g.j1 - g.j0, rows = g.s.q_len * p.G;
