@@ -137,6 +137,27 @@ int paged_append(const rope_rows *q, const rope_rows *k, const rope_rows *v, con
 #define PAGED_TOO_LONG 2  /* the row's table has no room */
 #define PAGED_IN_USE 3    /* the fork's target row holds tokens */
 
+/*
+ * A step after a refused request. Append and attention place a sequence's new
+ * tokens by counting back from kv_lens, which a refused request does not move: they
+ * would lie over keys that the row has already, in pages that it may share. Either
+ * leave the rows whose status is not 0 out of cu_seqlens (their ranges empty), or
+ * give the step's calls a guard: device int32 [4][B], zeros at first, written by
+ * these two calls only. Then the append drops the new tokens of a row that was
+ * refused room since its last append if they would lie over keys from before its
+ * requests (their q is still turned), and leaves in guard[3 B + b] the lengths to
+ * give the attention as kv_lens: 0 for such a row, whose tokens then see no key (O =
+ * 0, lse = -inf), else kv_lens[b]; of rows without new tokens, anything. A row that
+ * was granted one request and refused another may still bring the tokens that it was
+ * granted. With guard NULL these are the plain calls.
+ */
+int paged_reserve_guarded(int *page_table, long long table_stride, int *kv_lens, int *page_refs, const int *n_new,
+                          int *status, int *guard, int B, int max_pages, int n_pages, int page_size,
+                          attn_stream_t stream);
+int paged_append_guarded(const rope_rows *q, const rope_rows *k, const rope_rows *v, const paged_cache *cache,
+                         const int *positions, long long pos_axis, int n_axes, const double *inv_freq, const int *axes,
+                         int total, int interleaved, int *guard, attn_stream_t stream);
+
 /* A pool whose pages paged_fork, paged_copy and paged_compact move: n_layers
  * pools at layer_stride, pages page_stride apart, page_bytes each (all in bytes,
  * multiples of 16, base 16-byte aligned). */

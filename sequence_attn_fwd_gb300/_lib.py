@@ -19,7 +19,8 @@ EXPORTS = ["attn_fwd", "attn_partial", "lse_merge", "attn_query_device_error",
 
 # Every function include/seqattn_paged.h declares.
 PAGED_EXPORTS = ["attn_paged", "attn_paged_workspace_bytes", "rope_axes", "paged_append", "paged_reserve",
-                 "paged_free", "paged_fork", "paged_copy", "paged_compact", "paged_compact_workspace_bytes"]
+                 "paged_free", "paged_fork", "paged_copy", "paged_compact", "paged_compact_workspace_bytes",
+                 "paged_append_guarded", "paged_reserve_guarded"]
 
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED",
           3: "ATTN_ERR_CUDA", 4: "ATTN_ERR_TIMEOUT"}
@@ -98,6 +99,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.rope_axes.argtypes = [P, P, P, LL, LL, I, P, P, I, I, I, I, I, I, P]
     L.paged_append.argtypes = [P, P, P, P, P, LL, I, P, P, I, I, P]
     L.paged_reserve.argtypes = [P, LL, P, P, P, P, I, I, I, I, P]
+    L.paged_append_guarded.argtypes = [P, P, P, P, P, LL, I, P, P, I, I, P, P]
+    L.paged_reserve_guarded.argtypes = [P, LL, P, P, P, P, P, I, I, I, I, P]
     L.paged_free.argtypes = [P, LL, P, P, P, I, I, I, I, P]
     L.paged_fork.argtypes = [P, I, P, LL, P, P, P, P, P, I, I, I, I, I, P]
     L.paged_copy.argtypes = [P, I, P, P, I, I, P]

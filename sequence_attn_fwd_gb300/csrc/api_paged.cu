@@ -253,12 +253,19 @@ int rope_axes(const rope_rows *q, const rope_rows *k, const int *positions, long
 int paged_append(const rope_rows *q, const rope_rows *k, const rope_rows *v, const paged_cache *cache,
                  const int *positions, long long pos_axis, int n_axes, const double *inv_freq, const int *axes,
                  int total, int interleaved, attn_stream_t stream) {
+  return paged_append_guarded(q, k, v, cache, positions, pos_axis, n_axes, inv_freq, axes, total, interleaved, nullptr,
+                              stream);
+}
+
+int paged_append_guarded(const rope_rows *q, const rope_rows *k, const rope_rows *v, const paged_cache *cache,
+                         const int *positions, long long pos_axis, int n_axes, const double *inv_freq, const int *axes,
+                         int total, int interleaved, int *guard, attn_stream_t stream) {
   int st = check_cache(cache);
   if (st != ATTN_OK) return st;
   if (total < 0 || (interleaved != 0 && interleaved != 1)) return ATTN_ERR_INVALID_ARG;
   if (total > kMaxKeys) return ATTN_ERR_UNSUPPORTED;
   if (!k || !v || k->heads != cache->Hkv || v->heads != cache->Hkv) return ATTN_ERR_INVALID_ARG;
-  if (!positions && q && q->heads > 0) return ATTN_ERR_INVALID_ARG;
+  if ((!positions && q && q->heads > 0) || !aligned(guard, 4)) return ATTN_ERR_INVALID_ARG;
   seqattn::RopeTable tbl{};
   if (positions) {
     if (!aligned(positions, 4)) return ATTN_ERR_INVALID_ARG;
@@ -273,6 +280,7 @@ int paged_append(const rope_rows *q, const rope_rows *k, const rope_rows *v, con
   p.k = rows_of(k);
   p.v = rows_of(v);
   p.cache = view_of(cache);
+  p.guard = guard;
   p.positions = positions;
   p.pos_axis = pos_axis;
   p.B = 1;
@@ -282,15 +290,22 @@ int paged_append(const rope_rows *q, const rope_rows *k, const rope_rows *v, con
 
 int paged_reserve(int *page_table, long long table_stride, int *kv_lens, int *page_refs, const int *n_new, int *status,
                   int B, int max_pages, int n_pages, int page_size, attn_stream_t stream) {
+  return paged_reserve_guarded(page_table, table_stride, kv_lens, page_refs, n_new, status, nullptr, B, max_pages,
+                               n_pages, page_size, stream);
+}
+
+int paged_reserve_guarded(int *page_table, long long table_stride, int *kv_lens, int *page_refs, const int *n_new,
+                          int *status, int *guard, int B, int max_pages, int n_pages, int page_size,
+                          attn_stream_t stream) {
   int st = check_tables(page_table, table_stride, B, max_pages, n_pages);
   if (st == ATTN_OK) st = check_page_size(page_size, max_pages);
   if (st != ATTN_OK) return st;
   if (B == 0) return ATTN_OK;
   if (!kv_lens || !page_refs || !n_new || !status || !aligned(kv_lens, 4) || !aligned(page_refs, 4) ||
-      !aligned(n_new, 4) || !aligned(status, 4))
+      !aligned(n_new, 4) || !aligned(status, 4) || !aligned(guard, 4))
     return ATTN_ERR_INVALID_ARG;
   const seqattn::PageTables t{page_table, table_stride, kv_lens, page_refs, B, max_pages, n_pages, log2_of(page_size)};
-  return done(seqattn::launch_reserve(t, n_new, status, reinterpret_cast<cudaStream_t>(stream)));
+  return done(seqattn::launch_reserve(t, n_new, status, guard, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int paged_free(int *page_table, long long table_stride, int *kv_lens, int *page_refs, const int *rows, int n, int B,

@@ -122,6 +122,34 @@ struct PagedView {
   int B, n_pages, page_size, max_pages, Hkv;
 };
 
+// What a row's requests for room left for the step that follows them (null: no
+// row is guarded). A request that was refused does not move kv_lens, so that the
+// step's tokens, counted back from it, would lie over older keys.
+//   base   the row's length before its first request after its last append
+//   held   its length after the last one, plus 1, if one of them was refused, else 0
+//   open   its length after the last one, plus 1, until an append comes, then 0
+//   lens   what the attention of the step takes as its length, written by the append
+// A length that differs from `open` was changed otherwise (freed, forked): the next
+// request is a first one again; and one that differs from `held` is not guarded.
+struct RowGuard {
+  int *base, *held, *open, *lens;
+#ifdef __CUDACC__
+  __device__ __forceinline__ RowGuard(int *guard, int B)
+      : base(guard), held(guard + B), open(guard + 2 * B), lens(guard + 3 * B) {}
+  // Whether q_len new tokens of row b, which has kv_len keys, would lie over older ones.
+  __device__ __forceinline__ bool refuses(int b, int kv_len, int q_len) const {
+    return held[b] == kv_len + 1 && kv_len - q_len < base[b];
+  }
+  // After a request for tokens of row b, by one thread: its length before and after.
+  __device__ __forceinline__ void request(int b, int len, int after, bool refused) const {
+    const bool same = open[b] == len + 1;
+    if (!same) base[b] = len;
+    held[b] = refused || (same && held[b] != 0) ? after + 1 : 0;
+    open[b] = after + 1;
+  }
+#endif
+};
+
 // Attention of packed new tokens over a paged cache. The rows of a KV head are
 // numbered (token, query head of the group), group fastest; a 128-row tile has
 // `tok` whole tokens (tok * G <= 128), a work item two tiles.
@@ -165,6 +193,7 @@ struct RopeTable {
 struct RopeParams {
   RopeView q, k, v;        // v: appends only
   PagedView cache;         // appends only
+  int *guard;              // appends only: [4][B] or null, see RowGuard
   const int *positions;    // null: nothing is turned (appends only)
   long long pos_axis, pos_b;
   int B, S, inverse;       // appends: B = 1, S = the packed tokens
@@ -195,7 +224,7 @@ struct PoolList {
   int n, total_layers;
   PoolView pool[kMaxPools];
 };
-cudaError_t launch_reserve(const PageTables &t, const int *n_new, int *status, cudaStream_t stream);
+cudaError_t launch_reserve(const PageTables &t, const int *n_new, int *status, int *guard, cudaStream_t stream);
 cudaError_t launch_free(const PageTables &t, const PageList &rows, cudaStream_t stream);
 cudaError_t launch_fork(const PageTables &t, const PoolList &pools, const PageList &pairs, int *status,
                         cudaStream_t stream);

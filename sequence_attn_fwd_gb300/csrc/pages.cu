@@ -120,7 +120,7 @@ __device__ void scan_needs(int *prefix, int n, int *warp_sums) {
 // gives rank r to the row whose range holds it. A row that the pool cannot
 // serve whole (only the last one reached can have got some pages) gives them
 // back. Bound by latency: lengths and the first counts are loaded together.
-__global__ void __launch_bounds__(kPlanThreads) reserve_kernel(PageTables t, const int *n_new, int *status) {
+__global__ void __launch_bounds__(kPlanThreads) reserve_kernel(PageTables t, const int *n_new, int *status, int *guard) {
   __shared__ int prefix[kPagedMaxRows + 1];
   __shared__ int length[kPagedMaxRows];  // -1: the row's table has no room
   __shared__ int warp_sums[33];
@@ -154,7 +154,12 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(PageTables t, con
         *e = -1;
       }
     }
-    if (st == 0) t.kv_lens[b] = length[b] + max(n_new[b], 0);
+    const int asked = max(n_new[b], 0);
+    if (guard != nullptr && asked > 0) {
+      const int len = static_cast<int>(min(static_cast<long long>(max(t.kv_lens[b], 0)), room));
+      RowGuard(guard, t.B).request(b, len, st == 0 ? len + asked : len, st != 0);
+    }
+    if (st == 0) t.kv_lens[b] = length[b] + asked;
     status[b] = st;
   }
 }
@@ -395,8 +400,8 @@ int chunks_of(const PoolList &pools) {
 
 }  // namespace
 
-cudaError_t launch_reserve(const PageTables &t, const int *n_new, int *status, cudaStream_t stream) {
-  return launch_dependent(reserve_kernel, dim3(1), dim3(kPlanThreads), 0, stream, t, n_new, status);
+cudaError_t launch_reserve(const PageTables &t, const int *n_new, int *status, int *guard, cudaStream_t stream) {
+  return launch_dependent(reserve_kernel, dim3(1), dim3(kPlanThreads), 0, stream, t, n_new, status, guard);
 }
 
 cudaError_t launch_free(const PageTables &t, const PageList &rows, cudaStream_t stream) {

@@ -93,8 +93,10 @@ __device__ __forceinline__ int piece_at(int sl, int i) {
 }
 
 // The slot of token t of an append: its element offset in the pools, -1 if it has
-// none; *live: whether the token belongs to a sequence.
-__device__ __forceinline__ long long slot_of(const PagedView &c, long long t, long long n_tok, int D, bool *live) {
+// none; *live: whether the token belongs to a sequence. `one`: of the threads with
+// this token, the one that writes for a guarded row.
+__device__ __forceinline__ long long slot_of(const PagedView &c, int *guard, long long t, long long n_tok, int D,
+                                             bool one, bool *live) {
   int lo = 0, hi = c.B;  // the first sequence that ends behind t
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -108,6 +110,16 @@ __device__ __forceinline__ long long slot_of(const PagedView &c, long long t, lo
   len = len < 0 ? 0 : (len > max_keys ? max_keys : len);
   const long long end = c.cu_seqlens[lo + 1] < n_tok ? c.cu_seqlens[lo + 1] : n_tok;
   const long long slot = len - (end - t);
+  if (guard != nullptr) {
+    const RowGuard row(guard, c.B);
+    const int q0 = max(c.cu_seqlens[lo], 0);
+    const bool refused = row.refuses(lo, static_cast<int>(len), static_cast<int>(end) - q0);
+    if (one && t == q0) {
+      row.open[lo] = 0;
+      row.lens[lo] = refused ? 0 : static_cast<int>(len);
+    }
+    if (refused) return -1;
+  }
   if (slot < 0) return -1;
   const int page = c.page_table[lo * c.table_stride + slot / c.page_size];
   if (page < 0 || page >= c.n_pages) return -1;
@@ -130,7 +142,8 @@ __global__ void __launch_bounds__(kRopeThreads)
   if (t >= n_tok) return;
   const long long b = kAppend ? 0 : t / p.S, s = kAppend ? t : t - b * p.S;
   bool live = true;
-  const long long slot = kAppend ? slot_of(p.cache, t, n_tok, D, &live) : -1;
+  const bool one = blockIdx.y == 0 && sl == 0 && threadIdx.x < kSlices * kTok;
+  const long long slot = kAppend ? slot_of(p.cache, p.guard, t, n_tok, D, one, &live) : -1;
   float cn[8], sn[8];
   if (p.positions != nullptr) {
     const int *pos = p.positions + b * p.pos_b + s;

@@ -83,6 +83,16 @@ def _tables(page_table: torch.Tensor, kv_lens=None, page_refs=None):
     return B, W, sb if B > 1 else W
 
 
+def _guard(guard, B: int, used: list):
+    """The guard's address (it joins `used`), or None."""
+    if guard is None:
+        return None
+    if guard.dtype != _I32 or guard.shape != (4, B) or not guard.is_contiguous():
+        raise ValueError(f"guard must be contiguous int32 [4, {B}]")
+    used.append(guard)
+    return guard.data_ptr()
+
+
 def _distinct_memory(t: torch.Tensor, what: str) -> None:
     """Every dimension longer than one has a non-zero stride (no expanded output)."""
     if 0 in t.stride() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
@@ -269,13 +279,15 @@ def rope_axes_bwd(dq, dk, positions: torch.Tensor, inv_freq, axes, interleaved: 
 
 def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                  page_table: torch.Tensor, kv_lens: torch.Tensor, cu_seqlens: torch.Tensor, q=None, positions=None,
-                 inv_freq=None, axes=None, interleaved: bool = False, out_q=None):
+                 inv_freq=None, axes=None, interleaved: bool = False, out_q=None, guard: torch.Tensor | None = None):
     """Writes the new tokens' k, v bf16 [Hkv,total,D] into the last slots of their
     sequences (kv_lens counts them already). With positions (int32
     [n_axes,total], inv_freq and axes as for rope_axes) k is turned on the way,
     and q [Hq,total,D] into out_q (may be q), which is returned. Tokens whose slot
-    is on no page are dropped."""
-    view, dev, _, Hkv, D = _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens)
+    is on no page are dropped, and with a guard (that of the step's paged_reserve)
+    those of rows that were refused room, which would lie over older keys; guard[3]
+    then holds the lengths for the attention of the step, 0 for such a row."""
+    view, dev, B, Hkv, D = _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens)
     if k.dim() != 3:
         raise ValueError("expected k [Hkv, total, D]")
     if q is not None and positions is None:
@@ -305,10 +317,11 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         pos, pos_axis, n_axes = positions.data_ptr(), positions.stride(0), positions.shape[0]
         f, a = inv_freq.data_ptr(), axes.data_ptr()
         used.append(positions)
+    held = _guard(guard, B, used)
     _one_device("paged_append", *used)
-    _call(lib.paged_append, "paged_append", dev, vq, _ROWS.pack(k.data_ptr(), 0, 0, sk[0], sk[1], 0, 0, 0, Hkv),
+    _call(lib.paged_append_guarded, "paged_append", dev, vq, _ROWS.pack(k.data_ptr(), 0, 0, sk[0], sk[1], 0, 0, 0, Hkv),
           _ROWS.pack(v.data_ptr(), 0, 0, sv[0], sv[1], 0, 0, 0, Hkv), view, pos, pos_axis, n_axes, f, a, total,
-          1 if interleaved else 0)
+          1 if interleaved else 0, held)
     return out_q
 
 
@@ -333,19 +346,24 @@ def _pools(pools, n_pages: int):
 
 
 def paged_reserve(page_table: torch.Tensor, kv_lens: torch.Tensor, page_refs: torch.Tensor, n_new: torch.Tensor,
-                  page_size: int, status: torch.Tensor | None = None) -> torch.Tensor:
+                  page_size: int, status: torch.Tensor | None = None,
+                  guard: torch.Tensor | None = None) -> torch.Tensor:
     """Room for n_new (int32 [B], device) more tokens in every row of the table: the
     lowest free pages (page_refs 0) in the order of the rows; kv_lens grows by
     n_new. Returns status int32 [B]: 0, PAGED_NO_PAGES or PAGED_TOO_LONG (that row
-    unchanged)."""
+    unchanged: appended tokens would lie over the keys that it has, so it must bring
+    none, or the append gets the guard of this call too). guard: int32 [4, B] on the
+    device, zeros at first, then for paged_reserve and paged_append only."""
     B, W, row = _tables(page_table, kv_lens, page_refs)
     _ints(n_new, B, "n_new")
     if status is None:
         status = torch.empty(B, dtype=_I32, device=page_table.device)
     _ints(status, B, "status")
-    dev = _one_device("paged_reserve", page_table, kv_lens, page_refs, n_new, status)
-    _call(lib.paged_reserve, "paged_reserve", dev, page_table.data_ptr(), row, kv_lens.data_ptr(), page_refs.data_ptr(),
-          n_new.data_ptr(), status.data_ptr(), B, W, page_refs.numel(), int(page_size))
+    used = [page_table, kv_lens, page_refs, n_new, status]
+    held = _guard(guard, B, used)
+    dev = _one_device("paged_reserve", *used)
+    _call(lib.paged_reserve_guarded, "paged_reserve", dev, page_table.data_ptr(), row, kv_lens.data_ptr(),
+          page_refs.data_ptr(), n_new.data_ptr(), status.data_ptr(), held, B, W, page_refs.numel(), int(page_size))
     return status
 
 
@@ -425,8 +443,10 @@ class PagedCache:
     One serving step: reserve(n_new) once, then step(layer, ...) in every layer
     (append the new tokens, attend over the cache). fork / free / compact work on
     all layers at once. Rows without new tokens in a step have an empty range in
-    cu_seqlens. Everything runs on the current stream and can be captured (the
-    row lists of fork and free are then part of the graph)."""
+    cu_seqlens. A row that reserve refuses keeps its keys: the new tokens that a step
+    brings for it all the same are dropped and see nothing (O = 0, lse = -inf).
+    Everything runs on the current stream and can be captured (the row lists of fork
+    and free are then part of the graph)."""
 
     def __init__(self, n_pages: int, Hkv: int, D: int, rows: int, max_pages: int, page_size: int = 16, layers: int = 1,
                  plan: RopePlan | None = None, interleaved: bool = False, device=None):
@@ -437,10 +457,12 @@ class PagedCache:
         self.page_table = torch.full((rows, max_pages), -1, dtype=_I32, device=device)
         self.kv_lens = torch.zeros(rows, dtype=_I32, device=device)
         self.page_refs = torch.zeros(n_pages, dtype=_I32, device=device)
+        self.guard = torch.zeros((4, rows), dtype=_I32, device=device)  # what reserve leaves for the steps
+        self._step_lens = self.guard[3]
         self.page_size, self.plan, self.interleaved = page_size, plan, interleaved
 
     def reserve(self, n_new: torch.Tensor) -> torch.Tensor:
-        return paged_reserve(self.page_table, self.kv_lens, self.page_refs, n_new, self.page_size)
+        return paged_reserve(self.page_table, self.kv_lens, self.page_refs, n_new, self.page_size, guard=self.guard)
 
     def step(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
              positions: torch.Tensor | None = None, causal: bool = True, scale: float | None = None, workspace=None):
@@ -449,12 +471,13 @@ class PagedCache:
         pools = self.k_pages[layer], self.v_pages[layer]
         tables = self.page_table, self.kv_lens, cu_seqlens
         if self.plan is None:
-            paged_append(k, v, *pools, *tables)
+            paged_append(k, v, *pools, *tables, guard=self.guard)
         else:
             _require(positions is not None, "the cache turns its keys by their positions: pass them")
             q = paged_append(k, v, *pools, *tables, q=q, positions=positions, inv_freq=self.plan.inv_freq,
-                             axes=self.plan.axes, interleaved=self.interleaved)
-        return attn_paged(q, *pools, *tables, causal=causal, scale=scale, workspace=workspace)
+                             axes=self.plan.axes, interleaved=self.interleaved, guard=self.guard)
+        return attn_paged(q, *pools, self.page_table, self._step_lens, cu_seqlens, causal=causal, scale=scale,
+                          workspace=workspace)
 
     def fork(self, src, dst) -> torch.Tensor:
         return paged_fork((self.k_pages, self.v_pages), self.page_table, self.kv_lens, self.page_refs, src, dst)

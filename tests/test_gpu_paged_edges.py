@@ -59,3 +59,136 @@ def test_low_scores_behind_missing_pages_few_rows(sa):
     table[0, :100], table[1, :20], table[2, 500:2000] = -1, -1, -1
     got = sa.attn_paged(q, kp, vp, table, lens, cu)
     ref.check_attention(got, ref.attention(q, kp, vp, table, lens, cu, True, 1 / math.sqrt(128)))
+
+
+# ---------------------------------------------------------------------------- rows without room
+def filled_cache(sa, rows=4, n_pages=10, seed=1):
+    """Rows 0 and 1 hold 48 and 20 tokens (16 a page), row 2 is a fork of row 0 (every page shared); 5 pages are free."""
+    cache = sa.PagedCache(n_pages, 2, 64, rows=rows, max_pages=9, page_size=16, layers=2, plan=sa.RopePlan(64, (32,)))
+    for p in (cache.k_pages, cache.v_pages):
+        p.copy_(torch.randn(p.shape, generator=torch.Generator().manual_seed(seed)).to(BF))
+    assert cache.reserve(i32([48, 20] + [0] * (rows - 2))).tolist() == [0] * rows
+    assert cache.fork([0], [2]).tolist() == [0]
+    return cache
+
+
+def tokens(total, seed=2):
+    g = torch.Generator().manual_seed(seed)
+    q, k, v = (torch.randn((H, total, 64), generator=g).to(BF).cuda() for H in (4, 2, 2))
+    return q, k, v, torch.arange(total, dtype=I32, device="cuda")[None] + 60
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("n_new,why", [([200, 2, 1, 0], 2), ([96, 2, 1, 0], 1)])
+def test_a_row_without_room_keeps_its_keys(sa, n_new, why, captured):
+    """Row 0's request is refused (its table is too short, or the pool): its tokens are dropped and see nothing, the
+    keys that it and its fork hold stay as they are, and the rows that got room are served as if it were not there."""
+    cache, other = filled_cache(sa), filled_cache(sa)
+    cu = i32([0] + torch.tensor(n_new).cumsum(0).tolist())
+    q, k, v, pos = tokens(sum(n_new))
+    before = cache.k_pages.clone(), cache.v_pages.clone()
+    held = cache.page_table[0, :3].long()
+    n = i32(n_new)
+
+    def step(c, n, q, k, v, cu, pos):
+        """Both layers; each twice, as the second time writes what the first one wrote."""
+        status = c.reserve(n)
+        for layer in (0, 1, 0, 1):
+            o = c.step(layer, q, k, v, cu, pos)
+        return status, o
+
+    if captured:
+        warm = filled_cache(sa)
+        step(warm, n, q, k, v, cu, pos)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            status, (o, lse) = step(cache, n, q, k, v, cu, pos)
+        graph.replay()
+    else:
+        status, (o, lse) = step(cache, n, q, k, v, cu, pos)
+    got = status.tolist()
+    assert got[0] == why
+    for pool, old in zip((cache.k_pages, cache.v_pages), before):
+        assert torch.equal(pool[:, held], old[:, held])
+    a = n_new[0]
+    assert (o[:, :a] == 0).all() and torch.isneginf(lse[:, :a]).all()
+    # the same step without row 0's request, and without the rows that were refused with it
+    served = [0] + [m if s == 0 else 0 for m, s in zip(n_new[1:], got[1:])]
+    if why == 2:
+        assert served[1:] == n_new[1:]
+    keep = torch.cat([torch.arange(int(cu[b]), int(cu[b + 1])) for b in range(4) if served[b]] or [torch.zeros(0).long()])
+    if len(keep):
+        _, (wo, wl) = step(other, i32(served), *(t[:, keep].contiguous() for t in (q, k, v)),
+                           i32([0] + torch.tensor(served).cumsum(0).tolist()), pos[:, keep].contiguous())
+        assert torch.equal(o[:, keep], wo) and torch.equal(lse[:, keep], wl)
+        assert torch.equal(cache.k_pages, other.k_pages) and torch.equal(cache.v_pages, other.v_pages)
+    # a request that fits, afterwards, is served
+    n2 = i32([1, 0, 0, 0])
+    status, (o, lse) = step(cache, n2, q[:, :1], k[:, :1], v[:, :1], i32([0, 1, 1, 1, 1]), pos[:, :1])
+    assert status.tolist() == [0] * 4 and torch.isfinite(lse).all()
+    assert torch.equal(cache.v_pages[1, int(cache.page_table[0, 3]), :, 0], v[:, 0])
+
+
+def test_reserve_results_stay_apart_and_rows_may_change_between_steps(sa):
+    """Each reserve's answer is a tensor of its own; a table changed through the functions is served by the cache."""
+    cache = filled_cache(sa)
+    first = cache.reserve(i32([200, 1, 0, 0]))
+    second = cache.reserve(i32([0, 0, 0, 3]))
+    assert first.tolist() == [2, 0, 0, 0] and second.tolist() == [0] * 4
+    own = sa.PagedCache(12, 2, 64, rows=1, max_pages=9)
+    assert sa.paged_reserve(own.page_table, own.kv_lens, own.page_refs, i32([5]), 16).tolist() == [0]
+    q, k, v, _ = tokens(5)
+    o, lse = own.step(0, q, k, v, i32([0, 5]))
+    assert torch.isfinite(lse).all() and torch.equal(own.k_pages[0, 0, :, :5], k)
+
+
+def test_requests_between_two_steps(sa):
+    """A row that was granted tokens and refused more brings the granted ones; one that brings all keeps its keys."""
+    q, k, v, pos = tokens(60)
+    for bring, ok in ((3, True), (60, False)):
+        cache = filled_cache(sa)
+        held = cache.page_table[0, :3].long()
+        before = cache.k_pages[0, held].clone()
+        assert cache.reserve(i32([3, 0, 0, 0])).tolist() == [0] * 4
+        assert cache.reserve(i32([0, 0, 1, 0])).tolist() == [0] * 4  # another row's request in between
+        assert cache.reserve(i32([200, 0, 0, 0])).tolist() == [2, 0, 0, 0]
+        assert cache.reserve(i32([0, 2, 0, 0])).tolist() == [0] * 4
+        o, lse = cache.step(0, q[:, :bring], k[:, :bring], v[:, :bring], i32([0] + [bring] * 4), pos[:, :bring])
+        assert torch.equal(cache.k_pages[0, held], before)
+        assert torch.isfinite(lse).all() if ok else (torch.isneginf(lse).all() and (o == 0).all())
+
+
+def test_a_refused_row_starts_over(sa):
+    """Freed, forked into or asked again with success, a row is served as any other."""
+    q, k, v, pos = tokens(9)
+    cache = filled_cache(sa)
+    assert cache.reserve(i32([200, 0, 200, 0])).tolist() == [2, 0, 2, 0]
+    cache.free([0, 2])
+    assert cache.fork([1], [2]).tolist() == [0]
+    assert cache.reserve(i32([9, 0, 0, 0])).tolist() == [0] * 4  # shorter than it was when it was refused
+    o, lse = cache.step(0, q, k, v, i32([0, 9, 9, 9, 9]), pos)
+    assert torch.isfinite(lse).all() and torch.equal(cache.v_pages[0, int(cache.page_table[0, 0]), :, :9], v)
+    assert cache.reserve(i32([0, 0, 9, 0])).tolist() == [0] * 4
+    o, lse = cache.step(0, q, k, v, i32([0, 0, 0, 9, 9]), pos)
+    assert torch.isfinite(lse).all() and cache.kv_lens.tolist() == [9, 20, 29, 0]
+    assert cache.reserve(i32([0, 0, 200, 0])).tolist() == [0, 0, 2, 0]
+    assert cache.reserve(i32([0, 0, 2, 0])).tolist() == [0] * 4
+    o, lse = cache.step(0, q[:, :2], k[:, :2], v[:, :2], i32([0, 0, 0, 2, 2]), pos[:, :2])
+    assert torch.isfinite(lse).all() and cache.kv_lens[2] == 31
+
+
+def test_guarded_calls_of_a_caller_without_the_handle(sa):
+    """The functions on tensors of the caller's own, and without a guard the plain calls."""
+    cache = filled_cache(sa)
+    guard = torch.zeros((4, 4), dtype=I32, device="cuda")
+    t, pools = (cache.page_table, cache.kv_lens), (cache.k_pages[0], cache.v_pages[0])
+    q, k, v, _ = tokens(8)
+    before = cache.k_pages.clone()
+    cu = i32([0, 4, 8, 8, 8])
+    assert sa.paged_reserve(*t, cache.page_refs, i32([200, 4, 0, 0]), 16, guard=guard).tolist() == [2, 0, 0, 0]
+    sa.paged_append(k, v, *pools, *t, cu, guard=guard)
+    o, lse = sa.attn_paged(q, *pools, cache.page_table, guard[3], cu)
+    assert torch.isneginf(lse[:, :4]).all() and torch.isfinite(lse[:, 4:]).all()
+    assert torch.equal(cache.k_pages[:, cache.page_table[0, :3].long()], before[:, cache.page_table[0, :3].long()])
+    _, plain = sa.attn_paged(q, *pools, *t, cu)
+    assert torch.isfinite(plain).all() and torch.equal(plain[:, 4:], lse[:, 4:])

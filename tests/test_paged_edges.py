@@ -1,8 +1,15 @@
 """Checks of the serving side that need no GPU."""
+import ctypes
 import os
 import re
 
-from tests.test_abi import build_mod
+import pytest
+import torch
+
+from tests.test_abi import FAKE, build_mod
+from tests.test_paged_abi import lib, rows, view  # noqa: F401  (lib: the fixture)
+
+BF, I32 = torch.bfloat16, torch.int32
 
 
 def test_warps_that_share_a_barrier_leave_their_loop_together():
@@ -21,3 +28,20 @@ def test_warps_that_share_a_barrier_leave_their_loop_together():
     assert seen == 1  # the narrow form's softmax
     text = open(os.path.join(build_mod.CSRC, "attn_paged.cuh")).read()
     assert re.search(r"bool wait_together\(int id.*?\{\s*return named_bar_and\(id, 128, wait\(", text, flags=re.S)
+
+
+def test_guards_of_another_shape_or_type_are_refused(lib):  # noqa: F811
+    import sequence_attn_fwd_gb300 as sa
+
+    A = ctypes.addressof
+    c, r = view(), rows()
+    assert lib.paged_append_guarded(None, A(r), A(r), A(c), None, 0, 0, None, None, 9, 0, FAKE + 2, None) == 1
+    assert lib.paged_reserve_guarded(FAKE, 8, FAKE, FAKE, FAKE, FAKE, FAKE + 1, 4, 8, 16, 16, None) == 1
+    table, lens, refs = torch.zeros((2, 4), dtype=I32), torch.zeros(2, dtype=I32), torch.zeros(8, dtype=I32)
+    for bad in (torch.zeros((4, 3), dtype=I32), torch.zeros((3, 2), dtype=I32), torch.zeros((4, 2)),
+                torch.zeros((2, 4), dtype=I32).t()):
+        with pytest.raises(ValueError, match="guard"):
+            sa.paged_reserve(table, lens, refs, lens, 16, guard=bad)
+    kp, x = torch.zeros((8, 1, 16, 64), dtype=BF), torch.zeros((1, 5, 64), dtype=BF)
+    with pytest.raises(ValueError, match="CUDA"):  # the cache's tensors are looked at first
+        sa.paged_append(x, x, kp, kp, table, lens, torch.zeros(3, dtype=I32), guard=torch.zeros((4, 3), dtype=I32))
