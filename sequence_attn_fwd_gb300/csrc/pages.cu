@@ -178,6 +178,15 @@ __global__ void free_kernel(PageTables t, const __grid_constant__ PageList rows)
   if (threadIdx.x == 0) t.kv_lens[b] = 0;
 }
 
+// Whether a row of `len` tokens ends in a partly filled page that is there: the
+// one that a fork copies. (An evicted last page is shared like the others: as the
+// entry that it is.)
+__device__ __forceinline__ bool copies_last(const PageTables &t, const int *row, int len) {
+  if ((len & ((1 << t.page_log2) - 1)) == 0) return false;
+  const int e = row[len >> t.page_log2];
+  return e >= 0 && e < t.n_pages;
+}
+
 // Fork, first part (one CTA): checks the pairs and hands out the pages for
 // their partly filled last ones.
 __global__ void __launch_bounds__(kPlanThreads)
@@ -195,7 +204,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int dst = pairs.b[i];
     in_use = t.kv_lens[dst] != 0;
     const int len = static_cast<int>(min(static_cast<long long>(max(t.kv_lens[pairs.a[i]], 0)), room));
-    prefix[i] = !in_use && (len & ((1 << t.page_log2) - 1)) != 0;
+    prefix[i] = !in_use && copies_last(t, t.page_table + pairs.a[i] * t.table_stride, len);
     entry[i] = t.page_table + dst * t.table_stride + (len >> t.page_log2);
   }
   scan_needs(prefix, pairs.n, warp_sums);
@@ -252,10 +261,13 @@ __global__ void __launch_bounds__(kCopyThreads)
   if (status[i] != 0) return;
   const int room = static_cast<int>(min(static_cast<long long>(t.max_pages) << t.page_log2, 0x7fffffffll));
   const int len = min(max(t.kv_lens[src], 0), room);
-  const int whole = len >> t.page_log2;
-  const bool part = (len & ((1 << t.page_log2) - 1)) != 0;
   const int *from = t.page_table + src * t.table_stride;
   int *to = t.page_table + dst * t.table_stride;
+  const bool ends_inside = (len & ((1 << t.page_log2) - 1)) != 0;
+  const int last = ends_inside ? len >> t.page_log2 : 0;
+  const int page = ends_inside ? from[last] : -1, own = ends_inside ? to[last] : -1;  // both loads at once
+  const bool part = page >= 0 && page < t.n_pages;  // copies_last
+  const int whole = part ? last : pages_for(len, t.page_log2);  // entries that are shared
   if (blockIdx.x == 0) {
     for (int c = threadIdx.x; c < t.max_pages; c += kCopyThreads) {
       if (c < whole) {
@@ -269,8 +281,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     if (threadIdx.x == 0) t.kv_lens[dst] = len;
   } else if (part) {
     const int item = blockIdx.x - 1;
-    const int page = from[whole], own = to[whole];
-    if (page >= 0 && page < t.n_pages && own >= 0 && own < t.n_pages)
+    if (own >= 0 && own < t.n_pages)
       copy_page(pools, item / chunks, page, own, item % chunks);
   }
 }

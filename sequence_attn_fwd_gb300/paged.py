@@ -379,7 +379,7 @@ def paged_free(page_table: torch.Tensor, kv_lens: torch.Tensor, page_refs: torch
 def paged_fork(pools, page_table: torch.Tensor, kv_lens: torch.Tensor, page_refs: torch.Tensor, src, dst,
                status: torch.Tensor | None = None, page_size: int | None = None) -> torch.Tensor:
     """Empty rows dst become copies of rows src (src may repeat): whole pages shared,
-    a partly filled last page copied in every pool. Returns status int32 [n]: 0,
+    a partly filled last page copied in every pool (evicted pages stay evicted). Returns status int32 [n]: 0,
     PAGED_NO_PAGES or PAGED_IN_USE (that row unchanged)."""
     src, dst = _host_ints(src, "src"), _host_ints(dst, "dst")
     n = src.numel()

@@ -192,3 +192,45 @@ def test_guarded_calls_of_a_caller_without_the_handle(sa):
     assert torch.equal(cache.k_pages[:, cache.page_table[0, :3].long()], before[:, cache.page_table[0, :3].long()])
     _, plain = sa.attn_paged(q, *pools, *t, cu)
     assert torch.isfinite(plain).all() and torch.equal(plain[:, 4:], lse[:, 4:])
+
+
+# ---------------------------------------------------------------------------- forks of evicted pages
+@pytest.mark.parametrize("entry", [-1, 10 ** 6])
+def test_fork_of_a_row_whose_last_page_was_evicted(sa, entry):
+    """The child holds what its parent holds: no page where the parent has none, and none is taken from the pool."""
+    cache = filled_cache(sa)
+    cache.k_pages.fill_(math.nan)  # what a page that no one has written may hold
+    cache.v_pages.fill_(math.inf)
+    gone = int(cache.page_table[1, 1])
+    cache.page_table[1, 1] = entry  # the partly filled last page of row 1, given up by the caller
+    cache.page_refs[gone] -= 1
+    live = cache.page_refs.clone()
+    first = int(cache.page_table[1, 0])
+    g = torch.Generator().manual_seed(3)
+    for p in (cache.k_pages, cache.v_pages):
+        p[:, first] = torch.randn(p[:, first].shape, generator=g).to(BF).cuda()
+    assert cache.fork([1, 0], [3, 2]).tolist() == [0, 3]
+    assert cache.page_table[3].tolist() == [first, entry] + [-1] * 7 and cache.kv_lens[3] == 20
+    live[first] += 1
+    assert torch.equal(cache.page_refs, live)
+    assert cache.kv_lens.tolist() == [48, 20, 48, 20]
+    q = torch.randn((4, 1, 64), generator=g).to(BF).cuda()
+    see = [sa.attn_paged(q, cache.k_pages[0], cache.v_pages[0], cache.page_table, cache.kv_lens, i32(cu), causal=False)
+           for cu in ([0, 0, 1, 1, 1], [0, 0, 0, 0, 1])]  # the parent's row, the child's
+    assert torch.isfinite(see[0][1]).all()
+    assert torch.equal(see[0][0], see[1][0]) and torch.equal(see[0][1], see[1][1])
+
+
+def test_forks_of_evicted_and_of_whole_rows_in_one_call(sa):
+    """Rows that end in a page, at its end, in an evicted page, and in a table's last column."""
+    ps, W = 16, 4
+    table = i32([[0, 1, 2, 3], [4, 5, -1, -1], [6, -1, 8, -1], [9, -1, -1, -1]] + [[-1] * W] * 5)
+    lens = i32([64, 23, 45, 21, 0, 0, 0, 0, 0])  # row 3 ends in column 1, evicted; row 2 lost its middle
+    refs = torch.zeros(16, dtype=I32, device="cuda")
+    refs[[0, 1, 2, 3, 4, 5, 6, 8, 9]] = 1
+    pool = torch.arange(16.0, device="cuda")[:, None, None, None].expand(16, 1, ps, 64).contiguous()
+    status = sa.paged_fork(pool, table, lens, refs, [3, 1, 2, 0, 1], [4, 5, 6, 7, 8])
+    assert status.tolist() == [0] * 5 and lens.tolist() == [64, 23, 45, 21, 21, 23, 45, 64, 23]
+    assert table[4:].tolist() == [[9, -1, -1, -1], [4, 7, -1, -1], [6, -1, 10, -1], [0, 1, 2, 3], [4, 11, -1, -1]]
+    assert refs.tolist() == [2, 2, 2, 2, 3, 1, 2, 1, 1, 2, 1, 1, 0, 0, 0, 0]
+    assert [pool[p].unique().tolist() for p in (7, 10, 11)] == [[5.0], [8.0], [5.0]]
