@@ -471,6 +471,7 @@ class PagedCache:
         pools = self.k_pages[layer], self.v_pages[layer]
         tables = self.page_table, self.kv_lens, cu_seqlens
         if self.plan is None:
+            _require(positions is None, "the cache has no plan to turn its keys by: positions are of no use to it")
             paged_append(k, v, *pools, *tables, guard=self.guard)
         else:
             _require(positions is not None, "the cache turns its keys by their positions: pass them")

@@ -45,3 +45,12 @@ def test_guards_of_another_shape_or_type_are_refused(lib):  # noqa: F811
     kp, x = torch.zeros((8, 1, 16, 64), dtype=BF), torch.zeros((1, 5, 64), dtype=BF)
     with pytest.raises(ValueError, match="CUDA"):  # the cache's tensors are looked at first
         sa.paged_append(x, x, kp, kp, table, lens, torch.zeros(3, dtype=I32), guard=torch.zeros((4, 3), dtype=I32))
+
+
+def test_positions_for_a_cache_that_does_not_turn_are_refused():
+    import sequence_attn_fwd_gb300 as sa
+
+    cache = sa.PagedCache(4, 1, 64, rows=1, max_pages=4, device="cpu")
+    x = torch.zeros((1, 1, 64), dtype=BF)
+    with pytest.raises(ValueError, match="plan"):
+        cache.step(0, x, x, x, torch.zeros(2, dtype=I32), torch.zeros((1, 1), dtype=I32))
