@@ -81,6 +81,24 @@ __device__ __forceinline__ void pack(const float (&x)[16], uint4 (&w)[4]) {
                       __float_as_uint(x[4 * i + 3]));
 }
 
+// Puts the turned elements into w and leaves those of the pairs `still` (one bit
+// each) as they are, a 32-bit word at a time.
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void keep_copied(unsigned still, const uint4 (&turned)[Vec16<T>::kPieces],
+                                            uint4 (&w)[Vec16<T>::kPieces]) {
+  constexpr int kPer = 4 / static_cast<int>(sizeof(T)), kWords = 16 / kPer;  // elements of a word, words
+  uint32_t *to = reinterpret_cast<uint32_t *>(w);
+  const uint32_t *from = reinterpret_cast<const uint32_t *>(turned);
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    // pairs of the word's first and last element
+    const int a = kPer * i, b = a + kPer - 1, pa = kInterleaved ? a / 2 : a % 8, pb = kInterleaved ? b / 2 : b % 8;
+    const uint32_t keep = (still >> pa & 1u ? (pa == pb ? 0xffffffffu : 0xffffu) : 0u) |
+                          (pa != pb && (still >> pb & 1u) ? 0xffff0000u : 0u);
+    to[i] = (to[i] & keep) | (from[i] & ~keep);
+  }
+}
+
 // Element offset of piece i (16 bytes) of the 16 elements that slice `sl` of a
 // row has: consecutive ones when pairs are neighbours, else eight at 8 sl and
 // their partners D / 2 further on.
@@ -127,9 +145,14 @@ __device__ __forceinline__ long long slot_of(const PagedView &c, int *guard, lon
 }
 
 // blockIdx.x: tile of kTok tokens; blockIdx.y: share of the heads (those of q,
-// then k, then, in an append, v).
-template <typename T, int D, bool kInterleaved, bool kAppend, int kTok>
-__global__ void __launch_bounds__(kRopeThreads)
+// then k, then, in an append, v). kStill: some pairs are copied, whatever they hold
+// (turned by an angle of 0, an infinity would make its partner NaN). A variant of
+// its own: tested in the one loop, it cost the others 17 %. Held to 64 registers,
+// and to two rows in flight in fp32, it takes their time (32,768 tokens of 28 heads
+// of 128: bf16 81 us in either pairing 83, fp32 155 and 165; with 72 to 77 registers
+// 94 to 96, 163 to 179; four fp32 rows in flight 162, 179).
+template <typename T, int D, bool kInterleaved, bool kAppend, int kTok, bool kStill>
+__global__ void __launch_bounds__(kRopeThreads, kStill ? 4 : 0)
     rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopeTable tbl) {
   constexpr int kSlices = D / 16;                               // threads per row
   constexpr int kHeads = kRopeThreads / (kSlices * kTok);       // heads of a CTA at a time
@@ -145,11 +168,13 @@ __global__ void __launch_bounds__(kRopeThreads)
   const bool one = blockIdx.y == 0 && sl == 0 && threadIdx.x < kSlices * kTok;
   const long long slot = kAppend ? slot_of(p.cache, p.guard, t, n_tok, D, one, &live) : -1;
   float cn[8], sn[8];
+  unsigned still = 0;  // pairs that are copied
   if (p.positions != nullptr) {
     const int *pos = p.positions + b * p.pos_b + s;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int axis = tbl.axis[8 * sl + k];
+      if (kStill && axis < 0) still |= 1u << k;
       const long long at = axis < 0 ? 0 : pos[axis * p.pos_axis];
       // position times turns per position, whole turns dropped: [-1/2, 1/2) turns in 64 bits
       const long long turn = static_cast<long long>(static_cast<uint64_t>(at) * tbl.turns[8 * sl + k]);
@@ -157,6 +182,7 @@ __global__ void __launch_bounds__(kRopeThreads)
       if (p.inverse) sn[k] = -sn[k];
     }
   }
+  constexpr int kRows = kStill && sizeof(T) == 4 ? 2 : 4;  // in flight
   const int heads = p.q.heads + p.k.heads + (kAppend ? p.v.heads : 0);
   const int h_per = (heads + gridDim.y - 1) / gridDim.y;
   const int h0 = blockIdx.y * h_per + threadIdx.x / (kSlices * kTok), h1 = min(heads, static_cast<int>(blockIdx.y + 1) * h_per);
@@ -164,7 +190,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   auto rows = [&](int first, int n, const T *src, long long src_h, T *dst, long long dst_h, bool turned) {
     const int lo = h0 >= first ? h0 : first + (kHeads - (first - h0) % kHeads) % kHeads;
     const int hi = min(h1, first + n);
-#pragma unroll 4
+#pragma unroll kRows
     for (int h = lo; h < hi; h += kHeads) {
       const T *from = src + (h - first) * src_h;
       T *to = dst + (h - first) * dst_h;
@@ -181,7 +207,13 @@ __global__ void __launch_bounds__(kRopeThreads)
           y[i1] = fmaf(v[i1], cn[k], -v[i2] * sn[k]);
           y[i2] = fmaf(v[i1], sn[k], v[i2] * cn[k]);
         }
-        pack(y, w);
+        if (kStill) {
+          uint4 turned_w[kPieces];
+          pack(y, turned_w);
+          keep_copied<T, kInterleaved>(still, turned_w, w);
+        } else {
+          pack(y, w);
+        }
       }
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)  // (streaming stores: 2 % of a long sequence's time)
@@ -200,7 +232,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   }
 }
 
-template <typename T, int D, bool kInterleaved, bool kAppend, int kTok>
+template <typename T, int D, bool kInterleaved, bool kAppend, int kTok, bool kStill>
 cudaError_t launch_tile(const RopeParams &p, const RopeTable &tbl, cudaStream_t stream) {
   const long long n_tok = static_cast<long long>(p.B) * p.S;
   const long long tiles = (n_tok + kTok - 1) / kTok;
@@ -211,20 +243,30 @@ cudaError_t launch_tile(const RopeParams &p, const RopeTable &tbl, cudaStream_t 
   const long long most = (heads + kHeads - 1) / kHeads;
   want = want < 1 ? 1 : (want > most ? most : want);
   if (tiles > 0x7fffffffll || want > 65535) return cudaErrorInvalidValue;
-  return launch_dependent(rope_kernel<T, D, kInterleaved, kAppend, kTok>,
+  return launch_dependent(rope_kernel<T, D, kInterleaved, kAppend, kTok, kStill>,
                           dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(want)), dim3(kRopeThreads), 0, stream, p,
                           tbl);
 }
 
-template <typename T, int D, bool kAppend>
-cudaError_t launch_typed_rope(const RopeParams &p, const RopeTable &tbl, bool interleaved, cudaStream_t stream) {
+template <typename T, int D, bool kAppend, bool kStill>
+cudaError_t launch_variant(const RopeParams &p, const RopeTable &tbl, bool interleaved, cudaStream_t stream) {
   // Tiles of 32 tokens give a thread the most heads to its sines (32,768 tokens
   // of 32 heads in bf16: 89 us; tiles of 16 and 8: 4 us more); with fewer tokens than
   // one such tile an SM, tiles of 4 give more CTAs.
   const bool small = static_cast<long long>(p.B) * p.S < 32ll * device_sm_count();
   if (interleaved)
-    return small ? launch_tile<T, D, true, kAppend, 4>(p, tbl, stream) : launch_tile<T, D, true, kAppend, 32>(p, tbl, stream);
-  return small ? launch_tile<T, D, false, kAppend, 4>(p, tbl, stream) : launch_tile<T, D, false, kAppend, 32>(p, tbl, stream);
+    return small ? launch_tile<T, D, true, kAppend, 4, kStill>(p, tbl, stream)
+                 : launch_tile<T, D, true, kAppend, 32, kStill>(p, tbl, stream);
+  return small ? launch_tile<T, D, false, kAppend, 4, kStill>(p, tbl, stream)
+               : launch_tile<T, D, false, kAppend, 32, kStill>(p, tbl, stream);
+}
+
+template <typename T, int D, bool kAppend>
+cudaError_t launch_typed_rope(const RopeParams &p, const RopeTable &tbl, bool interleaved, cudaStream_t stream) {
+  bool still = false;
+  for (int i = 0; i < D / 2; ++i) still |= tbl.axis[i] < 0;
+  return still ? launch_variant<T, D, kAppend, true>(p, tbl, interleaved, stream)
+               : launch_variant<T, D, kAppend, false>(p, tbl, interleaved, stream);
 }
 
 }  // namespace

@@ -234,3 +234,38 @@ def test_forks_of_evicted_and_of_whole_rows_in_one_call(sa):
     assert table[4:].tolist() == [[9, -1, -1, -1], [4, 7, -1, -1], [6, -1, 10, -1], [0, 1, 2, 3], [4, 11, -1, -1]]
     assert refs.tolist() == [2, 2, 2, 2, 3, 1, 2, 1, 1, 2, 1, 1, 0, 0, 0, 0]
     assert [pool[p].unique().tolist() for p in (7, 10, 11)] == [[5.0], [8.0], [5.0]]
+
+
+# ---------------------------------------------------------------------------- pairs that are not turned
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("S", [3, 6000])
+def test_pairs_without_an_axis_are_copied(sa, dtype, interleaved, S):
+    """Whatever they hold: infinities, NaN, signed zeros stay in their own elements."""
+    D = 64
+    plan = sa.RopePlan(D, (5, 6))  # eleven pairs turn, 21 do not
+    x = torch.randn((1, 2, S, D), generator=torch.Generator().manual_seed(S)).to(dtype)
+    first = torch.arange(11, 32) * 2 if interleaved else torch.arange(11, 32)
+    second = first + 1 if interleaved else first + 32
+    odd = torch.tensor([math.inf, -math.inf, math.nan, -0.0, 3e38])
+    x[..., first[:20]] = odd.repeat(4).to(dtype)
+    x[..., second[:20]] = odd.repeat_interleave(4).to(dtype)
+    x = x.cuda()
+    pos = torch.randint(0, 10 ** 6, (2, 1, S), generator=torch.Generator().manual_seed(1)).to(I32).cuda()
+    still = torch.cat([first, second]).cuda()
+    bits = torch.int16 if dtype == BF else torch.int32
+
+    def copied(y, x):
+        y, x = y[..., still], x[..., still]
+        assert torch.equal(y.isnan(), x.isnan())
+        assert torch.equal(y.view(bits)[~x.isnan()], x.view(bits)[~x.isnan()])
+
+    for fn in (sa.rope_axes, sa.rope_axes_bwd):
+        copied(fn(x, None, pos, *plan, interleaved=interleaved)[0], x)
+    if dtype == BF:
+        cache = sa.PagedCache(400, 2, D, rows=1, max_pages=400, plan=plan, interleaved=interleaved)
+        assert cache.reserve(i32([S])).tolist() == [0]
+        q = sa.paged_append(x[0], x[0], cache.k_pages[0], cache.v_pages[0], cache.page_table, cache.kv_lens, i32([0, S]),
+                            q=x[0], positions=pos[:, 0], inv_freq=plan.inv_freq, axes=plan.axes, interleaved=interleaved)
+        copied(q, x[0])
+        copied(cache.k_pages[0].transpose(0, 1).reshape(2, -1, D)[:, :S], x[0])
