@@ -131,7 +131,7 @@ int make_pools(seqattn::PoolList *list, const paged_pool *pools, int n, int n_pa
   if (n < 0 || (n > 0 && !pools)) return ATTN_ERR_INVALID_ARG;
   if (n > seqattn::kMaxPools) return ATTN_ERR_UNSUPPORTED;
   list->n = list->total_layers = 0;
-  long long items = 0;
+  long long items = 0, layers = 0;  // at most 32 x 2^31
   for (int i = 0; i < n; ++i) {
     const paged_pool &p = pools[i];
     if (p.n_layers < 0 || p.page_bytes < 0) return ATTN_ERR_INVALID_ARG;
@@ -140,10 +140,12 @@ int make_pools(seqattn::PoolList *list, const paged_pool *pools, int n, int n_pa
       return ATTN_ERR_INVALID_ARG;
     if (n_pages > 1 && p.page_stride < p.page_bytes) return ATTN_ERR_INVALID_ARG;
     list->pool[list->n++] = {static_cast<unsigned char *>(p.base), p.layer_stride, p.page_stride, p.page_bytes, p.n_layers};
-    list->total_layers += p.n_layers;
-    items += (p.page_bytes + 16383) / 16384;
+    layers += p.n_layers;
+    items += (p.page_bytes - 1) / 16384 + 1;
   }
-  if (items * list->total_layers > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  // copies of 16 KB of one page
+  if (items > (1 << 30) || layers > (1 << 30) || items * layers > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  list->total_layers = static_cast<int>(layers);
   return ATTN_OK;
 }
 

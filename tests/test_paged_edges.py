@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests.test_abi import FAKE, build_mod
-from tests.test_paged_abi import lib, rows, view  # noqa: F401  (lib: the fixture)
+from tests.test_paged_abi import ints, lib, pool, rows, view  # noqa: F401  (lib: the fixture)
 
 BF, I32 = torch.bfloat16, torch.int32
 
@@ -54,3 +54,15 @@ def test_positions_for_a_cache_that_does_not_turn_are_refused():
     x = torch.zeros((1, 1, 64), dtype=BF)
     with pytest.raises(ValueError, match="plan"):
         cache.step(0, x, x, x, torch.zeros(2, dtype=I32), torch.zeros((1, 1), dtype=I32))
+
+
+def test_layers_are_counted_in_64_bits(lib):  # noqa: F811
+    """Four pools of 2^30 layers are refused, not taken for none at all."""
+    pools = pool(4, n_layers=1 << 30)
+    s, d = ints(0), ints(1)
+    A = ctypes.addressof
+    assert lib.paged_copy(A(pools), 4, A(s), A(d), 1, 16, None) == 2
+    pools = pool(2, n_layers=(1 << 31) - 1)
+    assert lib.paged_copy(A(pools), 2, A(s), A(d), 1, 16, None) == 2
+    big = (1 << 63) - 16  # bytes of a page, which rounded up to whole copies would pass 64 bits
+    assert lib.paged_copy(A(pool(page_bytes=big, page_stride=big)), 1, A(s), A(d), 1, 16, None) == 2
