@@ -112,8 +112,8 @@ def _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens):
         raise ValueError("pools must be [n_pages, Hkv, page_size, D]")
     n_pages, Hkv, ps, D = k_pages.shape
     sk, sv = k_pages.stride(), v_pages.stride()
-    if (k_pages.dtype != _BF16 or v_pages.dtype != _BF16 or sk[3] != 1 or (ps > 1 and sk[2] != D)
-            or (Hkv > 1 and sk[1] != ps * D) or sv[1:] != sk[1:]):
+    if (k_pages.dtype != _BF16 or v_pages.dtype != _BF16 or sk[3] != 1 or sv[3] != 1
+            or (ps > 1 and (sk[2] != D or sv[2] != D)) or (Hkv > 1 and (sk[1] != ps * D or sv[1] != ps * D))):
         raise ValueError("pools must be bf16 with contiguous pages")
     if n_pages > 1 and sv[0] != sk[0]:
         raise ValueError("the K and V pools must share their page stride")

@@ -66,3 +66,20 @@ def test_layers_are_counted_in_64_bits(lib):  # noqa: F811
     assert lib.paged_copy(A(pools), 2, A(s), A(d), 1, 16, None) == 2
     big = (1 << 63) - 16  # bytes of a page, which rounded up to whole copies would pass 64 bits
     assert lib.paged_copy(A(pool(page_bytes=big, page_stride=big)), 1, A(s), A(d), 1, 16, None) == 2
+
+
+def test_strides_of_pool_dimensions_of_one_are_free():
+    """One KV head: its stride may be anything, in either pool. (Past the layout checks, the refusal is that of CPU tensors.)"""
+    import sequence_attn_fwd_gb300 as sa
+
+    kp = torch.zeros((8, 1, 16, 64), dtype=BF)
+    vp = torch.zeros((8, 16, 1, 64), dtype=BF).transpose(1, 2)
+    assert vp.shape == kp.shape and vp.stride() != kp.stride()
+    q = torch.zeros((4, 2, 64), dtype=BF)
+    table, lens, cu = torch.zeros((1, 4), dtype=I32), torch.zeros(1, dtype=I32), torch.zeros(2, dtype=I32)
+    for a, b in ((kp, vp), (vp, kp)):
+        with pytest.raises(ValueError, match="CUDA"):
+            sa.attn_paged(q, a, b, table, lens, cu)
+    both = torch.zeros((8, 2, 16, 64), dtype=BF)
+    with pytest.raises(ValueError, match="pools"):
+        sa.attn_paged(q, both, torch.zeros((8, 16, 2, 64), dtype=BF).transpose(1, 2), table, lens, cu)
