@@ -62,7 +62,9 @@ typedef struct {
  *             bytes; no other call may use it at the same time
  * Strides are in elements and multiples of 8. Rows that see no key: O = 0,
  * lse = -inf. Keys and values
- * inside kv_lens must be finite (a row with a NaN score comes out as NaN). D 64 or 128, Hq / Hkv at
+ * inside kv_lens must be finite (a row with a NaN score comes out as NaN). Scores, sums and
+ * accumulators are fp32; the exponentials are rounded to bf16 for the product with V, as in
+ * attn_fwd, and summed before that. D 64 or 128, Hq / Hkv at
  * most 128, B at most 4096, max_pages * page_size at most 2^30, and at most
  * 2^31 tiles of 128 keys over all row blocks of 256 rows (else
  * ATTN_ERR_UNSUPPORTED). Two kernels: the attention itself, its key tiles
@@ -126,8 +128,11 @@ int paged_append(const rope_rows *q, const rope_rows *k, const rope_rows *v, con
  * entries that hold each page; a page with 0 is free. New pages are always the
  * lowest free ones, handed out in the order of the rows that need them.
  * kv_lens and the entries of the table change through these calls only: a
- * row's entries behind its length are -1. Entries in front may be set to -1
- * (evicted) by the caller, who then counts their references down.
+ * row's entries behind its length are -1 (pages behind a length that the caller
+ * lowered would never be free again: there is no call that gives single tokens
+ * back). Entries in front may be set to -1 (evicted) by the caller, who then counts
+ * their references down; in an evicted page that is partly filled, tokens appended
+ * later have no place either.
  * status (int32 per row or pair, device, output): 0 done, PAGED_NO_PAGES, or
  * the reason given below; a row or pair that is not done is left unchanged.
  * All rows of one call belong to one table; calls that change the same table
@@ -170,8 +175,9 @@ typedef struct {
 #define PAGED_MAX_POOLS 32
 
 /* Room for n_new[b] more tokens (device int32 [B], negative counts as 0) in
- * every row: pages are added to the table and kv_lens grows by n_new[b]. B at
- * most 4096. */
+ * every row: pages are added to the table and kv_lens grows by n_new[b]. Rows are
+ * served in order while the free pages last: behind one that gets PAGED_NO_PAGES
+ * every row that needs a page gets it too, even if it needs fewer. B at most 4096. */
 int paged_reserve(int *page_table, long long table_stride, int *kv_lens, int *page_refs, const int *n_new,
                   int *status, int B, int max_pages, int n_pages, int page_size, attn_stream_t stream);
 

@@ -26,10 +26,10 @@
 // keys a page cost no more than 128 (319 us against 318 for the batch below).
 //
 // Measured (GB300): 1,024 new tokens behind 65,536 keys, 32 heads over 8 KV heads
-// of 128, 0.76 ms = 1,450 TFLOP/s, 3,000 clocks a pair of tiles (the dense
-// forward's share; the tensor pipe's own time is 2,048); six sequences of up to
-// 600 new tokens behind up to 12,400 keys 162 us, and 11 more for the merge: the
-// tiles at that rate, 12,000 clocks until the first scores of a CTA and about as
+// of 128, 0.75 ms = 1,470 TFLOP/s in a chain of 15 calls and 0.86 ms = 1,290 under
+// sustained load (power), 3,000 clocks a pair of tiles (the dense forward's share;
+// the tensor pipe's own time is 2,048); six sequences of up to 600 new tokens behind
+// up to 12,400 keys 162 us, and 11 more for the merge: the tiles at that rate, 12,000 clocks until the first scores of a CTA and about as
 // many from an item to the next, most of it the epilogue of the softmax warps.
 //
 // This is the wide form. Sequences of at most 64 rows per KV head are the narrow

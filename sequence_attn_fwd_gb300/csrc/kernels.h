@@ -237,8 +237,9 @@ size_t compact_workspace_ints(int n_pages);
 
 // Launches a kernel that may start before the one ahead of it on the stream has
 // finished; it calls wait_prerequisites() before it touches memory. Every kernel
-// of the serving side is launched so, waits first and lets the next one start
-// as soon as its own CTAs have: 1.5 to 2.5 us a call of a chain.
+// of the serving side is launched so and waits first; all but the merge of the
+// attention let the next one start as soon as their own CTAs have: 1.5 to 2.5 us a
+// call of a chain.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                              Args &&...args) {

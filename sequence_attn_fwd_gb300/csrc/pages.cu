@@ -8,9 +8,10 @@
 // The searches read the counts (4 bytes a page) and are bound by latency; the
 // copies move whole pages and are bound by DRAM. Measured (GB300): freeing 100
 // forks of a 4,096-page pool, forking them again (26 MB of last pages over 16
-// layer pools) and reserving their next tokens, four kernels, 21.8 us; making a
-// pool of 8 layers dense, 0.52 GB of pages moved, 168 us = 6.1 TB/s of the 6.8
-// that a copy reaches.
+// layer pools) and reserving their next tokens, four kernels, 22 us of the device in
+// a chain of such cycles (the three calls, one after the other, 27 to 30 us: their
+// host side); making a pool of 8 layers dense, 0.52 GB of pages moved, 168 us = 6.1
+// TB/s of the 6.8 that a copy reaches.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

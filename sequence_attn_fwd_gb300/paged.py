@@ -350,7 +350,8 @@ def paged_reserve(page_table: torch.Tensor, kv_lens: torch.Tensor, page_refs: to
                   guard: torch.Tensor | None = None) -> torch.Tensor:
     """Room for n_new (int32 [B], device) more tokens in every row of the table: the
     lowest free pages (page_refs 0) in the order of the rows; kv_lens grows by
-    n_new. Returns status int32 [B]: 0, PAGED_NO_PAGES or PAGED_TOO_LONG (that row
+    n_new. Behind a row that gets PAGED_NO_PAGES every row that needs a page gets it
+    too, even if it needs fewer. Returns status int32 [B]: 0, PAGED_NO_PAGES or PAGED_TOO_LONG (that row
     unchanged: appended tokens would lie over the keys that it has, so it must bring
     none, or the append gets the guard of this call too). guard: int32 [4, B] on the
     device, zeros at first, then for paged_reserve and paged_append only."""
