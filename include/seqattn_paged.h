@@ -189,7 +189,8 @@ int paged_free(int *page_table, long long table_stride, int *kv_lens, int *page_
 /* Row dst[i] becomes a copy of row src[i] (host arrays; dst distinct, none of
  * them in src; src may repeat): whole pages are shared, a partly filled last
  * page is copied to a page of its own in every pool, so that both rows can
- * grow (an evicted one stays evicted in both). A dst row must be empty (kv_lens 0), else PAGED_IN_USE. */
+ * grow (an evicted one stays evicted in both). A dst row must be empty (kv_lens
+ * 0), else PAGED_IN_USE. */
 int paged_fork(const paged_pool *pools, int n_pools, int *page_table, long long table_stride, int *kv_lens,
                int *page_refs, const int *src, const int *dst, int *status, int n, int B, int max_pages,
                int n_pages, int page_size, attn_stream_t stream);

@@ -149,8 +149,8 @@ __device__ __forceinline__ long long slot_of(const PagedView &c, int *guard, lon
 // (turned by an angle of 0, an infinity would make its partner NaN). A variant of
 // its own: tested in the one loop, it cost the others 17 %. Held to 64 registers,
 // and to two rows in flight in fp32, it takes their time (32,768 tokens of 28 heads
-// of 128: bf16 81 us in either pairing 83, fp32 155 and 165; with 72 to 77 registers
-// 94 to 96, 163 to 179; four fp32 rows in flight 162, 179).
+// of 128, halves and neighbours as pairs: bf16 81 and 83 us, fp32 153 and 165; with
+// 72 to 77 registers 94 and 96, 163 and 179; with four fp32 rows in flight 162 and 179).
 template <typename T, int D, bool kInterleaved, bool kAppend, int kTok, bool kStill>
 __global__ void __launch_bounds__(kRopeThreads, kStill ? 4 : 0)
     rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopeTable tbl) {
