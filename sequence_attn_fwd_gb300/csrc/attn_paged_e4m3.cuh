@@ -493,6 +493,7 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
   // (in turns the warpgroups take an item together or leave together, and the second
   // waits here until the first has done with its results)
   while (kTurns ? named_bar_and(4, 256, items.wait(abort_flag, err)) : items.wait_together(id, abort_flag, err)) {
+    if (kTurns) tc_fence_after();  // the first warpgroup's loads of the second's O, ahead of its next product
     const Segment g = items.get();
     items.release();
     const int n = g.j1 - g.j0, rows = g.s.q_len * p.G, j_first = first_of(first_step);
@@ -685,7 +686,9 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
     auto sum_at = [&](const Reductions<C> &x, int c) { return (x.red[c] + x.red[C + c]) + (x.red[2 * C + c] + x.red[3 * C + c]); };
     if (kTurns) {
       if (gi != 0 && key == 0) mine.tops[0] = top_e;
+      tc_fence_before();  // the second's products, which only it has waited for, ahead of the first's loads
       if (!named_bar_and(3, 256, ok)) return;
+      tc_fence_after();
       if (gi != 0) continue;
     } else {
       if (!named_bar_and(id, 128, ok)) return;
@@ -765,6 +768,7 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
       }
       __syncwarp();
     }
+    if (kTurns) tc_fence_before();
   }
 }
 
