@@ -281,6 +281,10 @@ int draft_tree(const int *parents, const int *cu_seqlens, long long *masks, int 
  * at). Tokens of longer sequences see what they see in attn_paged. In
  * attn_paged_e4m3 tree may be NULL (tree_words 0), and causal is as in attn_paged
  * then. Workspace: attn_paged_workspace_bytes. Queries are bf16 in both.
+ * Over the 8-bit cache, weights of sequences of at most 64 rows (new tokens times
+ * Hq / Hkv) are rounded to 2^-9 of themselves for the product with V, if they and their value's
+ * scale multiply to 2^-23 of the row's largest such product or more; below that, to steps of
+ * 2^-31 of it (2^-48 of the largest scale that a row sees counts as the least scale there).
  */
 int attn_paged_tree(const void *q, long long q_head_stride, long long q_row_stride, const paged_cache *cache, void *o,
                     long long o_head_stride, long long o_row_stride, float *lse, void *workspace,

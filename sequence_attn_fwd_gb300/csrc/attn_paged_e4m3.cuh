@@ -12,12 +12,17 @@
 //     significant bits, e4m3 4, and the remainder needs no more than 4. The powers of
 //     two and the keys' scales multiply the fp32 scores.
 //   O = P V   wants every weight scaled by its value's scale (V is read by columns, its
-//     scales belong to rows): w = p 2^(e_j - E), E the largest exponent of the values
-//     seen so far, so w <= p; when a larger one comes O is brought to it, as it is to a
-//     new reference of the softmax. Sums l are of p, in fp32. w 2^4 is two e4m3 numbers,
-//     the second, of what the first leaves, times 2^5, in columns of their own, so that V
-//     is read once for both: together 2^-8 of a weight, as bf16 gives, and 2^-18 of the
-//     largest.
+//     scales belong to rows): w = 2^(s_j + e_j - E - m), E an exponent that the tiles of a
+//     segment share. The column's reference m follows the largest s_j + e_j - E, what a
+//     key brings to O, and not the largest s_j: a key of much weight and next to no value,
+//     the first of many long contexts, takes no bits from the others, and neither does a
+//     large value of no weight. Sums l are of 2^(s_j - m), in fp32. w 2^11, rounded to
+//     fp16, is three e5m2 numbers (fp16's upper byte; that of the rest; the rest of that
+//     to nearest, times 2^4), three bits each, in columns of their own, so that V is read
+//     once for all: 2^-9 of a weight, as bf16 gives, down to 2^-23 of the column's largest,
+//     and steps of 2^-31 of that below. (As two e4m3 numbers, steps of 2^-18: batch decoding
+//     177 us, now 183, trees of up to 64 rows 143, now 151; but a first key of 12 nats
+//     above 8,191 others left 0.1 of their answer lost.)
 // Wide form (compute bound), in fp16, which holds codes and ratios of scales: warps of their
 // own turn K and V tiles, each to units of the tile's largest scale, on their way into the ring of
 // the bf16 form; Q goes there after its rows' powers of two. The softmax has two factors
@@ -26,7 +31,7 @@
 // 1,024 tokens behind 65,536 keys.)
 //
 // Measured (GB300): 64 sequences' next tokens over 300 to 16,000 keys (1.06 GB, 8 KV
-// heads of 128) 177 us = 6.0 TB/s; 1,024 tokens behind 65,536 keys, 32 heads over 8 of
+// heads of 128) 183 us = 5.8 TB/s; 1,024 tokens behind 65,536 keys, 32 heads over 8 of
 // 128, 911 us = 1,216 TFLOP/s.
 #pragma once
 
@@ -71,7 +76,7 @@ struct Cfg8 {
   static_assert(4 * 2560 <= Wide::kTileBytes, "epilogue in the place of Q");
   static constexpr int kItemBarrier = 2 * kMaxStages + 10, kMaxBarriers = kItemBarrier + 8;
   static constexpr int kPrefixAt = Wide::kPrefixAt;         // inside the ring of either form
-  static_assert(kPrefixAt + 4 * (kPagedMaxSeqs + 1) <= 163840, "prefix sums inside the narrow ring");
+  static_assert(kPrefixAt + 4 * (kPagedMaxSeqs + 1) <= 131072, "prefix sums inside the narrow ring");
   // behind them: barriers, three words, segments, the wide form's exponents and factors (before: sums over warps)
   static constexpr int kSmallBytes = 4 * 32 + 4 * 256;
   static constexpr int kSmemBytes = 1024 + kAreaBytes + 8 * kMaxBarriers + 16 + 4 * 48 + kSmallBytes;
@@ -257,15 +262,20 @@ struct Narrow8 {
   bool turns;  // they take tiles in turn, each with sums, reference and O of its own; else half the columns each
   __device__ __forceinline__ explicit Narrow8(int rows) {
     N = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-    stages = (N == 64 ? 163840 : 196608) / Cfg8<D>::kTileBytes;
+    stages = (N == 16 ? 196608 : (N == 32 ? 163840 : 131072)) / Cfg8<D>::kTileBytes;
     turns = N == 16;
   }
-  // shared memory: ring, P (128 bytes a key: two buffers of 2 N codes, or two tiles), Q (two parts)
+  // shared memory: ring, two buffers of P, Q (two parts). A key's 3 N codes of P lie in rows of 128 bytes: half a
+  // row a buffer, a row, or two rows a block of 128 columns apart.
   static constexpr int kPBytes = kRowsPerTile * 128;
   __device__ __forceinline__ int p_at() const { return stages * Cfg8<D>::kTileBytes; }
-  __device__ __forceinline__ int q_at() const { return p_at() + (N == 64 ? 2 : 1) * kPBytes; }
-  static_assert(163840 + 2 * kPBytes + 2 * 64 * D <= Cfg8<D>::kAreaBytes && 196608 + kPBytes + 2 * 32 * D <= Cfg8<D>::kAreaBytes,
+  __device__ __forceinline__ int p_step() const { return N == 16 ? 64 : (N == 32 ? kPBytes : 2 * kPBytes); }
+  __device__ __forceinline__ int q_at() const { return p_at() + (N == 16 ? 1 : (N == 32 ? 2 : 4)) * kPBytes; }
+  static_assert(196608 + kPBytes + 2 * 16 * D <= Cfg8<D>::kRedAt && 163840 + 2 * kPBytes + 2 * 32 * D <= Cfg8<D>::kRedAt &&
+                    131072 + 4 * kPBytes + 2 * 64 * D <= Cfg8<D>::kRedAt,
                 "narrow layouts");
+  // TMEM columns: two buffers of S, then O, 3 N columns, or with turns two of 48, 64 apart
+  static constexpr int kOStep = 64;
   // barriers
   static constexpr int kFull = 0, kEmpty = Cfg8<D>::kMaxStages, kQFull = 2 * Cfg8<D>::kMaxStages, kSFull = kQFull + 1,
                        kPFull = kSFull + 2, kPvDone = kPFull + 2, kScoresDone = kPvDone + 2, kProductsDone = kScoresDone + 1,
@@ -288,7 +298,7 @@ __device__ __forceinline__ void narrow_scores8(const Narrow8<D> &sh, Items items
   const bool leader = elect_one();
   const uint32_t tmem = uniform(tmem_in), N = uniform(static_cast<uint32_t>(sh.N));
   const int stages = uniform(sh.stages);
-  const uint32_t q_at = smem + stages * C::kTileBytes + (N == 64 ? 2 : 1) * L::kPBytes;
+  const uint32_t q_at = smem + uniform(static_cast<uint32_t>(sh.q_at()));
   const uint32_t idesc_s = idesc_e4m3_f32(128, 0, false, false) | (N >> 3) << 17;
   const uint64_t qd = code_desc<D>(q_at, 16), q_lo = static_cast<uint64_t>((N * D) >> 4);
   paged::RingPos k{0, 0};
@@ -340,8 +350,8 @@ __device__ __forceinline__ void narrow_products8(const Narrow8<D> &sh, Items ite
   const bool leader = elect_one();
   const uint32_t tmem = uniform(tmem_in), N = uniform(static_cast<uint32_t>(sh.N));
   const int stages = uniform(sh.stages);
-  const uint32_t p_at = smem + stages * C::kTileBytes, p_step = N == 64 ? static_cast<uint32_t>(L::kPBytes) : 2 * N;
-  const uint32_t idesc_o = idesc_e4m3_f32(128, 0, true, true) | (2 * N >> 3) << 17;
+  const uint32_t p_at = smem + stages * C::kTileBytes, p_step = uniform(static_cast<uint32_t>(sh.p_step()));
+  const uint32_t idesc_o = idesc_e4m3_e5m2_f32(128, 0, true, true) | (3 * N >> 3) << 17;
   const bool turns = N == 16;
   paged::RingPos v{1, 0};
   uint32_t step = 0;  // key tiles so far
@@ -358,8 +368,8 @@ __device__ __forceinline__ void narrow_products8(const Narrow8<D> &sh, Items ite
       // V as stored, [key][column], is the M-major A operand; for D = 64 the upper 64
       // rows of the product read the tile behind it and are never looked at
       const uint64_t vd = code_desc<D>(smem + v.slot * C::kTileBytes, C::kTileBytes);
-      const uint64_t pd = sw128_desc(p_at + (step & 1u) * p_step, 16, 1024);
-      const uint32_t add = j > (turns ? 1 : 0) ? 1u : 0u, o_col = tmem + 2 * N + (turns ? (step & 1u) * 2 * N : 0u);
+      const uint64_t pd = sw128_desc(p_at + (step & 1u) * p_step, L::kPBytes, 1024);
+      const uint32_t add = j > (turns ? 1 : 0) ? 1u : 0u, o_col = tmem + 2 * N + (turns ? (step & 1u) * L::kOStep : 0u);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < kRowsPerTile / 32; ++kk)
@@ -390,12 +400,19 @@ __device__ __forceinline__ bool clear_tail8(int valid_keys, uint32_t v, uint32_t
   return true;
 }
 
-// Two weights to codes of both numbers (see the top of the file): hi, and what it leaves times 2^5.
-__device__ __forceinline__ void split_weights(float a, float b, uint32_t &hi, uint32_t &lo) {
-  const uint32_t w = f16x2_of_floats(a, b);
-  hi = e4m3x2_of_f16x2(w);
-  lo = e4m3x2_of_f16x2(mul_f16x2(sub_f16x2(w, f16x2_of_e4m3x2(hi)), 0x50005000u));  // 32, 32
+// Four weights to the codes of their three numbers (see the top of the file): the upper bytes of their fp16 forms,
+// those of what these leave, and what both leave times 2^4, to the nearest code.
+__device__ __forceinline__ void split_weights(const float (&a)[4], uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  const uint32_t w0 = f16x2_of_floats(a[0], a[1]), w1 = f16x2_of_floats(a[2], a[3]);
+  auto upper = [](uint32_t x, uint32_t y) { return __byte_perm(x, y, 0x7531); };
+  auto rest = [](uint32_t x) { return sub_f16x2(x, x & 0xff00ff00u); };  // exact
+  hi = upper(w0, w1);
+  const uint32_t r0 = rest(w0), r1 = rest(w1);
+  mid = upper(r0, r1);
+  lo = e5m2x2_of_f16x2(mul_f16x2(rest(r0), 0x4c004c00u)) | e5m2x2_of_f16x2(mul_f16x2(rest(r1), 0x4c004c00u)) << 16;  // 16, 16
 }
+constexpr float kLastPart = 0.0625f;  // the third number's unit
+constexpr int kWeightUnit = 11;       // a weight of 1 as a code: 2^11
 
 // This thread's share of a segment's rows of Q, eight threads a row, 16 rows from
 // col0 + h on: asked for, and brought to shared memory as codes of two numbers.
@@ -466,7 +483,7 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
   const int col0 = kTurns ? 0 : gi * C, id = 1 + gi;
   const bool brings_q = !kTurns || gi == 0;
   const uint32_t lane_off = static_cast<uint32_t>(32 * w) << 16;
-  const uint32_t o_addr = tmem + lane_off + 2 * sh.N + col0 + (kTurns ? gi * 2 * sh.N : 0);
+  const uint32_t o_addr = tmem + lane_off + 2 * sh.N + col0 + (kTurns ? gi * L::kOStep : 0);
   auto product_done = [&](uint32_t s) {  // of key tile s, and so of all before it
     return __all_sync(0xffffffffu, mbar_wait(bar(L::kPvDone + (s & 1u)), (s >> 1) & 1u, abort_flag, err));
   };
@@ -474,7 +491,11 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
   auto sum_of = [](float a, float b) { return a + b; };
   const Reductions<C> mine(reds + 256 * gi);
   const float *back = Reductions<C>(reds + (kTurns ? 0 : 256 * gi)).back;
-  constexpr float kMost = 4.f;  // 2^4: how far a weight may pass the reference; 2^4 more is in the weights' codes
+  // In powers of two: how far w may pass 1 (fp16 ends at 2^5 of it); how far 2^(s - m) may, as much as a value's scale
+  // counts in the reference at most; and how far a reference may fall behind its highest, as it does when E
+  // rises. Together they hold l, of up to 2^30 keys, below 2^126.
+  constexpr float kMost = 4.f, kFar = 48.f;
+  constexpr int kFall = 48;
   paged::RingPos k{0, 0};       // of the segment's first K tile
   uint32_t first_step = 0;      // key tiles of the segments before
   uint32_t nq = 0;
@@ -517,6 +538,7 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
     for (int c = 0; c < C; ++c) l[c] = 0.f;
     if (key < C) mine.ref[key] = paged::kNoReference;
     int top_e = kNoExponent;  // E
+    float highest = paged::kNoReference;  // of the reference of column `key`
     bool ok = true;
     // `back` is there
     if (kTurns && gi != 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kQFull), nq & 1u, abort_flag, err));
@@ -562,34 +584,41 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
       float x[C];
       float top = -INFINITY;
       const bool begun = j > j_first;  // O holds a sum of tiles before
-      if (begun) {
 #pragma unroll
-        for (int h = 0; h < C; h += 16) {
-          load_scores(h, true, x + h);
+      for (int h = 0; h < C; h += 16) {
+        load_scores(h, true, x + h);
 #pragma unroll
-          for (int c = 0; c < 16; c += 2) top = fmax3(top, x[h + c], x[h + c + 1]);
-        }
+        for (int c = 0; c < 16; c += 2) top = fmax3(top, x[h + c], x[h + c + 1]);
       }
-      // the first tile of a segment has no reference yet
-      if (!begun || !named_bar_and(id, 128, ok && !(top > kMost) && e <= top_e)) {
-        // maxima of the tile's 128 keys and of its values' exponents, then O and l onto the new references
+      const bool seen = top > -INFINITY;  // by a row of these
+      const bool fits = !(top + static_cast<float>(e - top_e) > kMost || top > kFar || (seen && e - top_e > 100));
+      // the first tile of a segment has no reference yet (its scores were only looked at for masks)
+      if (!begun || !named_bar_and(id, 128, ok && fits)) {
+        // the largest exponent of the values that a row sees, then the maxima of s + e - E over the tile's 128 keys, then
+        // O and l onto the new references
+        const int warp_e = __reduce_max_sync(0xffffffffu, seen ? e : kNoExponent);
+        if (lane == 0) mine.tops[w] = warp_e;
+        named_bar_sync(id, 128);
+        const int new_e = max(top_e, max(max(mine.tops[0], mine.tops[1]), max(mine.tops[2], mine.tops[3])));
+        const float less_e = fmaxf(static_cast<float>(e - new_e), -kFar);
 #pragma unroll
         for (int h = 0; h < C; h += 16) {
           float y[16];
           load_scores(h, false, y);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) y[c] += less_e;
           const float most = paged::reduce16(y, larger);
           if (!(lane & 1)) mine.red[w * C + h + (lane >> 1)] = most;
         }
-        const int warp_e = __reduce_max_sync(0xffffffffu, e);
-        if (lane == 0) mine.tops[w] = warp_e;
         named_bar_sync(id, 128);
         if (key < C) {
           const float most = fmaxf(fmaxf(mine.red[key], mine.red[C + key]), fmaxf(mine.red[2 * C + key], mine.red[3 * C + key]));
-          const float old_ref = mine.ref[key], new_ref = fmaxf(old_ref, most);
+          const float old_ref = mine.ref[key];
+          const float new_ref = fmaxf(fmaxf(most, highest - kFall), old_ref + static_cast<float>(max(top_e - new_e, -kFall)));
+          highest = fmaxf(highest, new_ref);
           mine.ref[key] = new_ref;
           mine.factor[key] = ex2_approx(old_ref - new_ref);
         }
-        const int new_e = max(top_e, max(max(mine.tops[0], mine.tops[1]), max(mine.tops[2], mine.tops[3])));
         const float down = two_to(top_e - new_e);  // what a larger exponent takes from O
         top_e = new_e;
         ok = named_bar_and(id, 128, ok);
@@ -606,7 +635,7 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
           }
           if (old) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
+            for (int part = 0; part < 3; ++part) {
               uint32_t v[16];
               const uint32_t o = o_addr + part * sh.N + h;
               tmem_ld16(o, v);
@@ -620,34 +649,34 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
         }
         if (old) tmem_st_wait();
       }
-      const float fw = there ? two_to(e - top_e + 4) : 0.f;
-      uint32_t hi[C / 4], lo[C / 4];
+      const float fw = seen ? two_to(e - top_e + kWeightUnit) : 0.f;
+      const uint32_t p_key = smem + sh.p_at() + (sh.N == 16 ? 0u : (step & 1u) * sh.p_step()) + key * 128;
+      const int first = sh.N == 16 ? static_cast<int>(step & 1u) * 64 : 0;
 #pragma unroll
-      for (int i = 0; i < C; i += 4) {
-        float a[4];
+      for (int h = 0; h < C; h += 16) {
+        uint32_t part[3][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          a[c] = ex2_approx(x[i + c]);
-          l[i + c] += a[c];
+        for (int i = 0; i < 16; i += 4) {
+          float a[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            a[c] = ex2_approx(x[h + i + c]);
+            l[h + i + c] += a[c];
+            a[c] *= fw;
+          }
+          split_weights(a, part[0][i / 4], part[1][i / 4], part[2][i / 4]);
         }
-        uint32_t h0, l0, h1, l1;
-        split_weights(a[0] * fw, a[1] * fw, h0, l0);
-        split_weights(a[2] * fw, a[3] * fw, h1, l1);
-        hi[i / 4] = h0 | h1 << 16;
-        lo[i / 4] = l0 | l1 << 16;
+        // the product of the tile before the last has read its P
+        if (h == 0 && step >= 2) ok = ok && product_done(step - 2);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+          const int byte = first + n * sh.N + col0 + h;  // of the key's row, or past it of the next block's
+          if (ok)
+            st_shared_v4(p_key + (byte >> 7) * L::kPBytes + (static_cast<uint32_t>((byte >> 4 & 7) ^ (key & 7)) << 4), part[n][0],
+                         part[n][1], part[n][2], part[n][3]);
+        }
       }
-      // the product of the tile before the last has read its P
-      if (step >= 2) ok = ok && product_done(step - 2);
       if (ok) {
-        const uint32_t p_key = smem + sh.p_at() + (sh.N == 64 ? (step & 1u) * L::kPBytes : 0u) + key * 128;
-        const int piece = (col0 + (sh.N == 64 ? 0 : static_cast<int>(step & 1u) * 2 * sh.N)) / 16;
-#pragma unroll
-        for (int i = 0; i < C / 16; ++i) {
-          st_shared_v4(p_key + (static_cast<uint32_t>((piece + i) ^ (key & 7)) << 4), hi[4 * i], hi[4 * i + 1], hi[4 * i + 2],
-                       hi[4 * i + 3]);
-          st_shared_v4(p_key + (static_cast<uint32_t>((piece + sh.N / 16 + i) ^ (key & 7)) << 4), lo[4 * i], lo[4 * i + 1],
-                       lo[4 * i + 2], lo[4 * i + 3]);
-        }
         const paged::RingPos v = at.next(sh.stages);
         if ((kTurns || gi == 0) && g.s.kv_len - kv0 < kRowsPerTile)
           ok = clear_tail8<D>(g.s.kv_len - kv0, smem + v.slot * Cfg8<D>::kTileBytes, bar(L::kFull + v.slot), v.phase, abort_flag,
@@ -717,9 +746,9 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
       }
     }
     named_bar_sync(id, 128);
-    // O back from 2^(4 - E), in two steps as that may leave the range of one number
+    // O back from 2^(kWeightUnit - E), in two steps as that may leave the range of one number
     auto halves = [](int e, float &a, float &b) {
-      const int unit = max(e, -200) - 4;
+      const int unit = max(e, -200) - kWeightUnit;
       a = two_to(unit / 2);
       b = two_to(unit - unit / 2);
     };
@@ -735,25 +764,22 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
 #pragma unroll 1
     for (int h = 0; h < n_rows; h += 8) {
       float o[8];
-      uint32_t v[8], u[8];
-      if (!kTurns || any) {
-        tmem_ld8(o_addr + h, v);
-        tmem_ld8(o_addr + sh.N + h, u);
-        tmem_ld_wait(v);
-        tmem_ld_wait(u);
-      }
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        o[c] = !kTurns || any ? fmaf(__uint_as_float(u[c]), 0.03125f, __uint_as_float(v[c])) * mine.factor[h + c] * up0 * up1 : 0.f;
-      if (kTurns && (both || !any)) {
-        tmem_ld8(o_addr + 2 * sh.N + h, v);
-        tmem_ld8(o_addr + 3 * sh.N + h, u);
+      for (int c = 0; c < 8; ++c) o[c] = 0.f;
+      auto add = [&](uint32_t at, const float *factor, float a, float b) {
+        uint32_t v[8], u[8], t[8];
+        tmem_ld8(at + h, v);
+        tmem_ld8(at + sh.N + h, u);
+        tmem_ld8(at + 2 * sh.N + h, t);
         tmem_ld_wait(v);
         tmem_ld_wait(u);
+        tmem_ld_wait(t);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          o[c] += fmaf(__uint_as_float(u[c]), 0.03125f, __uint_as_float(v[c])) * other.factor[h + c] * other0 * other1;
-      }
+          o[c] += fmaf(__uint_as_float(t[c]), kLastPart, __uint_as_float(v[c]) + __uint_as_float(u[c])) * factor[h + c] * a * b;
+      };
+      if (!kTurns || any) add(o_addr, mine.factor, up0, up1);
+      if (kTurns && (both || !any)) add(o_addr + L::kOStep, other.factor, other0, other1);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         if (h + c < n_rows && key < D) {

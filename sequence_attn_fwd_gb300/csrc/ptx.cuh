@@ -345,6 +345,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_ma
   return idesc_e4m3_f32(M, N) | (a_mn_major ? 1u << 15 : 0u) | (b_mn_major ? 1u << 16 : 0u);
 }
 
+// e4m3 A, e5m2 B (the 8-bit instructions take each operand's type by itself).
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_e4m3_f32(M, N, a_mn_major, b_mn_major) | (1u << 10);
+}
+
 // Instruction descriptor, kind::f16: f16 A and B (format 0), fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -395,6 +400,13 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two fp16 numbers to e5m2, which is fp16's upper byte, rounded to nearest.
+__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
   return r;
 }
 

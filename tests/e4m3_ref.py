@@ -1,0 +1,65 @@
+"""Bounds of the attention over the 8-bit cache that follow its weights one by one (drafts_ref.attention grants a floor
+that grows with the keys).
+
+Narrow form (at most 64 rows a KV head). A weight with its value's scale, W = 2^(s + e), against a reference R with W <= 2^4 R,
+is rounded to fp16 (2^-11 of itself) and then held as three e5m2 numbers: upper byte, upper byte of the rest, the rest of that
+to nearest times 2^4. Each takes three bits, so 2^-9 is off at most; below, half of e5m2's smallest step, 2^-17 / 2^4, where R is
+2^11: 2^-32 R. R is no more than the row's largest W -- or, of values that differ by more than 2^48, 2^(E - 48) times its largest
+2^s, E the largest exponent of the values that its sequence's rows see.
+Wide form. Weights 2^s are rounded to fp16 (2^-11), below half of its smallest step, 2^-25, where the reference is 2^7; and a tile
+of 128 keys whose weights sum to less than 2^-6 of the reference lowers it. Values are exact unless their exponent lies more than
+13 below the largest of their tile of 128; then half of a step of 2^-24, in units of at most four times the largest scale: 2^-23
+of that.
+Both. Scores as in drafts_ref.attention; keys of the wide form whose exponent lies more than 15 below the tile's largest are off
+by 2^-25 of the largest scale."""
+import math
+
+import torch
+
+from tests.paged_ref import BF16_HALF, F32_HALF
+
+U8 = torch.uint8
+
+
+def exponents(scales):
+    return scales.view(U8).double() - 127
+
+
+def attention(q, k, v, ek, ev, codes, seen, scale, wide, at=None):
+    """One sequence and KV head, on any device, in 64 bits: q [R, D], values k, v [n, D], exponents ek, ev [n], codes of v [n, D],
+    seen [R, n] -> O, its bound, lse, its bound. at [n]: the keys' places in the sequence (0 .. n - 1 if not given)."""
+    q, k, v, ek, ev, codes = (x.double() for x in (q, k, v, ek, ev, codes))
+    n, D = k.shape
+    tile = (torch.arange(n, device=k.device) if at is None else at) // 128
+    n_tiles = int(tile.max()) + 1 if n else 0
+    most = lambda x: torch.full((n_tiles,), -1e4, dtype=torch.float64, device=x.device).scatter_reduce_(0, tile, x, "amax")[tile]  # noqa: E731
+    s = q @ k.T * scale
+    ds = 1.25 * (2 * D + 2) * F32_HALF * scale * (q.abs() @ k.abs().T)
+    ds = ds + 2.0 ** -17 * scale * q.abs().amax(-1, keepdim=True) * k.abs().sum(-1)
+    if wide:
+        far = torch.where(ek < most(ek) - 15, 2.0 ** (most(ek) - 25), 0.0)
+        ds = ds + scale * q.abs().sum(-1, keepdim=True) * far
+    s = torch.where(seen, s, -math.inf)
+    some = seen.any(-1)
+    z = torch.where(some, torch.logsumexp(s, -1), -math.inf)
+    z0 = torch.where(some, z, 0.0)
+    w = torch.exp(s - z0[:, None])
+    o = w @ v
+    rel = 2 * torch.where(seen, ds, 0.0).amax(-1) + 2.0 ** -17 + 2 * n * F32_HALF + 2.0 ** -20
+    tol = (w @ v.abs()) * rel[:, None] * (1 + BF16_HALF)
+    if wide:
+        tol = tol + (w @ v.abs()) * (2.0 ** -11 * (1 + BF16_HALF))
+        sums = torch.zeros((q.shape[0], n_tiles), dtype=torch.float64, device=k.device).index_add_(1, tile, w)
+        sizes = torch.zeros((n_tiles, D), dtype=torch.float64, device=k.device)
+        # (a key that a row does not see has no weight; counting its value only widens the bound)
+        sizes.index_add_(0, tile, v.abs())
+        tol = tol + 2.0 ** (-32 + 6) * (sums @ sizes)
+        small = torch.where(ev < most(ev) - 13, 2.0 ** (most(ev) - 23), 0.0)
+        tol = tol + (w @ small)[:, None]
+    else:
+        tol = tol + (w @ v.abs()) * ((2.0 ** -9 + 2.0 ** -11) * (1 + BF16_HALF))
+        top_e = ev[seen.any(0)].amax() if bool(seen.any()) else 0.0
+        unit = torch.maximum((w * 2.0 ** ev).amax(-1), w.amax(-1) * 2.0 ** (top_e - 48))
+        tol = tol + 2.0 ** -32 * (1 + 2.0 ** -3) * unit[:, None] * (seen.double() @ codes.abs())
+    tol = tol + BF16_HALF * o.abs() + 1e-30
+    return o, tol, z, rel + 8 * F32_HALF * z0.abs() + 2.0 ** -20

@@ -1,11 +1,17 @@
-"""The 8-bit cache where its kernels hand work from one warpgroup to the other."""
+"""The 8-bit cache where its kernels hand work from one warpgroup to the other, and where weights and values lie far
+apart (bounds: e4m3_ref.py)."""
+import math
+
 import pytest
 import torch
 
+from tests import drafts_ref, e4m3_ref
 from tests.test_gpu_drafts import Cache, queries, sa  # noqa: F401
 from tests.test_gpu_paged import i32
 
 pytestmark = pytest.mark.gpu
+BF, I32, U8 = torch.bfloat16, torch.int32, torch.uint8
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
 @pytest.mark.parametrize("D,G,q_len", [(128, 1, 1), (128, 4, 3), (64, 16, 1), (64, 2, 8)])
@@ -24,3 +30,126 @@ def test_items_joined_by_one_warpgroup_for_both(sa, D, G, q_len):  # noqa: F811
     pick = torch.cat([torch.arange(b * q_len, (b + 1) * q_len) for b in few]).cuda()
     c.table, c.lens, c.cu = c.table[few], c.lens[few], i32([i * q_len for i in range(len(few) + 1)])
     c.check((first[0][:, pick], first[1][:, pick]), q[:, pick])
+
+
+class OneContext:
+    """A context of n keys that B sequences share, page by page, so that an item of one CTA goes through all of it: keys and
+    values in fp64 [Hkv, n, D], as codes in the pools, and B * q_len queries with a common direction, which no key has a
+    part in until one is given it."""
+
+    def __init__(self, n, B, q_len, G, D, Hkv=2, seed=0):
+        g = torch.Generator().manual_seed(seed)
+        self.n, self.B, self.q_len, self.G, self.Hkv, self.D = n, B, q_len, G, Hkv, D
+        self.u = torch.ones(D, dtype=torch.float64) / math.sqrt(D)
+        k, self.v = (torch.randn((Hkv, n, D), generator=g).double() for _ in range(2))
+        self.k = k - (k @ self.u)[..., None] * self.u
+        q = torch.randn((B * q_len, Hkv * G, D), generator=g).double()
+        q = q - (q @ self.u)[..., None] * self.u + math.sqrt(D) * self.u
+        self.q = q.to(BF).cuda().transpose(0, 1)
+        self.order = torch.randperm(n // 16, generator=g)
+
+    def raise_key(self, i, nats):
+        """Key i's score of every row is about `nats` (others: normal, about 1)."""
+        self.k[:, i] = self.u * nats
+
+    def fill(self):
+        pools, scales, self.values, self.exps, self.codes = [], [], [], [], []
+        for x in (self.k, self.v):
+            codes, sc = drafts_ref.quantise(x)
+            self.values.append(drafts_ref.values(codes, sc).cuda())
+            self.exps.append(e4m3_ref.exponents(sc).cuda())
+            self.codes.append(codes.float().cuda())
+            p = torch.empty((self.n // 16, self.Hkv, 16, self.D), dtype=U8)
+            p[self.order] = codes.view(U8).reshape(self.Hkv, -1, 16, self.D).transpose(0, 1)
+            s = torch.empty((self.n // 16, self.Hkv, 16), dtype=U8)
+            s[self.order] = sc.view(U8).reshape(self.Hkv, -1, 16).transpose(0, 1)
+            pools.append(p.cuda().view(E4M3))
+            scales.append(s.cuda().view(E8M0))
+        self.pools, self.kw = pools, {"k_scales": scales[0], "v_scales": scales[1]}
+        self.table = self.order.to(I32).repeat(self.B, 1).cuda()
+        self.lens, self.cu = i32([self.n] * self.B), i32([b * self.q_len for b in range(self.B + 1)])
+
+    def check(self, sa, picked=(0, 17), tree=None, seen_new=None, least=2.0 ** -7):  # noqa: F811
+        """Every element within its bound; and a row's error, as a whole, within `least` of the row: a weight's rounding error of
+        at most 2^-9, of either sign, adds up over keys as the row itself does, to about 2^-10 of it, the row's own rounding
+        is as much again, and what a form loses of a score far above 1 less; 2^-7 is four times all of it."""
+        o, lse = sa.attn_paged(self.q, *self.pools, self.table, self.lens, self.cu, tree=tree, **self.kw)
+        again = sa.attn_paged(self.q, *self.pools, self.table, self.lens, self.cu, tree=tree, **self.kw)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+        draft = torch.arange(self.n, device="cuda") - (self.n - self.q_len)
+        own = torch.ones((self.q_len, self.q_len), dtype=torch.bool).tril().cuda() if seen_new is None else seen_new
+        seen = (draft < 0)[None, :] | own[:, draft.clamp(min=0)]
+        seen = seen.repeat_interleave(self.G, 0)
+        wide = self.q_len * self.G > 64
+        for b in picked:
+            for h in range(self.Hkv):
+                heads, rows = slice(h * self.G, (h + 1) * self.G), slice(b * self.q_len, (b + 1) * self.q_len)
+                flat = lambda x: x[heads, rows].transpose(0, 1).reshape(self.q_len * self.G, *x.shape[2:]).double()  # noqa: E731
+                r = e4m3_ref.attention(flat(self.q), self.values[0][h], self.values[1][h], self.exps[0][h], self.exps[1][h],
+                                       self.codes[1][h], seen, 1 / math.sqrt(self.D), wide)
+                got, got_lse = flat(o), flat(lse)
+                assert ((got - r[0]).abs() <= r[1]).all(), float(((got - r[0]).abs() / r[1]).max())
+                assert ((got_lse - r[2]).abs() <= r[3]).all()
+                off = (got - r[0]).norm(dim=-1) / r[0].norm(dim=-1).clamp(min=1e-300)
+                assert (off <= least).all(), float(off.max())
+
+
+# rows of a KV head in each width of the narrow form: 1 and 16 (tiles in turn), 32, 64
+FORMS = [(1, 1), (4, 4), (2, 16), (8, 8)]
+
+
+@pytest.mark.parametrize("q_len,G", FORMS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,nats,size", [(8192, 12.0, 0.0), (16384, 14.0, 2.0 ** -10), (65536, 16.0, 0.0), (4096, 10.0, 0.01),
+                                         (16384, 20.0, 0.0)])
+def test_a_first_key_that_takes_most_of_the_weight(sa, q_len, G, D, n, nats, size):  # noqa: F811
+    """A sink: its value is small or zero, and what the other keys' small weights bring is the answer."""
+    c = OneContext(n, 200, q_len, G, D, seed=n + D)
+    c.raise_key(0, nats)
+    c.v[:, 0] *= size
+    c.fill()
+    c.check(sa)
+
+
+@pytest.mark.parametrize("q_len,G", FORMS)
+@pytest.mark.parametrize("bits", [8, 12, 20])
+@pytest.mark.parametrize("sink", [None, 13.0])
+def test_one_value_far_larger_than_the_others_and_of_no_weight(sa, q_len, G, bits, sink):  # noqa: F811
+    """Its scale must not take bits from the other keys, in its own tile and behind it, with a sink and without."""
+    c = OneContext(16384, 200, q_len, G, 128, seed=bits)
+    for i in (37, 5000):
+        c.raise_key(i, -120.0)
+        c.v[:, i] *= 2.0 ** bits
+    if sink is not None:
+        c.raise_key(0, sink)
+        c.v[:, 0] = 0
+    c.fill()
+    c.check(sa)
+
+
+@pytest.mark.parametrize("q_len,G", FORMS)
+def test_weights_that_fall_and_rise_over_the_tiles(sa, q_len, G):  # noqa: F811
+    """Tiles of large and of small weights in turn, the large ones with values of next to nothing; sizes of values that
+    come and go."""
+    c = OneContext(8192, 200, q_len, G, 128, seed=5)
+    for t in range(0, 64, 3):
+        c.raise_key(128 * t + 11, 9.0 + t / 8)
+        c.v[:, 128 * t + 11] *= 2.0 ** -30
+    for t in range(64):
+        c.v[:, 128 * t:128 * t + 128] *= 2.0 ** (-14 if t % 7 == 3 else 0)
+    c.fill()
+    c.check(sa)
+
+
+@pytest.mark.parametrize("q_len,G,bits", [(4, 4, 12), (4, 4, 60), (8, 8, 12), (8, 8, 60)])
+def test_drafts_of_another_branch_take_no_bits(sa, q_len, G, bits):  # noqa: F811
+    """The second half of the drafts has values far larger than all others; the first half does not see them."""
+    c = OneContext(2048, 200, q_len, G, 128, seed=bits)
+    half, first = q_len // 2, c.n - q_len
+    c.v[:, first + half:] *= 2.0 ** bits
+    c.fill()
+    own = torch.zeros((q_len, q_len), dtype=torch.bool)
+    own[:half, :half] = torch.ones((half, half), dtype=torch.bool).tril()
+    own[half:, half:] = torch.ones((q_len - half, q_len - half), dtype=torch.bool).tril()
+    bits_of = [[sum(1 << i for i in range(q_len) if own[t, i])] for t in range(q_len)] * c.B
+    c.check(sa, tree=torch.tensor(bits_of, dtype=torch.int64).cuda(), seen_new=own.cuda())
