@@ -994,8 +994,10 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, Items ite
         if (kCodes || j > 0) {
           // as in the dense forward: the reference moves, and O with it, only
           // when the tile's P would sum to more than 2^8
-          const bool big = row_valid && !(rowsum <= kRescaleSum);
-          if (__any_sync(0xffffffffu, big) || (kCodes && (first || units.down != 1.f))) {
+          // (kCodes: or to so little that its fp16 weights would lack bits)
+          const bool big = row_valid && !(rowsum <= (kCodes ? codes::kMostSum : kRescaleSum));
+          const bool small = kCodes && row_valid && rowsum < codes::kLeastSum && rowsum > 0.f;
+          if (__any_sync(0xffffffffu, big || small) || (kCodes && (first || units.down != 1.f))) {
             float mx = -INFINITY;  // 32 columns at a time: few live registers
 #pragma unroll 1
             for (int cb = 0; cb < 4; ++cb) {
@@ -1006,7 +1008,9 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, Items ite
 #pragma unroll
               for (int c = 0; c < 32; ++c) mx = fmaxf(mx, __uint_as_float(x[c]));
             }
-            const float m_new = fmaxf(m, scaled(mx));
+            const float headroom = !kCodes ? 0.f : (j == 0 ? codes::kFirstHeadroom : codes::kHeadroom);
+            const float least = small ? m + log2f(l) - codes::kMostL : m;
+            const float m_new = fmaxf(least, scaled(mx) - headroom);
             const float alpha = (m_new == -INFINITY) ? 1.f : ex2_approx(m - m_new);
             m = m_new;
             l *= alpha;

@@ -30,27 +30,38 @@ __device__ __forceinline__ float largest_of(const uint4 &x) {
 // 2^e for any e: 0 below the range of normal numbers.
 __device__ __forceinline__ float two_to(int e) { return ex2_approx(static_cast<float>(e)); }
 
-// What a tile's exponents make of it. K and V come in fp16, each tile in units of a
-// power of two of its own: `key` that of K; weights carry 2^shift, the unit of V over
-// that of O, in their reference, and their sum is brought back by `unshift`. O's unit is
-// that of the first tile, until a tile's is 2^7 larger (weights are below 2^8, fp16
-// ends below 2^16): then O is brought to it, by `down`.
+// What a tile's exponents make of it. K and V come in fp16, in units of powers of two:
+// `key` that of K, the tile's own; that of V, O's unit too, changes where the tiles'
+// largest scales leave its range (value_unit): `down` brings O along.
 struct TileUnits {
-  float key, shift, unshift, down;
+  float key, down;
 };
 constexpr int kExponents = 32;   // places for the exponents of ring positions
-constexpr int kMaxShift = 7, kMinShift = -12;
 __device__ __forceinline__ TileUnits tile_units(const volatile int *exps, int cv, bool first, int &e_ref) {
   const int ek = exps[(cv - 1) % kExponents], ev = exps[cv % kExponents];
-  int shift = ev - e_ref;
-  float down = 1.f;
-  if (first || shift > kMaxShift) {
-    if (!first) down = two_to(-shift);
-    e_ref = ev;
-    shift = 0;
-  }
-  return {two_to(ek), static_cast<float>(shift), two_to(-shift), down};
+  const float down = first ? 1.f : two_to(e_ref - ev);
+  e_ref = ev;
+  return {two_to(ek), down};
 }
+// The unit's exponent for a tile of V whose largest scale is 2^e, behind one of `unit`, the largest so far
+// `most`: the same for a few sizes. Codes end at 2^9 and fp16 at 2^16, so there are seven
+// bits above; and down to 2^-2 of it nothing that fp16 ends with is missed. (2^40 below the
+// largest at the least, as O holds it, too.)
+constexpr int kAbove = 7, kBelow = 2, kChosen = 4, kUnitFall = 40;
+__device__ __forceinline__ int value_unit(int e, int unit, int most, bool first) {
+  if (!first && e <= unit + kAbove && e >= unit - kBelow) return unit;
+  return first ? e - kChosen : max(e - kChosen, most - kUnitFall);
+}
+// A row's weights are against a reference 2^kHeadroom below its largest score. Sums of a
+// tile's weights up to kMostSum, 2^15 of fp16, are let by. Sums below kLeastSum bring the
+// reference down, so that what the keys behind an attention sink bring, a little each, keeps
+// its bits: fp16 ends in steps of 2^-24, so a weight is held to 2^-11 of itself or to 2^-18 of its
+// tile's sum. References fall as far as l stays below 2^kMostL. A segment's first tile has
+// kFirstHeadroom: the keys beside a sink at the start of a context have no other tile to be held in.
+// (1,024 tokens behind 65,536 keys of sizes 2^-1.5 to 2^1.5, and a batch of prompt pieces with heads
+// of 64: with both 7, 7, 6, 5, 3: 968, 898, 880, 869, 855 us and 236, 203, 192, 184, 183, the first with
+// kLeastSum 2; 5 and 13: 868 and 201.)
+constexpr float kHeadroom = 5.f, kFirstHeadroom = 13.f, kMostSum = 32768.f, kLeastSum = 0.0078125f, kMostL = 57.f;
 // O from units of 2^e: 1 / l times two factors, as 2^e may leave the range of one.
 __device__ __forceinline__ void units_back(int e, float &inv_l, float &back) {
   const int half = e / 2;
@@ -58,8 +69,8 @@ __device__ __forceinline__ void units_back(int e, float &inv_l, float &back) {
   back = two_to(e - half);
 }
 
-// The weights of a row's 128 scores, times 2^shift, packed as fp16 pairs; returns
-// the fp32 sum of the weights. x = s unit key - ref, fused, or, kApart, with the second
+// The weights of a row's 128 scores, packed as fp16 pairs; returns the fp32 sum of the
+// weights. x = s unit key - ref, fused, or, kApart, with the second
 // product exact and the first rounded as in the reference: then a score that is the
 // reference comes out as 0 however large it is. (Scores past 2^24 have no more
 // than whole powers of two between them; fused, the sum passes its bound there and the
@@ -82,7 +93,7 @@ __device__ __forceinline__ float weights_row(const float *s, float unit, float k
     float p0, p1, p2, p3;
     f2_unpack(pa, p0, p1);
     f2_unpack(pb, p2, p3);
-    // fp16: 2^-11 of a weight, and nothing of the largest that bf16 outputs would show
+    // fp16: 2^-11 of a weight, or 2^-18 of their sum (kLeastSum)
     pk[q] = f16x2_of_floats(p0, p1);
     pk[q + 1] = f16x2_of_floats(p2, p3);
   }
@@ -93,7 +104,7 @@ __device__ __forceinline__ float weights_row(const float *s, float unit, float k
 }
 template <bool kApart>
 __device__ __forceinline__ float weights(const float *s, float unit, const TileUnits &u, float ref, uint32_t (&pk)[64]) {
-  return weights_row<kApart>(s, unit, u.key, ref - u.shift, pk) * u.unshift;
+  return weights_row<kApart>(s, unit, u.key, ref, pk);
 }
 
 // This thread's row of a query tile (first: the tile's first token) to shared

@@ -24,15 +24,16 @@
 //     177 us, now 183, trees of up to 64 rows 143, now 151; but a first key of 12 nats
 //     above 8,191 others left 0.1 of their answer lost.)
 // Wide form (compute bound), in fp16, which holds codes and ratios of scales: warps of their
-// own turn K and V tiles, each to units of the tile's largest scale, on their way into the ring of
-// the bf16 form; Q goes there after its rows' powers of two. The softmax has two factors
-// more a tile and none an element. (Scales applied to scores and weights by the softmax
+// own turn K and V tiles, K to units of the tile's largest scale, V to a unit that fits many tiles
+// (value_unit), on their way into the ring of the bf16 form; Q goes there after its rows'
+// powers of two. The softmax has a factor more a tile and none an element, and references
+// that fall as well as rise, as fp16's weights need (kLeastSum). (Scales applied to scores and weights by the softmax
 // warps instead, read from shared memory: 6,700 clocks a pair of tiles, 1,554 us for
 // 1,024 tokens behind 65,536 keys.)
 //
 // Measured (GB300): 64 sequences' next tokens over 300 to 16,000 keys (1.06 GB, 8 KV
 // heads of 128) 183 us = 5.8 TB/s; 1,024 tokens behind 65,536 keys, 32 heads over 8 of
-// 128, 911 us = 1,216 TFLOP/s.
+// 128, 868 us = 1,276 TFLOP/s.
 #pragma once
 
 namespace seqattn {
@@ -808,8 +809,6 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
 // for V, 8,000 by bulk copies through shared memory, 500 to start one, 5,700 by
 // asynchronous ones; code longer than the instruction caches hold, all of a tile
 // unrolled in two roles, 24,000.)
-constexpr int kNoKey = -126;  // exponent of a tile without a key
-
 template <int D>
 struct Turner {
   static constexpr int kRows = 512 / D;  // rows of a warp's access: 512 bytes
@@ -821,7 +820,7 @@ struct Turner {
 
   bool word;          // scales can be read four at a time
   uint32_t bytes;     // scale bytes of keys 4 lane .. 4 lane + 3 of the next tile, 0: not there
-  int e;              // the tile's exponent
+  int e, largest;     // the exponent of the tile's unit; V: the largest of the segment
   __device__ __forceinline__ Turner(const PagedAttnParams &p_, bool values, int half_, uint32_t place_, uint32_t factors_)
       : p(p_), pool(static_cast<const unsigned char *>(values ? p.cache.v_pages : p.cache.k_pages)),
         scales(values ? p.scales.v : p.scales.k), lane(threadIdx.x & 31), half(half_), place(place_), factors(factors_) {
@@ -850,8 +849,9 @@ struct Turner {
       }
     }
   }
-  // The factors 2^(e_key - e) of the tile whose scales were loaded, e at least `least`.
-  __device__ __forceinline__ void take_scales(int valid, int least) {
+  // The factors 2^(e_key - e) of the tile whose scales were loaded: for K e is the largest exponent (-126 without a key), for V
+  // value_unit makes it of that.
+  __device__ __forceinline__ void take_scales(int valid, bool values, bool first) {
     int b[4], most = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -859,11 +859,17 @@ struct Turner {
       if (4 * lane + i < valid) most = max(most, b[i]);  // (those past the end may be anything)
     }
     most = __reduce_max_sync(0xffffffffu, most);
-    e = max(max(most, 1) - 127, least);
+    const int top = max(most, 1) - 127;
+    if (!values) {
+      e = top;
+    } else if (first || most > 0) {  // (a tile without a key leaves the unit)
+      e = paged::codes::value_unit(top, e, largest, first);
+      largest = first ? e : max(largest, e);
+    }
     uint32_t f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float x = fminf(two_to(max(b[i], 1) - 127 - e), 1.f);
+      const float x = fminf(two_to(max(b[i], 1) - 127 - e), static_cast<float>(1 << paged::codes::kAbove));
       f[i] = f16x2_of_floats(x, x);
     }
     if (4 * lane >= half && 4 * lane < half + 64) st_shared_v4(factors + 4 * (4 * lane - half), f[0], f[1], f[2], f[3]);
@@ -972,14 +978,12 @@ __device__ __forceinline__ void wide_turner(bool values, int half, const PagedAt
     int page = pages.page(p, j0), valid = kv_len - j0 * kRowsPerTile;
     t.load_scales(page, j0, valid);
     t.fetch(page, j0, valid);
-    int run = kNoKey;  // V: the largest exponent so far
     // the factors of a tile, its exponent where the softmax finds it
-    auto take = [&](int at) {
-      t.take_scales(valid, values ? run + paged::codes::kMinShift : kNoKey);
-      if (values) run = max(run, t.e);
+    auto take = [&](int at, bool first) {
+      t.take_scales(valid, values, first);
       if (lane == 0) exps[at % paged::codes::kExponents] = t.e;  // (both halves' warps the same)
     };
-    take(values ? c + 1 : c);
+    take(values ? c + 1 : c, true);
 #pragma unroll 1
     for (int j = 0; j < n; ++j, c += 2) {
       const int at = c + (values ? 1 : 0), slot = at % C::kStages;
@@ -998,7 +1002,7 @@ __device__ __forceinline__ void wide_turner(bool values, int half, const PagedAt
       __syncwarp();  // (the codes and factors have been read, too)
       // the next tile's exponent before this tile: the softmax needs that of V, whose slot
       // is free only behind the product before, ahead of the scores' way through it
-      if (more) take(at + 2);
+      if (more) take(at + 2, false);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(W::kFull + slot));
       if (more) t.fetch(page, j0 + j + 1, valid);

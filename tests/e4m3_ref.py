@@ -6,8 +6,9 @@ is rounded to fp16 (2^-11 of itself) and then held as three e5m2 numbers: upper 
 to nearest times 2^4. Each takes three bits, so 2^-9 is off at most; below, half of e5m2's smallest step, 2^-17 / 2^4, where R is
 2^11: 2^-32 R. R is no more than the row's largest W -- or, of values that differ by more than 2^48, 2^(E - 48) times its largest
 2^s, E the largest exponent of the values that its sequence's rows see.
-Wide form. Weights 2^s are rounded to fp16 (2^-11), below half of its smallest step, 2^-25, where the reference is 2^7; and a tile
-of 128 keys whose weights sum to less than 2^-6 of the reference lowers it. Values are exact unless their exponent lies more than
+Wide form. Weights 2^s are rounded to fp16 (2^-11), or by half of its smallest step, 2^-25, where a tile of 128 keys whose weights
+sum to less than 2^-7 gets a new reference, against which its largest weight is 2^5: 2^-18 of its sum. In the first tile the
+largest is 2^13: 2^-38 of it. Values are exact unless their exponent lies more than
 13 below the largest of their tile of 128; then half of a step of 2^-24, in units of at most four times the largest scale: 2^-23
 of that.
 Both. Scores as in drafts_ref.attention; keys of the wide form whose exponent lies more than 15 below the tile's largest are off
@@ -53,7 +54,9 @@ def attention(q, k, v, ek, ev, codes, seen, scale, wide, at=None):
         sizes = torch.zeros((n_tiles, D), dtype=torch.float64, device=k.device)
         # (a key that a row does not see has no weight; counting its value only widens the bound)
         sizes.index_add_(0, tile, v.abs())
-        tol = tol + 2.0 ** (-32 + 6) * (sums @ sizes)
+        floor = 2.0 ** -18 * sums
+        floor[:, 0] = 2.0 ** -38 * torch.where(tile == 0, w, 0.0).amax(-1)
+        tol = tol + floor @ sizes
         small = torch.where(ev < most(ev) - 13, 2.0 ** (most(ev) - 23), 0.0)
         tol = tol + (w @ small)[:, None]
     else:

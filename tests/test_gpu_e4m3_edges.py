@@ -94,8 +94,8 @@ class OneContext:
                 assert (off <= least).all(), float(off.max())
 
 
-# rows of a KV head in each width of the narrow form: 1 and 16 (tiles in turn), 32, 64
-FORMS = [(1, 1), (4, 4), (2, 16), (8, 8)]
+# rows of a KV head in each form: 1 and 16 (tiles in turn), 32, 64, and 160 (wide)
+FORMS = [(1, 1), (4, 4), (2, 16), (8, 8), (40, 4)]
 
 
 @pytest.mark.parametrize("q_len,G", FORMS)
@@ -141,7 +141,7 @@ def test_weights_that_fall_and_rise_over_the_tiles(sa, q_len, G):  # noqa: F811
     c.check(sa)
 
 
-@pytest.mark.parametrize("q_len,G,bits", [(4, 4, 12), (4, 4, 60), (8, 8, 12), (8, 8, 60)])
+@pytest.mark.parametrize("q_len,G,bits", [(4, 4, 12), (4, 4, 60), (8, 8, 12), (8, 8, 60), (40, 4, 12), (40, 4, 20)])
 def test_drafts_of_another_branch_take_no_bits(sa, q_len, G, bits):  # noqa: F811
     """The second half of the drafts has values far larger than all others; the first half does not see them."""
     c = OneContext(2048, 200, q_len, G, 128, seed=bits)
