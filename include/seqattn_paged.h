@@ -310,9 +310,17 @@ int attn_paged_e4m3(const void *q, long long q_head_stride, long long q_row_stri
  *   n_keep  int32 [B] (output): how many; 0 for a sequence without new tokens
  *   last    int32 [B] (output): the choice behind the last kept token, or -1
  * Rows of path of no sequence are left as they are.
+ *
+ * draft_accept follows trees of any size, as they are given. The attention does not: a
+ * sequence of more than 64 * tree_words tokens is a chain to it, and what the model chose
+ * behind a token of another branch was chosen behind all tokens before it.
+ * draft_accept_words takes such a sequence as the chain that it was attended as, whatever
+ * its parents: `words` is that of the attention's masks (0: none, as draft_accept).
  */
 int draft_accept(const int *parents, const int *cu_seqlens, const int *tokens, const int *choices, const int *given,
                  int *path, int *n_keep, int *last, int B, int total, attn_stream_t stream);
+int draft_accept_words(const int *parents, const int *cu_seqlens, const int *tokens, const int *choices, const int *given,
+                       int *path, int *n_keep, int *last, int B, int total, int words, attn_stream_t stream);
 
 /*
  * paged_keep -- of the last q_len(b) keys of row b, those of a step's new tokens, only

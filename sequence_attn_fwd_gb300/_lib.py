@@ -21,7 +21,7 @@ EXPORTS = ["attn_fwd", "attn_partial", "lse_merge", "attn_query_device_error",
 PAGED_EXPORTS = ["attn_paged", "attn_paged_workspace_bytes", "rope_axes", "paged_append", "paged_reserve",
                  "paged_free", "paged_fork", "paged_copy", "paged_compact", "paged_compact_workspace_bytes",
                  "paged_append_guarded", "paged_reserve_guarded", "paged_append_e4m3", "paged_read", "draft_tree",
-                 "attn_paged_tree", "attn_paged_e4m3", "draft_accept", "paged_keep"]
+                 "attn_paged_tree", "attn_paged_e4m3", "draft_accept", "draft_accept_words", "paged_keep"]
 
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED",
           3: "ATTN_ERR_CUDA", 4: "ATTN_ERR_TIMEOUT"}
@@ -118,6 +118,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.paged_read.argtypes = [P, P, P, P, LL, LL, P, LL, LL, I, P]
     L.draft_tree.argtypes = [P, P, P, P, I, I, I, P]
     L.draft_accept.argtypes = [P, P, P, P, P, P, P, P, I, I, P]
+    L.draft_accept_words.argtypes = [P, P, P, P, P, P, P, P, I, I, I, P]
     L.paged_keep.argtypes = [P, P, I, P, LL, P, P, P, P, P, P, P, I, I, I, I, I, P]
     for name in PAGED_EXPORTS:
         getattr(L, name).restype = Z if name.endswith("_bytes") else I

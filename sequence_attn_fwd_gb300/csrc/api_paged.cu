@@ -394,8 +394,13 @@ int draft_tree(const int *parents, const int *cu_seqlens, long long *masks, int 
 
 int draft_accept(const int *parents, const int *cu_seqlens, const int *tokens, const int *choices, const int *given,
                  int *path, int *n_keep, int *last, int B, int total, attn_stream_t stream) {
-  if (B < 0 || total < 0) return ATTN_ERR_INVALID_ARG;
-  if (B > seqattn::kPagedMaxSeqs || total > kMaxKeys) return ATTN_ERR_UNSUPPORTED;
+  return draft_accept_words(parents, cu_seqlens, tokens, choices, given, path, n_keep, last, B, total, 0, stream);
+}
+
+int draft_accept_words(const int *parents, const int *cu_seqlens, const int *tokens, const int *choices, const int *given,
+                       int *path, int *n_keep, int *last, int B, int total, int words, attn_stream_t stream) {
+  if (B < 0 || total < 0 || words < 0) return ATTN_ERR_INVALID_ARG;
+  if (B > seqattn::kPagedMaxSeqs || total > kMaxKeys || words > seqattn::kDraftWords) return ATTN_ERR_UNSUPPORTED;
   if (B == 0) return ATTN_OK;
   if (!cu_seqlens || !n_keep || !last || !aligned(cu_seqlens, 4) || !aligned(n_keep, 4) || !aligned(last, 4) ||
       !aligned(given, 4))
@@ -403,7 +408,7 @@ int draft_accept(const int *parents, const int *cu_seqlens, const int *tokens, c
   if (total > 0 && (!parents || !tokens || !choices || !path || !aligned(parents, 4) || !aligned(tokens, 4) ||
                     !aligned(choices, 4) || !aligned(path, 4)))
     return ATTN_ERR_INVALID_ARG;
-  return done(seqattn::launch_draft_accept(parents, cu_seqlens, tokens, choices, given, path, n_keep, last, B, total,
+  return done(seqattn::launch_draft_accept(parents, cu_seqlens, tokens, choices, given, path, n_keep, last, B, total, words,
                                            reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -82,13 +82,15 @@ __global__ void __launch_bounds__(kTreeThreads)
 // ---------------------------------------------------------------- the accepted path
 // One CTA a sequence; its first warp goes down the tree: the lowest child of the
 // current token that is what the model chose after it. Children are behind their
-// parents, so the search goes on from the token that was found.
+// parents, so the search goes on from the token that was found. A sequence of more
+// tokens than the masks of `words` words have bits (0: no masks) was attended as a
+// chain, so it is one here: each token's only child is the next.
 constexpr int kAcceptThreads = 128;
 constexpr int kStaged = 1024;  // tokens from the last given one on that are brought to shared memory
 
 __global__ void __launch_bounds__(kAcceptThreads)
     accept_kernel(const int *parents, const int *cu, const int *tokens, const int *choices, const int *given, int *path,
-                  int *n_keep, int *last, int total) {
+                  int *n_keep, int *last, int total, int words) {
   __shared__ int staged[3][kStaged];
   __shared__ int kept;
   launch_dependents();
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(kAcceptThreads)
     return;
   }
   const int sure = given ? min(max(given[b], 1), s.n) : 1;
+  const bool chain = words > 0 && s.n > 64 * words;
   const int from = sure - 1, rest = s.n - from;  // tokens from the last given one on
   const int *parent = parents + s.q0 + from, *token = tokens + s.q0 + from, *choice = choices + s.q0 + from;
   int *out = path + s.q0;
@@ -123,9 +126,10 @@ __global__ void __launch_bounds__(kAcceptThreads)
     for (bool found = true; found;) {
       const int want = choice[at];
       found = false;
-      for (int c0 = at + 1; c0 < rest && !found; c0 += 32) {
+      const int end = chain ? min(rest, at + 2) : rest;
+      for (int c0 = at + 1; c0 < end && !found; c0 += 32) {
         const int c = c0 + lane;
-        const unsigned hit = __ballot_sync(0xffffffffu, c < rest && parent[c] == at + from && token[c] == want);
+        const unsigned hit = __ballot_sync(0xffffffffu, c < end && (chain || parent[c] == at + from) && token[c] == want);
         if (hit != 0) {
           found = true;
           at = c0 + __ffs(hit) - 1;
@@ -280,9 +284,9 @@ cudaError_t launch_draft_tree(const int *parents, const int *cu, long long *mask
 }
 
 cudaError_t launch_draft_accept(const int *parents, const int *cu, const int *tokens, const int *choices, const int *given,
-                                int *path, int *n_keep, int *last, int B, int total, cudaStream_t stream) {
+                                int *path, int *n_keep, int *last, int B, int total, int words, cudaStream_t stream) {
   return launch_dependent(accept_kernel, dim3(B), dim3(kAcceptThreads), 0, stream, parents, cu, tokens, choices, given, path,
-                          n_keep, last, total);
+                          n_keep, last, total, words);
 }
 
 cudaError_t launch_keep(const KeepParams &p, cudaStream_t stream) {

@@ -269,7 +269,7 @@ size_t compact_workspace_ints(int n_pages);
 cudaError_t launch_draft_tree(const int *parents, const int *cu, long long *masks, int *depths, int B, int total, int words,
                               cudaStream_t stream);
 cudaError_t launch_draft_accept(const int *parents, const int *cu, const int *tokens, const int *choices, const int *given,
-                                int *path, int *n_keep, int *last, int B, int total, cudaStream_t stream);
+                                int *path, int *n_keep, int *last, int B, int total, int words, cudaStream_t stream);
 
 // A pool as slots: pages of [heads][page_size] slots of slot_bytes.
 struct SlotPool {

@@ -12,7 +12,7 @@ drafts and their trees, over the C ABI of include/seqattn_paged.h.
     cache = PagedCache(..., dtype=torch.float8_e4m3fn)        # half the bytes: codes and a scale per key and value
     tree, depths = draft_tree(parents, cu_seqlens)            # drafts that branch: masks for every layer
     o, lse = cache.step(0, q, k, v, cu_seqlens, positions, tree=tree)
-    path, n_keep, last = draft_accept(parents, cu_seqlens, tokens, choices)
+    path, n_keep, last = draft_accept(parents, cu_seqlens, tokens, choices, tree=tree)
     status = cache.keep(cu_seqlens, path, n_keep)             # the rejected drafts leave the cache
 
 New tokens are packed: [H, total, D] tensors (any strides with D contiguous and
@@ -442,24 +442,33 @@ def draft_tree(parents: torch.Tensor, cu_seqlens: torch.Tensor, words: int = 1):
 
 
 def draft_accept(parents: torch.Tensor, cu_seqlens: torch.Tensor, tokens: torch.Tensor, choices: torch.Tensor,
-                 given: torch.Tensor | None = None):
+                 given: torch.Tensor | None = None, tree: torch.Tensor | None = None):
     """The drafts that the model confirms: from each sequence's given tokens (the first
     given[b], int32 [B] on the device; one when not given: the token that the step
     before chose) down the tree to the lowest child whose token is the model's choice
     behind its parent. tokens, choices int32 [total]: the token of each row, and what
     the model chose behind it. Returns (path int32 [total]: the kept tokens' numbers in
     rows cu_seqlens[b] .., then -1; n_keep int32 [B]; last int32 [B]: the choice
-    behind the last kept token, -1 for a sequence without tokens)."""
+    behind the last kept token, -1 for a sequence without tokens). tree: the masks that the
+    attention had (draft_tree). A sequence of more tokens than they have bits is a chain
+    to it, and so here, whatever its parents; without tree, trees of any size are followed,
+    those too whose choices the attention made as of a chain."""
     used, total = [], parents.numel()
     _require(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1, "cu_seqlens must be [B + 1]")
     B = cu_seqlens.numel() - 1
     at = [_tokens(parents, total, "parents", used), _tokens(cu_seqlens, B + 1, "cu_seqlens", used),
           _tokens(tokens, total, "tokens", used), _tokens(choices, total, "choices", used),
           None if given is None else _tokens(given, B, "given", used)]
+    words = 0
+    if tree is not None:
+        if tree.dtype != _I64 or tree.dim() != 2 or tree.shape[0] != total:
+            raise ValueError(f"tree must be int64 [{total}, words]")
+        words = tree.shape[1]
+        _require(1 <= words <= DRAFT_MAX_WORDS, "a tree's masks have one to four words")
     dev = _one_device("draft_accept", *used)
     path = torch.empty(total, dtype=_I32, device=parents.device)
     n_keep, last = (torch.empty(B, dtype=_I32, device=parents.device) for _ in range(2))
-    _call(lib.draft_accept, "draft_accept", dev, *at, path.data_ptr(), n_keep.data_ptr(), last.data_ptr(), B, total)
+    _call(lib.draft_accept_words, "draft_accept", dev, *at, path.data_ptr(), n_keep.data_ptr(), last.data_ptr(), B, total, words)
     return path, n_keep, last
 
 
