@@ -231,7 +231,10 @@ typedef struct {
  * values are rounded once, from fp32, to code * scale with the least scale whose
  * largest number 448 scale reaches the row's largest size (2^-126 at the least, as
  * for a row of zeros). q is turned and written in bf16. A NaN becomes the NaN
- * code and does not count for the scale.
+ * code and does not count for the scale. An infinity becomes 448 2^120 with its sign, which
+ * no bf16 or fp32 number reaches: paged_read gives an infinity back, as it does for sizes of
+ * 248 2^120 (3.3e38) and more; of the rest of such a row only what the scale 2^120 leaves is kept
+ * (a bf16 cache keeps it all), and attention must not see the row (its scores are finite, but mean nothing).
  */
 int paged_append_e4m3(const rope_rows *q, const rope_rows *k, const rope_rows *v, const paged_cache *cache,
                       const paged_scales *scales, const int *positions, long long pos_axis, int n_axes,

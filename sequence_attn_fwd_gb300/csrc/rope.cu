@@ -151,7 +151,8 @@ __device__ __forceinline__ Slot slot_of(const PagedView &c, int *guard, long lon
 // elements each: the least e with max |y| <= 448 2^e (1.75 2^8 is the largest e4m3
 // number), so the lowest one that loses nothing at the top; -126 at the least.
 // A power of two costs no precision (e4m3 is a floating format) and makes every
-// product with it exact. NaN elements do not count, and stay NaN.
+// product with it exact. NaN elements do not count, and stay NaN. An infinity gives
+// 2^120, and its code, 448, is past what fp32 and bf16 hold: it is read as one again.
 template <int kSlices>
 __device__ __forceinline__ int scale_of(const float (&y)[16]) {
   float top = 0.f;

@@ -338,7 +338,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     those of rows that were refused room, which would lie over older keys; guard[3]
     then holds the lengths for the attention of the step, 0 for such a row. With
     k_scales / v_scales (as for attn_paged) the pools are float8_e4m3fn: k and v are
-    rounded to code * scale, the scale the least power of two that holds the row."""
+    rounded to code * scale, the scale the least power of two that holds the row (rows
+    with an infinity lose their other elements; it is read as an infinity again)."""
     view, dev, B, Hkv, D = _cache_view(k_pages, v_pages, page_table, kv_lens, cu_seqlens, k_scales, v_scales)
     if k.dim() != 3:
         raise ValueError("expected k [Hkv, total, D]")

@@ -153,3 +153,24 @@ def test_drafts_of_another_branch_take_no_bits(sa, q_len, G, bits):  # noqa: F81
     own[half:, half:] = torch.ones((q_len - half, q_len - half), dtype=torch.bool).tril()
     bits_of = [[sum(1 << i for i in range(q_len) if own[t, i])] for t in range(q_len)] * c.B
     c.check(sa, tree=torch.tensor(bits_of, dtype=torch.int64).cuda(), seen_new=own.cuda())
+
+
+def test_infinities_and_the_largest_numbers_are_read_as_infinities(sa):  # noqa: F811
+    """448 2^120 is past fp32 and bf16, and so is 256 2^120, the nearest code to bf16's largest numbers. Other rows and the
+    row's NaN do not notice."""
+    D, n = 128, 5
+    x = torch.randn((1, n, D), generator=torch.Generator().manual_seed(3)).to(BF)
+    x[0, 0, 3], x[0, 0, 4], x[0, 0, 5] = math.inf, -math.inf, math.nan
+    x[0, 1, 7], x[0, 1, 8], x[0, 1, 9] = torch.finfo(BF).max, 247 * 2.0 ** 120, -240 * 2.0 ** 120
+    x[0, 3, 0] = -math.inf
+    pools = [torch.zeros((1, 1, 16, D), dtype=U8, device="cuda").view(E4M3) for _ in range(2)]
+    scales = [torch.zeros((1, 1, 16), dtype=U8, device="cuda").view(E8M0) for _ in range(2)]
+    at = i32([[0]]), i32([n]), i32([0, n])
+    sa.paged_append(x.cuda(), x.cuda(), *pools, *at, k_scales=scales[0], v_scales=scales[1])
+    for out in sa.paged_read(*pools, *at, n, k_scales=scales[0], v_scales=scales[1]):
+        out = out[0].cpu()
+        assert out[0, 3] == math.inf and out[0, 4] == -math.inf and out[0, 5].isnan() and (out[0, 6:] == 0).all()
+        assert out[1, 7] == math.inf and out[1, 8] == 240 * 2.0 ** 120 and out[1, 9] == -240 * 2.0 ** 120
+        assert out[3, 0] == -math.inf and (out[3, 1:] == 0).all()
+        for i in (2, 4):
+            assert torch.equal(out[i].double(), drafts_ref.values(*drafts_ref.quantise(x[0, i].float())))
