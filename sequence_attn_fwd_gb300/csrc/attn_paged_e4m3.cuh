@@ -57,11 +57,12 @@ constexpr int kThreads8 = 512;
 constexpr int kMmaWarp = 8, kTmaWarp = 9, kMmaWarp1 = 10, kTurners = 12;
 constexpr int kSoftmaxRegs = 184, kIssuerRegs = 56, kTurnerRegs = 88;
 static_assert(2 * kSoftmaxRegs + kIssuerRegs + kTurnerRegs <= 4 * (65536 / kThreads8), "registers of the four warpgroups");
-// Cost of a narrow tile in wide ones (as kNarrowUnit of the bf16 form), by its rows:
-// 60 and 63 single tokens beside a piece of 512 took 110, 157 us at 0.35 (0.25: 119, 161;
-// 0.5: 135, 206), 20 drafts of 35 rows beside two pieces of 300 at 0.25, 0.35, 0.5, 0.65,
-// 0.85 199, 154, 126, 115, 122 us.
-__device__ __forceinline__ float narrow_unit8(int rows) { return rows <= 16 ? 0.32f : (rows <= 32 ? 0.4f : 0.65f); }
+// Cost of a narrow tile in wide ones (as kNarrowUnit of the bf16 form), by its rows. At
+// 0.29, 0.32, 0.34, 0.36, 0.40: 60 and 63 single tokens beside a piece of 512, and 20 pairs beside
+// two pieces of 700, in all 584, 569, 555, 562, 609 us; 30 fours of 28 rows beside a piece of 512 at
+// 0.36, 0.4, 0.45, 0.5: 105, 105, 97, 100; 20 drafts of 35 rows beside two pieces of 300, 40 of 32
+// beside one of 700, 32 trees of 6 to 60 drafts, in all, at 0.65, 0.76, 0.8, 0.85: 593, 545, 557, 588.
+__device__ __forceinline__ float narrow_unit8(int rows) { return rows <= 16 ? 0.34f : (rows <= 32 ? 0.45f : 0.77f); }
 
 template <int D>
 struct Cfg8 {
