@@ -287,10 +287,11 @@ int draft_tree(const int *parents, const int *cu_seqlens, long long *masks, int 
  * Over the 8-bit cache, weights of sequences of at most 64 rows (new tokens times
  * Hq / Hkv) are rounded to 2^-9 of themselves for the product with V, if they and their value's
  * scale multiply to 2^-23 of the row's largest such product or more; below that, to steps of
- * 2^-31 of it (2^-48 of the largest scale that a row sees counts as the least scale there).
+ * 2^-31 of it (2^-44 of the largest scale that a row sees counts as the least scale there).
  * Weights of longer sequences are rounded to 2^-11 of themselves or to 2^-18 of the weights of
- * their 128 keys together (keys 128 i on), what is more; values there, if their scale is below
- * 2^-13 of the largest of these keys, to 2^-23 of that; keys, below 2^-15, to 2^-25.
+ * their 128 keys together (keys 128 i on; or 2^-70 of all), what is more; values there, if their
+ * scale is below 2^-13 of the largest of these keys, to 2^-23 of that (or 2^-65 of the largest of
+ * all); keys, below 2^-15, to 2^-25.
  */
 int attn_paged_tree(const void *q, long long q_head_stride, long long q_row_stride, const paged_cache *cache, void *o,
                     long long o_head_stride, long long o_row_stride, float *lse, void *workspace,

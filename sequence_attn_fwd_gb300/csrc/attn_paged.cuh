@@ -996,7 +996,7 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, Items ite
           // when the tile's P would sum to more than 2^8
           // (kCodes: or to so little that its fp16 weights would lack bits)
           const bool big = row_valid && !(rowsum <= (kCodes ? codes::kMostSum : kRescaleSum));
-          const bool small = kCodes && row_valid && rowsum < codes::kLeastSum && rowsum > 0.f;
+          const bool small = kCodes && row_valid && rowsum < codes::kLeastSum && rowsum > 0.f && l < codes::kFallL;
           if (__any_sync(0xffffffffu, big || small) || (kCodes && (first || units.down != 1.f))) {
             float mx = -INFINITY;  // 32 columns at a time: few live registers
 #pragma unroll 1

@@ -56,12 +56,13 @@ __device__ __forceinline__ int value_unit(int e, int unit, int most, bool first)
 // tile's weights up to kMostSum, 2^15 of fp16, are let by. Sums below kLeastSum bring the
 // reference down, so that what the keys behind an attention sink bring, a little each, keeps
 // its bits: fp16 ends in steps of 2^-24, so a weight is held to 2^-11 of itself or to 2^-18 of its
-// tile's sum. References fall as far as l stays below 2^kMostL. A segment's first tile has
-// kFirstHeadroom: the keys beside a sink at the start of a context have no other tile to be held in.
-// (1,024 tokens behind 65,536 keys of sizes 2^-1.5 to 2^1.5, and a batch of prompt pieces with heads
+// tile's sum. References fall as far as l stays below 2^kMostL, and while it is below kFallL. A
+// segment's first tile has kFirstHeadroom: the keys beside a sink at the start of a context
+// have no other tile to be held in. (1,024 tokens behind 65,536 keys of sizes 2^-1.5 to 2^1.5, and a batch of prompt pieces with heads
 // of 64: with both 7, 7, 6, 5, 3: 968, 898, 880, 869, 855 us and 236, 203, 192, 184, 183, the first with
 // kLeastSum 2; 5 and 13: 868 and 201.)
-constexpr float kHeadroom = 5.f, kFirstHeadroom = 13.f, kMostSum = 32768.f, kLeastSum = 0.0078125f, kMostL = 57.f;
+constexpr float kHeadroom = 5.f, kFirstHeadroom = 13.f, kMostSum = 32768.f, kLeastSum = 0.0078125f, kMostL = 57.f,
+                kFallL = 0x1p50f;
 // O from units of 2^e: 1 / l times two factors, as 2^e may leave the range of one.
 __device__ __forceinline__ void units_back(int e, float &inv_l, float &back) {
   const int half = e / 2;

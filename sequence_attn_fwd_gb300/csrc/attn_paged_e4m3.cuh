@@ -493,9 +493,9 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
   auto sum_of = [](float a, float b) { return a + b; };
   const Reductions<C> mine(reds + 256 * gi);
   const float *back = Reductions<C>(reds + (kTurns ? 0 : 256 * gi)).back;
-  // In powers of two: how far w may pass 1 (fp16 ends at 2^5 of it); how far 2^(s - m) may, as much as a value's scale
-  // counts in the reference at most; and how far a reference may fall behind its highest, as it does when E
-  // rises. Together they hold l, of up to 2^30 keys, below 2^126.
+  // In powers of two: how far w may pass 1 (fp16 ends at 2^5 of it); how far 2^(s - m) may, and so, with as much
+  // room, a value's scale counts in the reference; and how far a reference may fall behind its highest, as it
+  // does when E rises. Together they hold l, of up to 2^30 keys, below 2^126.
   constexpr float kMost = 4.f, kFar = 48.f;
   constexpr int kFall = 48;
   paged::RingPos k{0, 0};       // of the segment's first K tile
@@ -602,7 +602,7 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
         if (lane == 0) mine.tops[w] = warp_e;
         named_bar_sync(id, 128);
         const int new_e = max(top_e, max(max(mine.tops[0], mine.tops[1]), max(mine.tops[2], mine.tops[3])));
-        const float less_e = fmaxf(static_cast<float>(e - new_e), -kFar);
+        const float less_e = fmaxf(static_cast<float>(e - new_e), kMost - kFar);
 #pragma unroll
         for (int h = 0; h < C; h += 16) {
           float y[16];

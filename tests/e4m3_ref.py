@@ -4,13 +4,13 @@ that grows with the keys).
 Narrow form (at most 64 rows a KV head). A weight with its value's scale, W = 2^(s + e), against a reference R with W <= 2^4 R,
 is rounded to fp16 (2^-11 of itself) and then held as three e5m2 numbers: upper byte, upper byte of the rest, the rest of that
 to nearest times 2^4. Each takes three bits, so 2^-9 is off at most; below, half of e5m2's smallest step, 2^-17 / 2^4, where R is
-2^11: 2^-32 R. R is no more than the row's largest W -- or, of values that differ by more than 2^48, 2^(E - 48) times its largest
+2^11: 2^-32 R. R is no more than the row's largest W -- or, of values that differ by more than 2^44, 2^(E - 44) times its largest
 2^s, E the largest exponent of the values that its sequence's rows see.
 Wide form. Weights 2^s are rounded to fp16 (2^-11), or by half of its smallest step, 2^-25, where a tile of 128 keys whose weights
 sum to less than 2^-7 gets a new reference, against which its largest weight is 2^5: 2^-18 of its sum. In the first tile the
 largest is 2^13: 2^-38 of it. Values are exact unless their exponent lies more than
 13 below the largest of their tile of 128; then half of a step of 2^-24, in units of at most four times the largest scale: 2^-23
-of that.
+of that (units fall 2^-40 behind the largest at most: 2^-65 of that one; references as far as l stays below 2^57: 2^-70 of all).
 Both. Scores as in drafts_ref.attention; keys of the wide form whose exponent lies more than 15 below the tile's largest are off
 by 2^-25 of the largest scale."""
 import math
@@ -28,7 +28,7 @@ def exponents(scales):
 
 def attention(q, k, v, ek, ev, codes, seen, scale, wide, at=None):
     """One sequence and KV head, on any device, in 64 bits: q [R, D], values k, v [n, D], exponents ek, ev [n], codes of v [n, D],
-    seen [R, n] -> O, its bound, lse, its bound. at [n]: the keys' places in the sequence (0 .. n - 1 if not given)."""
+    seen [R, n] -> O, its bound, lse, its bound, and of O's norm what the floor of the wide form's first tile can take. at [n]: the keys' places in the sequence (0 .. n - 1 if not given)."""
     q, k, v, ek, ev, codes = (x.double() for x in (q, k, v, ek, ev, codes))
     n, D = k.shape
     tile = (torch.arange(n, device=k.device) if at is None else at) // 128
@@ -48,6 +48,7 @@ def attention(q, k, v, ek, ev, codes, seen, scale, wide, at=None):
     o = w @ v
     rel = 2 * torch.where(seen, ds, 0.0).amax(-1) + 2.0 ** -17 + 2 * n * F32_HALF + 2.0 ** -20
     tol = (w @ v.abs()) * rel[:, None] * (1 + BF16_HALF)
+    taken = torch.zeros_like(z)
     if wide:
         tol = tol + (w @ v.abs()) * (2.0 ** -11 * (1 + BF16_HALF))
         sums = torch.zeros((q.shape[0], n_tiles), dtype=torch.float64, device=k.device).index_add_(1, tile, w)
@@ -56,13 +57,16 @@ def attention(q, k, v, ek, ev, codes, seen, scale, wide, at=None):
         sizes.index_add_(0, tile, v.abs())
         floor = 2.0 ** -18 * sums
         floor[:, 0] = 2.0 ** -38 * torch.where(tile == 0, w, 0.0).amax(-1)
+        beside = torch.where(tile == 0, torch.minimum(w, floor[:, :1]), 0.0)
+        taken = (beside @ v.abs()).norm(dim=-1) / o.norm(dim=-1).clamp(min=1e-300)
+        floor = floor + 2.0 ** -70
         tol = tol + floor @ sizes
-        small = torch.where(ev < most(ev) - 13, 2.0 ** (most(ev) - 23), 0.0)
+        small = torch.where(ev < most(ev) - 13, 2.0 ** (most(ev) - 23), 0.0) + (2.0 ** (ev.amax() - 65) if n else 0.0)
         tol = tol + (w @ small)[:, None]
     else:
         tol = tol + (w @ v.abs()) * ((2.0 ** -9 + 2.0 ** -11) * (1 + BF16_HALF))
         top_e = ev[seen.any(0)].amax() if bool(seen.any()) else 0.0
-        unit = torch.maximum((w * 2.0 ** ev).amax(-1), w.amax(-1) * 2.0 ** (top_e - 48))
+        unit = torch.maximum((w * 2.0 ** ev).amax(-1), w.amax(-1) * 2.0 ** (top_e - 44))
         tol = tol + 2.0 ** -32 * (1 + 2.0 ** -3) * unit[:, None] * (seen.double() @ codes.abs())
     tol = tol + BF16_HALF * o.abs() + 1e-30
-    return o, tol, z, rel + 8 * F32_HALF * z0.abs() + 2.0 ** -20
+    return o, tol, z, rel + 8 * F32_HALF * z0.abs() + 2.0 ** -20, taken

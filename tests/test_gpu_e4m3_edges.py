@@ -72,7 +72,9 @@ class OneContext:
     def check(self, sa, picked=(0, 17), tree=None, seen_new=None, least=2.0 ** -7):  # noqa: F811
         """Every element within its bound; and a row's error, as a whole, within `least` of the row: a weight's rounding error of
         at most 2^-9, of either sign, adds up over keys as the row itself does, to about 2^-10 of it, the row's own rounding
-        is as much again, and what a form loses of a score far above 1 less; 2^-7 is four times all of it."""
+        is as much again, and what a form loses of a score far above 1 less; 2^-7 is four times all of it. On top of it the wide
+        form is granted what its first tile's floor can take: each weight at most itself, and 2^-38 of the largest (with 30
+        nats, 2^43, between them, all that the sink's 127 neighbours bring)."""
         o, lse = sa.attn_paged(self.q, *self.pools, self.table, self.lens, self.cu, tree=tree, **self.kw)
         again = sa.attn_paged(self.q, *self.pools, self.table, self.lens, self.cu, tree=tree, **self.kw)
         assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
@@ -91,7 +93,7 @@ class OneContext:
                 assert ((got - r[0]).abs() <= r[1]).all(), float(((got - r[0]).abs() / r[1]).max())
                 assert ((got_lse - r[2]).abs() <= r[3]).all()
                 off = (got - r[0]).norm(dim=-1) / r[0].norm(dim=-1).clamp(min=1e-300)
-                assert (off <= least).all(), float(off.max())
+                assert (off <= least + r[4]).all(), float((off - r[4]).max())
 
 
 # rows of a KV head in each form: 1 and 16 (tiles in turn), 32, 64, and 160 (wide)
@@ -100,7 +102,7 @@ FORMS = [(1, 1), (4, 4), (2, 16), (8, 8), (40, 4)]
 
 @pytest.mark.parametrize("q_len,G", FORMS)
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("n,nats,size", [(8192, 12.0, 0.0), (16384, 14.0, 2.0 ** -10), (65536, 16.0, 0.0), (4096, 10.0, 0.01),
+@pytest.mark.parametrize("n,nats,size", [(8192, 12.0, 0.0), (8192, 30.0, 2.0 ** -60), (16384, 14.0, 2.0 ** -10), (65536, 16.0, 0.0), (4096, 10.0, 0.01),
                                          (16384, 20.0, 0.0)])
 def test_a_first_key_that_takes_most_of_the_weight(sa, q_len, G, D, n, nats, size):  # noqa: F811
     """A sink: its value is small or zero, and what the other keys' small weights bring is the answer."""
