@@ -331,7 +331,7 @@ int draft_accept_words(const int *parents, const int *cu_seqlens, const int *tok
  * path[cu_seqlens[b] + i], i < n_keep[b], stay (strictly ascending numbers within
  * them): they are moved together in every pool, in their order, behind the older keys,
  * kv_lens[b] shrinks by the others, and pages that hold no key any more are given
- * back. A kept token that has no page stays without one. The pools' pages hold
+ * back. A kept token whose place, old or new, is on no page has none. The pools' pages hold
  * [heads[i]][page_size] slots (heads: host array [n_pools], page_bytes a multiple of
  * heads * page_size). All device memory but pools and heads.
  * status: 0 done; a row that is not done is left unchanged:

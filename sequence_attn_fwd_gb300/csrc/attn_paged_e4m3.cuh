@@ -21,8 +21,8 @@
 //     to nearest, times 2^4), three bits each, in columns of their own, so that V is read
 //     once for all: 2^-9 of a weight, as bf16 gives, down to 2^-23 of the column's largest,
 //     and steps of 2^-31 of that below. (As two e4m3 numbers, steps of 2^-18: batch decoding
-//     177 us, now 183, trees of up to 64 rows 143, now 151; but a first key of 12 nats
-//     above 8,191 others left 0.1 of their answer lost.)
+//     177 us, now 183, trees of up to 64 rows 143, now 148 to 154; but of the answer behind a
+//     first key 12 nats above 8,191 others 3 to 5 % was lost, 14 above 16,383 half of it.)
 // Wide form (compute bound), in fp16, which holds codes and ratios of scales: warps of their
 // own turn K and V tiles, K to units of the tile's largest scale, V to a unit that fits many tiles
 // (value_unit), on their way into the ring of the bf16 form; Q goes there after its rows'
@@ -33,7 +33,7 @@
 //
 // Measured (GB300): 64 sequences' next tokens over 300 to 16,000 keys (1.06 GB, 8 KV
 // heads of 128) 183 us = 5.8 TB/s; 1,024 tokens behind 65,536 keys, 32 heads over 8 of
-// 128, 868 us = 1,276 TFLOP/s.
+// 128, 870 us = 1,273 TFLOP/s.
 #pragma once
 
 namespace seqattn {
