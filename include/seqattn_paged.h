@@ -289,9 +289,9 @@ int draft_tree(const int *parents, const int *cu_seqlens, long long *masks, int 
  * scale multiply to 2^-23 of the row's largest such product or more; below that, to steps of
  * 2^-31 of it (2^-44 of the largest scale that a row sees counts as the least scale there).
  * Weights of longer sequences are rounded to 2^-11 of themselves or to 2^-18 of the weights of
- * their 128 keys together (keys 128 i on; or 2^-70 of all), what is more; values there, if their
- * scale is below 2^-13 of the largest of these keys, to 2^-23 of that (or 2^-65 of the largest of
- * all); keys, below 2^-15, to 2^-25.
+ * their 128 keys together (keys 128 i on; or 2^-70 of all), what is more. Values there are exact
+ * down to scales of 2^-17 of the largest of these keys, held to 2^-27 of that down to 2^-26 (and to
+ * 2^-60 of the largest of all), and may count as zeros below; keys down to 2^-22, 2^-32, 2^-31.
  */
 int attn_paged_tree(const void *q, long long q_head_stride, long long q_row_stride, const paged_cache *cache, void *o,
                     long long o_head_stride, long long o_row_stride, float *lse, void *workspace,

@@ -44,12 +44,13 @@ __device__ __forceinline__ TileUnits tile_units(const volatile int *exps, int cv
   return {two_to(ek), down};
 }
 // The unit's exponent for a tile of V whose largest scale is 2^e, behind one of `unit`, the largest so far
-// `most`: the same for a few sizes. Codes end at 2^9 and fp16 at 2^16, so there are seven
-// bits above; and down to 2^-2 of it nothing that fp16 ends with is missed. (2^40 below the
-// largest at the least, as O holds it, too.)
-constexpr int kAbove = 7, kBelow = 2, kChosen = 4, kUnitFall = 40;
+// `most`: the same for a few sizes. Codes end at 2^9 and fp16 at 2^16, so scales may be up to 2^7
+// in it, and are 2^2 or more, for what fp16 has below: factors end at 2^-24. (K's unit is
+// 2^-7 of the tile's largest scale.) A unit 2^40 below the largest one at the least, as O
+// holds that, too.
+constexpr int kAbove = 7, kBelow = 2, kChosen = 5, kUnitFall = 40;
 __device__ __forceinline__ int value_unit(int e, int unit, int most, bool first) {
-  if (!first && e <= unit + kAbove && e >= unit - kBelow) return unit;
+  if (!first && e <= unit + kAbove && e >= unit + kBelow) return unit;
   return first ? e - kChosen : max(e - kChosen, most - kUnitFall);
 }
 // A row's weights are against a reference 2^kHeadroom below its largest score. Sums of a

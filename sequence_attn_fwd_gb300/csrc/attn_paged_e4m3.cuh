@@ -24,7 +24,7 @@
 //     177 us, now 183, trees of up to 64 rows 143, now 148 to 154; but of the answer behind a
 //     first key 12 nats above 8,191 others 3 to 5 % was lost, 14 above 16,383 half of it.)
 // Wide form (compute bound), in fp16, which holds codes and ratios of scales: warps of their
-// own turn K and V tiles, K to units of the tile's largest scale, V to a unit that fits many tiles
+// own turn K and V tiles, K to a unit of the tile's, V to one that fits many tiles
 // (value_unit), on their way into the ring of the bf16 form; Q goes there after its rows'
 // powers of two. The softmax has a factor more a tile and none an element, and references
 // that fall as well as rise, as fp16's weights need (kLeastSum). (Scales applied to scores and weights by the softmax
@@ -850,7 +850,7 @@ struct Turner {
       }
     }
   }
-  // The factors 2^(e_key - e) of the tile whose scales were loaded: for K e is the largest exponent (-126 without a key), for V
+  // The factors 2^(e_key - e) of the tile whose scales were loaded: for K e is 7 below the largest exponent, for V
   // value_unit makes it of that.
   __device__ __forceinline__ void take_scales(int valid, bool values, bool first) {
     int b[4], most = 0;
@@ -862,7 +862,7 @@ struct Turner {
     most = __reduce_max_sync(0xffffffffu, most);
     const int top = max(most, 1) - 127;
     if (!values) {
-      e = top;
+      e = max(top - paged::codes::kAbove, -126);  // (what masks leave is -inf times it: no zero)
     } else if (first || most > 0) {  // (a tile without a key leaves the unit)
       e = paged::codes::value_unit(top, e, largest, first);
       largest = first ? e : max(largest, e);

@@ -8,11 +8,13 @@ to nearest times 2^4. Each takes three bits, so 2^-9 is off at most; below, half
 2^s, E the largest exponent of the values that its sequence's rows see.
 Wide form. Weights 2^s are rounded to fp16 (2^-11), or by half of its smallest step, 2^-25, where a tile of 128 keys whose weights
 sum to less than 2^-7 gets a new reference, against which its largest weight is 2^5: 2^-18 of its sum. In the first tile the
-largest is 2^13: 2^-38 of it. Values are exact unless their exponent lies more than
-13 below the largest of their tile of 128; then half of a step of 2^-24, in units of at most four times the largest scale: 2^-23
-of that (units fall 2^-40 behind the largest at most: 2^-65 of that one; references as far as l stays below 2^57: 2^-70 of all).
-Both. Scores as in drafts_ref.attention; keys of the wide form whose exponent lies more than 15 below the tile's largest are off
-by 2^-25 of the largest scale."""
+largest is 2^13: 2^-38 of it. Values are codes times factors, in a unit U of at most 2^-2 of the tile's largest scale: exact
+while the factor is 2^-15 or more (a code's last bit is 2^-9), so down to 2^-17 of the largest scale; then off by half a step,
+2^-25 U, 2^-27 of the largest scale; and lost where the factor is below fp16's last step, 2^-24: below 2^-26 of that scale. (Units fall 2^-40 behind
+the largest at most, and that is 2^-2 of a scale: 2^-60 of the largest one of all; references as far as l stays below 2^57: 2^-70 of
+all.)
+Both. Scores as in drafts_ref.attention; keys of the wide form, in a unit of 2^-7 of the tile's largest scale, are exact down to
+2^-22 of that, then off by 2^-32 of it, and lost below 2^-31."""
 import math
 
 import torch
@@ -28,7 +30,7 @@ def exponents(scales):
 
 def attention(q, k, v, ek, ev, codes, seen, scale, wide, at=None):
     """One sequence and KV head, on any device, in 64 bits: q [R, D], values k, v [n, D], exponents ek, ev [n], codes of v [n, D],
-    seen [R, n] -> O, its bound, lse, its bound, and of O's norm what the floor of the wide form's first tile can take. at [n]: the keys' places in the sequence (0 .. n - 1 if not given)."""
+    seen [R, n] -> O, its bound, lse, its bound, and of O's norm what the floors of the wide form's first tile and of its values can take. at [n]: the keys' places in the sequence (0 .. n - 1 if not given)."""
     q, k, v, ek, ev, codes = (x.double() for x in (q, k, v, ek, ev, codes))
     n, D = k.shape
     tile = (torch.arange(n, device=k.device) if at is None else at) // 128
@@ -38,8 +40,9 @@ def attention(q, k, v, ek, ev, codes, seen, scale, wide, at=None):
     ds = 1.25 * (2 * D + 2) * F32_HALF * scale * (q.abs() @ k.abs().T)
     ds = ds + 2.0 ** -17 * scale * q.abs().amax(-1, keepdim=True) * k.abs().sum(-1)
     if wide:
-        far = torch.where(ek < most(ek) - 15, 2.0 ** (most(ek) - 25), 0.0)
+        far = torch.where(ek < most(ek) - 22, 2.0 ** (most(ek) - 32), 0.0)
         ds = ds + scale * q.abs().sum(-1, keepdim=True) * far
+        ds = ds + scale * (q.abs() @ torch.where((ek < most(ek) - 31)[:, None], k.abs(), 0.0).T)
     s = torch.where(seen, s, -math.inf)
     some = seen.any(-1)
     z = torch.where(some, torch.logsumexp(s, -1), -math.inf)
@@ -61,8 +64,10 @@ def attention(q, k, v, ek, ev, codes, seen, scale, wide, at=None):
         taken = (beside @ v.abs()).norm(dim=-1) / o.norm(dim=-1).clamp(min=1e-300)
         floor = floor + 2.0 ** -70
         tol = tol + floor @ sizes
-        small = torch.where(ev < most(ev) - 13, 2.0 ** (most(ev) - 23), 0.0) + (2.0 ** (ev.amax() - 65) if n else 0.0)
-        tol = tol + (w @ small)[:, None]
+        small = torch.where(ev < most(ev) - 17, 2.0 ** (most(ev) - 27), 0.0)[:, None] + (2.0 ** (ev.amax() - 60) if n else 0.0)
+        lost = torch.where((ev < most(ev) - 26)[:, None], v.abs(), small)
+        tol = tol + w @ lost
+        taken = taken + (w @ lost).norm(dim=-1) / o.norm(dim=-1).clamp(min=1e-300)
     else:
         tol = tol + (w @ v.abs()) * ((2.0 ** -9 + 2.0 ** -11) * (1 + BF16_HALF))
         top_e = ev[seen.any(0)].amax() if bool(seen.any()) else 0.0

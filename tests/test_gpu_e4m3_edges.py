@@ -74,7 +74,7 @@ class OneContext:
         at most 2^-9, of either sign, adds up over keys as the row itself does, to about 2^-10 of it, the row's own rounding
         is as much again, and what a form loses of a score far above 1 less; 2^-7 is four times all of it. On top of it the wide
         form is granted what its first tile's floor can take: each weight at most itself, and 2^-38 of the largest (with 30
-        nats, 2^43, between them, all that the sink's 127 neighbours bring)."""
+        nats, 2^43, between them, all that the sink's 127 neighbours bring); and what values beside far larger ones can lose."""
         o, lse = sa.attn_paged(self.q, *self.pools, self.table, self.lens, self.cu, tree=tree, **self.kw)
         again = sa.attn_paged(self.q, *self.pools, self.table, self.lens, self.cu, tree=tree, **self.kw)
         assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
@@ -125,6 +125,23 @@ def test_one_value_far_larger_than_the_others_and_of_no_weight(sa, q_len, G, bit
     if sink is not None:
         c.raise_key(0, sink)
         c.v[:, 0] = 0
+    c.fill()
+    c.check(sa)
+
+
+@pytest.mark.parametrize("q_len,G", FORMS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("of_keys", [False, True])
+def test_scales_that_lie_further_apart_than_fp16_in_one_tile(sa, q_len, G, D, of_keys):  # noqa: F811
+    """Keys of no weight whose value, or which themselves, are about 2^26 to 2^29 above all others of their tile: these keep
+    what fp16 can hold of them."""
+    c = OneContext(2048, 200, q_len, G, D, seed=3)
+    for n, i in enumerate((37, 300, 700, 1500, 1999)):
+        c.raise_key(i, -120.0)
+        if of_keys:
+            c.k[:, i] *= 2.0 ** 23  # elements of 120 / sqrt(D) against others of about 1
+        else:
+            c.v[:, i] *= 2.0 ** (26 + n % 4)
     c.fill()
     c.check(sa)
 
