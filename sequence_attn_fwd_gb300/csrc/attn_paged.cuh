@@ -1010,7 +1010,9 @@ __device__ __forceinline__ void wide_softmax(const PagedAttnParams &p, Items ite
             }
             const float headroom = !kCodes ? 0.f : (j == 0 ? codes::kFirstHeadroom : codes::kHeadroom);
             const float least = small ? m + log2f(l) - codes::kMostL : m;
-            const float m_new = fmaxf(least, scaled(mx) - headroom);
+            float low = scaled(mx) - headroom;
+            if (kCodes && scaled(mx) - low > codes::kMostHeadroom) low = scaled(mx);  // (scores past 2^26 lie 8 apart: 16, and fp16 ends)
+            const float m_new = fmaxf(least, low);
             const float alpha = (m_new == -INFINITY) ? 1.f : ex2_approx(m - m_new);
             m = m_new;
             l *= alpha;

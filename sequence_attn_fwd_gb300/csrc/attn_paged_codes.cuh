@@ -63,7 +63,7 @@ __device__ __forceinline__ int value_unit(int e, int unit, int most, bool first)
 // of 64: with both 7, 7, 6, 5, 3: 968, 898, 880, 869, 855 us and 236, 203, 192, 184, 183, the first with
 // kLeastSum 2; 5 and 13: 868 and 201.)
 constexpr float kHeadroom = 5.f, kFirstHeadroom = 13.f, kMostSum = 32768.f, kLeastSum = 0.0078125f, kMostL = 57.f,
-                kFallL = 0x1p50f;
+                kFallL = 0x1p50f, kMostHeadroom = 15.f;
 // O from units of 2^e: 1 / l times two factors, as 2^e may leave the range of one.
 __device__ __forceinline__ void units_back(int e, float &inv_l, float &back) {
   const int half = e / 2;

@@ -21,7 +21,7 @@
 //     to nearest, times 2^4), three bits each, in columns of their own, so that V is read
 //     once for all: 2^-9 of a weight, as bf16 gives, down to 2^-23 of the column's largest,
 //     and steps of 2^-31 of that below. (As two e4m3 numbers, steps of 2^-18: batch decoding
-//     177 us, now 183, trees of up to 64 rows 143, now 148 to 154; but of the answer behind a
+//     177 us, now 183 to 186, trees of up to 64 rows 143, now 148 to 157; but of the answer behind a
 //     first key 12 nats above 8,191 others 3 to 5 % was lost, 14 above 16,383 half of it.)
 // Wide form (compute bound), in fp16, which holds codes and ratios of scales: warps of their
 // own turn K and V tiles, K to a unit of the tile's, V to one that fits many tiles
@@ -32,8 +32,8 @@
 // 1,024 tokens behind 65,536 keys.)
 //
 // Measured (GB300): 64 sequences' next tokens over 300 to 16,000 keys (1.06 GB, 8 KV
-// heads of 128) 183 us = 5.8 TB/s; 1,024 tokens behind 65,536 keys, 32 heads over 8 of
-// 128, 870 us = 1,273 TFLOP/s.
+// heads of 128) 185 us = 5.7 TB/s; 1,024 tokens behind 65,536 keys, 32 heads over 8 of
+// 128, 874 us = 1,268 TFLOP/s.
 #pragma once
 
 namespace seqattn {
@@ -498,6 +498,9 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
   // does when E rises. Together they hold l, of up to 2^30 keys, below 2^126.
   constexpr float kMost = 4.f, kFar = 48.f;
   constexpr int kFall = 48;
+  // scores from here on lie 4 apart and more: their references are scores, without a scale, which would be rounded to
+  // as much (up to 2^kFar, and fp16 ends at 2^5)
+  constexpr float kLarge = 0x1p25f;
   paged::RingPos k{0, 0};       // of the segment's first K tile
   uint32_t first_step = 0;      // key tiles of the segments before
   uint32_t nq = 0;
@@ -608,7 +611,7 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
           float y[16];
           load_scores(h, false, y);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) y[c] += less_e;
+          for (int c = 0; c < 16; ++c) y[c] += fabsf(y[c]) < kLarge ? less_e : 0.f;
           const float most = paged::reduce16(y, larger);
           if (!(lane & 1)) mine.red[w * C + h + (lane >> 1)] = most;
         }
@@ -616,7 +619,8 @@ __device__ __forceinline__ void narrow_softmax8(const PagedAttnParams &p, const 
         if (key < C) {
           const float most = fmaxf(fmaxf(mine.red[key], mine.red[C + key]), fmaxf(mine.red[2 * C + key], mine.red[3 * C + key]));
           const float old_ref = mine.ref[key];
-          const float new_ref = fmaxf(fmaxf(most, highest - kFall), old_ref + static_cast<float>(max(top_e - new_e, -kFall)));
+          const float fall = fabsf(old_ref) < kLarge ? static_cast<float>(max(top_e - new_e, -kFall)) : 0.f;
+          const float new_ref = fmaxf(fmaxf(most, highest - kFall), old_ref + fall);
           highest = fmaxf(highest, new_ref);
           mine.ref[key] = new_ref;
           mine.factor[key] = ex2_approx(old_ref - new_ref);

@@ -147,6 +147,22 @@ def test_scales_that_lie_further_apart_than_fp16_in_one_tile(sa, q_len, G, D, of
 
 
 @pytest.mark.parametrize("q_len,G", FORMS)
+@pytest.mark.parametrize("bits", [16, 21, 23, 24, 25, 26, 27, 28, 30, 40])
+@pytest.mark.parametrize("spread", [0, 46, 60])
+def test_scores_whose_steps_are_larger_than_any_headroom(sa, q_len, G, bits, spread):  # noqa: F811
+    """Scores of 2^18 and far more, in every sequence other ones, so that references are rounded to steps of up to 2^20; values
+    of one size and of two that lie far apart. Everything within its bound, and so finite."""
+    c = OneContext(1024, 160, q_len, G, 128, seed=bits)
+    sizes = 2.0 ** (bits - 3 * torch.rand(c.q.shape[1], generator=torch.Generator().manual_seed(bits)))
+    c.q = (c.q * sizes.cuda()[None, :, None]).to(BF)
+    c.v[:, torch.arange(c.n) % 3 > 0] *= 2.0 ** -spread
+    c.fill()
+    c.check(sa, picked=range(0, 160, 9), least=math.inf)
+    o, lse = sa.attn_paged(c.q, *c.pools, c.table, c.lens, c.cu, **c.kw)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("q_len,G", FORMS)
 def test_weights_that_fall_and_rise_over_the_tiles(sa, q_len, G):  # noqa: F811
     """Tiles of large and of small weights in turn, the large ones with values of next to nothing; sizes of values that
     come and go."""
